@@ -25,7 +25,8 @@ OK = 0
 FMT_Q8_0, FMT_Q2_K, FMT_INT4_G64, FMT_MXFP4, FMT_FP8_B128 = 1, 2, 3, 4, 5
 FMT_BY_NAME = {"q8_0": FMT_Q8_0, "q2_k": FMT_Q2_K, "int4": FMT_INT4_G64, "mxfp4": FMT_MXFP4,
                "fp8_b128": FMT_FP8_B128}
-DEV_OK, DEV_BAD_EXPERT_ID, DEV_WAIT_TIMEOUT, DEV_SCALE_RANGE = 0, 1, 2, 3
+DEV_OK, DEV_BAD_EXPERT_ID, DEV_WAIT_TIMEOUT, DEV_SCALE_RANGE, DEV_BAD_ROW = 0, 1, 2, 3, 4
+DT_F32, DT_F16, DT_BF16 = 0, 1, 2
 STATUS_NAMES = {0: "BQ_OK", 1: "BQ_ERR_NULL", 2: "BQ_ERR_SHAPE", 3: "BQ_ERR_ALIGN", 4: "BQ_ERR_FORMAT",
                 5: "BQ_ERR_WORKSPACE", 6: "BQ_ERR_CUDA", 7: "BQ_ERR_DEVICE", 8: "BQ_ERR_ARCH"}
 
@@ -77,6 +78,22 @@ _SIGS = {
     "bq_test_set_wait_probe": (c_int32, [c_int32, c_uint64]),
     "bq_moe_gather_qmm": (c_int32, [POINTER(MoEDescC), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                     c_size_t, c_void_p]),
+    "bq_moe_dispatch": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_int64, c_void_p, c_int32, c_void_p, c_int64,
+                                  c_void_p]),
+    "bq_moe_dispatch_backward": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_int64, c_void_p, c_int32, c_void_p,
+                                           c_int64, c_void_p]),
+    "bq_moe_combine": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_int64, c_void_p, c_void_p, c_int32, c_int32,
+                                 c_void_p, c_int64, c_void_p]),
+    "bq_moe_combine_backward": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_int32, c_int32, c_int32, c_void_p,
+                                          c_void_p, c_int32, c_void_p, c_int64, c_void_p, c_void_p]),
+    "bq_quant_fp8_b128": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_int64, c_void_p, c_void_p, c_void_p,
+                                    c_void_p]),
+    "bq_moe_dispatch_fp8_b128": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_int64, c_void_p, c_int32, c_void_p,
+                                           c_void_p, c_void_p]),
+    "bq_mm_fp8_b128": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_void_p,
+                                 c_int32, c_int64, c_void_p]),
+    "bq_moe_mm_fp8_b128": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_int32,
+                                     c_int32, c_int32, c_void_p, c_int32, c_int64, c_void_p]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -85,9 +102,10 @@ for _name, (_res, _args) in _SIGS.items():
 
 
 class BQError(RuntimeError):
-    def __init__(self, status: int, where: str):
+    def __init__(self, status: int, where: str, msg: str | None = None):
         self.status = status
-        msg = _lib.bq_last_error().decode(errors="replace")
+        if msg is None:
+            msg = _lib.bq_last_error().decode(errors="replace")
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}: {msg}")
 
 
@@ -336,4 +354,212 @@ def moe_gather_qmm_hidden(layer: MoELayer, router: QWeight, hidden, gamma, eps: 
                                          eps, _ptr(logit_bias), _ptr(y), _ptr(workspace), workspace.numel(),
                                          _stream(stream)),
            "bq_moe_gather_qmm_hidden")
+    return y
+
+
+# ---------------------------------------------------------------- rows by expert, FP8 rows and products
+# These calls read shapes, strides and types from their tensors, so the tensors
+# are checked here: a call that does not fit raises BQError and launches nothing.
+_DT = None   # torch dtype -> bq_dtype, filled in on first use (torch is imported lazily)
+
+
+def _dtypes():
+    global _DT
+    if _DT is None:
+        import torch
+        _DT = {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}
+    return _DT
+
+
+def _refuse(status: int, where: str, msg: str):
+    raise BQError(status, where, msg)
+
+
+def _same_device(where: str, *tensors):
+    """Every tensor on the current CUDA device (the one the stream belongs to)."""
+    import torch
+    cur = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            _refuse(2, where, f"a tensor is on {t.device}, not on a CUDA device")
+        if cur is None:
+            cur = torch.cuda.current_device()
+        if t.device.index != cur:
+            _refuse(2, where, f"a tensor is on {t.device}, the current device is cuda:{cur}")
+
+
+def _rows_of(where: str, what: str, t, rows=None, cols=None, dtype=None):
+    """(pointer, bq_dtype, rows, cols, row stride) of a matrix whose rows are dense."""
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        want = f"[{'rows' if rows is None else rows}, {'columns' if cols is None else cols}]"
+        _refuse(2, where, f"{what} has shape {list(t.shape)}, expected {want}")
+    dt = _dtypes().get(t.dtype)
+    if dt is None or (dtype is not None and dt != dtype):
+        _refuse(4, where, f"{what} has type {t.dtype}")
+    r, c = t.shape
+    if c > 1 and t.stride(1) != 1:
+        _refuse(3, where, f"the rows of {what} are not contiguous (strides {tuple(t.stride())})")
+    if max(r, c) > 0x7fffffff:
+        _refuse(2, where, f"{what} has shape {list(t.shape)}")
+    return t.data_ptr(), dt, r, c, t.stride(0) if r > 1 else c
+
+
+def _dense(where: str, what: str, t, shape, kind: str):
+    """Pointer of a contiguous tensor of the given shape; kind: f32, i32 or fp8 (e4m3 bytes)."""
+    import torch
+    ok = {"f32": (torch.float32,), "i32": (torch.int32,), "fp8": (torch.float8_e4m3fn, torch.uint8)}[kind]
+    if t.dtype not in ok:
+        _refuse(4, where, f"{what} has type {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        _refuse(2, where, f"{what} has shape {list(t.shape)} and strides {tuple(t.stride())}, "
+                          f"expected contiguous {list(shape)}")
+    return t.data_ptr()
+
+
+def _pairs(where: str, inv, t: int):
+    """(pointer, k) of inv, int32 [T, k] or flat [T * k] as moe_permute writes it."""
+    import torch
+    if inv.dtype != torch.int32:
+        _refuse(4, where, f"inv has type {inv.dtype}")
+    n = inv.numel()
+    k = n // t
+    if k * t != n or not inv.is_contiguous() or inv.dim() > 2 or (inv.dim() == 2 and inv.shape[0] != t):
+        _refuse(2, where, f"inv has shape {list(inv.shape)} and strides {tuple(inv.stride())} for {t} tokens")
+    return inv.data_ptr(), k
+
+
+def moe_dispatch(x, inv, xs, stream=None):
+    """Rows into expert order: xs[inv[t][j]] = x[t].  x [T, H], xs [T*k, H] of one
+    type (fp32, fp16, bf16), rows 16-byte aligned; inv int32 [T, k] or [T*k] from
+    moe_permute (-1: a dropped pair)."""
+    where = "bq_moe_dispatch"
+    _same_device(where, x, inv, xs)
+    px, dt, t, h, ldx = _rows_of(where, "x", x)
+    if t == 0:
+        return xs
+    pi, k = _pairs(where, inv, t)
+    po, _, _, _, ldo = _rows_of(where, "xs", xs, t * k, h, dt)
+    _check(_lib.bq_moe_dispatch(px, dt, t, h, ldx, pi, k, po, ldo, _stream(stream)), where)
+    return xs
+
+
+def moe_dispatch_backward(dxs, inv, dx, stream=None):
+    """Gradient of moe_dispatch: dx[t] = sum_j dxs[inv[t][j]] (fp32 sum, slot order)."""
+    where = "bq_moe_dispatch_backward"
+    _same_device(where, dxs, inv, dx)
+    po, dt, t, h, ldo = _rows_of(where, "dx", dx)
+    if t == 0:
+        return dx
+    pi, k = _pairs(where, inv, t)
+    px, _, _, _, ldx = _rows_of(where, "dxs", dxs, t * k, h, dt)
+    _check(_lib.bq_moe_dispatch_backward(px, dt, t, h, ldx, pi, k, po, ldo, _stream(stream)), where)
+    return dx
+
+
+def moe_combine(ys, inv, weights, y, accumulate: bool = False, stream=None):
+    """Rows back in token order: y[t] = sum_j weights[t][j] * ys[inv[t][j]], with
+    accumulate y[t] += that.  ys [T*k, H], y [T, H] of one type; weights fp32 [T, k]."""
+    where = "bq_moe_combine"
+    _same_device(where, ys, inv, weights, y)
+    po, dt, t, h, ldo = _rows_of(where, "y", y)
+    if t == 0:
+        return y
+    pi, k = _pairs(where, inv, t)
+    px, _, _, _, ldx = _rows_of(where, "ys", ys, t * k, h, dt)
+    pw = _dense(where, "weights", weights, (t, k), "f32")
+    _check(_lib.bq_moe_combine(px, dt, t, h, ldx, pi, pw, k, int(bool(accumulate)), po, ldo, _stream(stream)), where)
+    return y
+
+
+def moe_combine_backward(dy, ys, inv, weights, dys, dweights, stream=None):
+    """Gradients of moe_combine: dys[inv[t][j]] = weights[t][j] * dy[t] and
+    dweights[t][j] = <dy[t], ys[inv[t][j]]>.  dys or dweights may be None (not
+    computed; then weights, or ys, may be None too)."""
+    where = "bq_moe_combine_backward"
+    _same_device(where, dy, ys, inv, weights, dys, dweights)
+    pg, dt, t, h, ldg = _rows_of(where, "dy", dy)
+    if t == 0:
+        return dys, dweights
+    pi, k = _pairs(where, inv, t)
+    px, ldx = None, 0
+    if ys is not None:
+        px, _, _, _, ldx = _rows_of(where, "ys", ys, t * k, h, dt)
+    po, ldo = None, 0
+    if dys is not None:
+        po, _, _, _, ldo = _rows_of(where, "dys", dys, t * k, h, dt)
+    pw = None if weights is None else _dense(where, "weights", weights, (t, k), "f32")
+    pd = None if dweights is None else _dense(where, "dweights", dweights, (t, k), "f32")
+    _check(_lib.bq_moe_combine_backward(pg, ldg, px, ldx, dt, t, h, pi, pw, k, po, ldo, pd, _stream(stream)), where)
+    return dys, dweights
+
+
+def quant_fp8_b128(x, q, scales, n_rows=None, stream=None):
+    """Rows to FP8 e4m3, one fp32 scale per 128 values.  x [rows, k] fp32, fp16 or
+    bf16 (k a multiple of 16); q [rows, k] float8_e4m3fn or uint8; scales fp32
+    [rows, ceil(k/128)].  n_rows: optional int32 device tensor of one element, the
+    number of rows to quantise (the others are left as they are)."""
+    where = "bq_quant_fp8_b128"
+    _same_device(where, x, q, scales, n_rows)
+    px, dt, r, k, ldx = _rows_of(where, "x", x)
+    pq = _dense(where, "q", q, (r, k), "fp8")
+    ps = _dense(where, "scales", scales, (r, -(-k // 128)), "f32")
+    pn = None if n_rows is None else _dense(where, "n_rows", n_rows.view(-1), (1,), "i32")
+    _check(_lib.bq_quant_fp8_b128(px, dt, r, k, ldx, pn, pq, ps, _stream(stream)), where)
+    return q, scales
+
+
+def moe_dispatch_fp8_b128(x, inv, q, scales, stream=None):
+    """moe_dispatch and quant_fp8_b128 in one pass: q [T*k, H] and scales
+    [T*k, ceil(H/128)] in expert order."""
+    where = "bq_moe_dispatch_fp8_b128"
+    _same_device(where, x, inv, q, scales)
+    px, dt, t, h, ldx = _rows_of(where, "x", x)
+    if t == 0:
+        return q, scales
+    pi, k = _pairs(where, inv, t)
+    pq = _dense(where, "q", q, (t * k, h), "fp8")
+    ps = _dense(where, "scales", scales, (t * k, -(-h // 128)), "f32")
+    _check(_lib.bq_moe_dispatch_fp8_b128(px, dt, t, h, ldx, pi, k, pq, ps, _stream(stream)), where)
+    return q, scales
+
+
+def _product(where, x, x_scales, w, w_scales, y, swiglu, grouped):
+    if x.dim() != 2 or w.dim() != (3 if grouped else 2):
+        _refuse(2, where, f"x has shape {list(x.shape)}, w {list(w.shape)}")
+    m, k = x.shape
+    n = w.shape[-2]
+    lead = tuple(w.shape[:1]) if grouped else ()
+    px = _dense(where, "x", x, (m, k), "fp8")
+    pxs = _dense(where, "x_scales", x_scales, (m, -(-k // 128)), "f32")
+    pw = _dense(where, "w", w, lead + (n, k), "fp8")
+    pws = _dense(where, "w_scales", w_scales, lead + (-(-n // 128), -(-k // 128)), "f32")
+    py, dt, _, _, ldy = _rows_of(where, "y", y, m, n // 2 if swiglu else n)
+    if max(m, n, k, *lead) > 0x7fffffff:
+        _refuse(2, where, f"x has shape {list(x.shape)}, w {list(w.shape)}")
+    return px, pxs, m, pw, pws, n, k, int(bool(swiglu)), py, dt, ldy
+
+
+def mm_fp8_b128(x, x_scales, w, w_scales, y, swiglu: bool = False, stream=None):
+    """y = x w^T of FP8 rows x [m, k] (quant_fp8_b128) and an FP8 weight w [n, k] with
+    one scale per 128 x 128 block; y [m, n] fp32, fp16 or bf16.  swiglu: w holds n/2
+    gate rows and n/2 up rows, y [m, n/2] = silu(gate) * up."""
+    where = "bq_mm_fp8_b128"
+    _same_device(where, x, x_scales, w, w_scales, y)
+    px, pxs, m, pw, pws, n, k, sw, py, dt, ldy = _product(where, x, x_scales, w, w_scales, y, swiglu, False)
+    _check(_lib.bq_mm_fp8_b128(px, pxs, m, pw, pws, n, k, sw, py, dt, ldy, _stream(stream)), where)
+    return y
+
+
+def moe_mm_fp8_b128(x, x_scales, offsets, w, w_scales, y, swiglu: bool = False, stream=None):
+    """mm_fp8_b128 over rows sorted by expert: rows offsets[e] .. offsets[e + 1] of x
+    take w[e].  w [E, n, k], w_scales [E, ceil(n/128), ceil(k/128)], offsets int32
+    [E + 1] from moe_permute.  Rows of y behind offsets[E] are left as they are."""
+    where = "bq_moe_mm_fp8_b128"
+    _same_device(where, x, x_scales, offsets, w, w_scales, y)
+    px, pxs, m, pw, pws, n, k, sw, py, dt, ldy = _product(where, x, x_scales, w, w_scales, y, swiglu, True)
+    e = w.shape[0]
+    po = _dense(where, "offsets", offsets, (e + 1,), "i32")
+    _check(_lib.bq_moe_mm_fp8_b128(px, pxs, m, po, e, pw, pws, n, k, sw, py, dt, ldy, _stream(stream)), where)
     return y

@@ -61,9 +61,18 @@ enum {
     BQ_DEV_OK = 0,
     BQ_DEV_BAD_EXPERT_ID = 1,   /* a routed expert id was outside [0, E)        */
     BQ_DEV_WAIT_TIMEOUT = 2,    /* a bounded mbarrier / flag wait ran out       */
-    BQ_DEV_SCALE_RANGE = 3      /* a block scale the device path cannot represent
+    BQ_DEV_SCALE_RANGE = 3,     /* a block scale the device path cannot represent
                                    met bq_repack_mxfp4 / bq_repack_fp8_b128       */
+    BQ_DEV_BAD_ROW = 4          /* a sorted row number outside [-1, T*k) or an
+                                   offset list that is not ascending in [0, rows] */
 };
+
+/* Element types of plain (unquantised) rows. */
+typedef enum {
+    BQ_DT_F32 = 0,
+    BQ_DT_F16 = 1,
+    BQ_DT_BF16 = 2
+} bq_dtype;
 
 typedef enum {
     BQ_FMT_Q8_0 = 1,      /* GGUF Q8_0: 32-value blocks, fp16 d + 32 int8 ([iron] kernel 1) */
@@ -402,6 +411,118 @@ bq_status bq_moe_gather_qmm_hidden(const bq_moe_desc* desc, const bq_qweight* ro
                                    const uint16_t* hidden, const uint16_t* gamma, float eps,
                                    const float* logit_bias, float* y, void* workspace,
                                    size_t workspace_bytes, bq_stream_t stream);
+
+/* ------------------------------------------------------------------ rows by expert
+ * Moving activation rows into expert order and back, with their gradients.
+ * inv (device int32 [T][k], from bq_moe_permute) names the sorted row of
+ * each pair (t, j): a number in [0, T*k), each at most once, or -1 for a
+ * pair that was dropped.  Sorted matrices have T*k rows; rows that no pair
+ * names are not touched.  An entry outside [-1, T*k) sets BQ_DEV_BAD_ROW
+ * and counts as dropped.  All sums are fp32, in slot order j = 0..k-1, so
+ * results do not change from run to run; the result is rounded once to
+ * `dtype` (bq_dtype, the type of every row matrix of the call).
+ *   bq_moe_dispatch           xs[inv[t][j]] = x[t]
+ *   bq_moe_dispatch_backward  dx[t] = sum_j dxs[inv[t][j]]
+ *   bq_moe_combine            y[t] = sum_j weights[t][j] * ys[inv[t][j]]
+ *                             (accumulate = 1: y[t] += the sum, added last)
+ *   bq_moe_combine_backward   dys[inv[t][j]] = weights[t][j] * dy[t]
+ *                             dweights[t][j] = sum_h dy[t][h] * ys[inv[t][j]][h]
+ *                             (0 for a dropped pair).  Either output may be
+ *                             NULL and is then not computed; ys is read only
+ *                             for dweights (else it may be NULL), weights
+ *                             only for dys (else it may be NULL).
+ * A dropped pair contributes nothing to a sum: its weight is not read as a
+ * factor, so a NaN there does no harm.  A zero weight multiplies like any
+ * other (0 * inf is NaN).
+ * Row matrices: device, H elements per row, rows ld* elements apart
+ * (ld* >= H), H and ld* such that rows start on 16-byte boundaries;
+ * weights, dweights: device fp32 [T][k], 4-byte aligned, as inv.  k in
+ * 1..8.  Outputs must not overlap inputs (bq_moe_combine's y with
+ * accumulate is the one matrix that is read and written).
+ * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_FORMAT (unknown dtype),
+ * BQ_ERR_ALIGN, BQ_ERR_CUDA.  T == 0 is a no-op.
+ */
+bq_status bq_moe_dispatch(const void* x, int32_t dtype, int32_t T, int32_t H, int64_t ldx,
+                          const int32_t* inv, int32_t k, void* xs, int64_t ldxs,
+                          bq_stream_t stream);
+bq_status bq_moe_dispatch_backward(const void* dxs, int32_t dtype, int32_t T, int32_t H,
+                                   int64_t ldxs, const int32_t* inv, int32_t k, void* dx,
+                                   int64_t ldx, bq_stream_t stream);
+bq_status bq_moe_combine(const void* ys, int32_t dtype, int32_t T, int32_t H, int64_t ldys,
+                         const int32_t* inv, const float* weights, int32_t k,
+                         int32_t accumulate, void* y, int64_t ldy, bq_stream_t stream);
+bq_status bq_moe_combine_backward(const void* dy, int64_t lddy, const void* ys, int64_t ldys,
+                                  int32_t dtype, int32_t T, int32_t H, const int32_t* inv,
+                                  const float* weights, int32_t k, void* dys, int64_t lddys,
+                                  float* dweights, bq_stream_t stream);
+
+/* ------------------------------------------------------------------ FP8 rows
+ * Quantises rows to FP8 e4m3 with one fp32 scale per 128 values of a row
+ * (the activation side of the 128 x 128 block-scaled FP8 weights).  For the
+ * values v of a group (the last group of a row may be shorter):
+ *   amax  = max |v|
+ *   scale = max(amax / 448, 2^-126)              (fp32, rounded once)
+ *   code  = e4m3(448 * v / max(amax, 448 * 2^-126)), half to even
+ * The quotient is rounded to e4m3 as if it were exact, so codes are the
+ * same on every machine.  A group holding a NaN gets NaN codes and a NaN
+ * scale; one holding an infinity gets the scale +inf, NaN codes where the
+ * value is infinite and 0 elsewhere.  Neither is hidden: a product over
+ * such a row gives NaN.
+ * x: device rows of k elements of `dtype`, ldx elements apart; k a multiple
+ * of 16, rows on 16-byte boundaries.  q: device uint8 [rows][k].  scales:
+ * device fp32 [rows][ceil(k/128)].
+ * n_rows: NULL, or a device int32: only the first min(*n_rows, rows) rows
+ * are read and written (for sorted rows: &offsets[E]).
+ *
+ * bq_moe_dispatch_fp8_b128 quantises row t of x and writes its codes and
+ * scales to the rows inv[t][j] of q [T*k][H] and scales [T*k][ceil(H/128)]:
+ * bq_moe_dispatch and bq_quant_fp8_b128 in one pass over x, with the same
+ * results and the same conditions on inv.
+ * Errors: as above.  No rows: a no-op.
+ */
+bq_status bq_quant_fp8_b128(const void* x, int32_t dtype, int32_t rows, int32_t k, int64_t ldx,
+                            const int32_t* n_rows, uint8_t* q, float* scales,
+                            bq_stream_t stream);
+bq_status bq_moe_dispatch_fp8_b128(const void* x, int32_t dtype, int32_t T, int32_t H,
+                                   int64_t ldx, const int32_t* inv, int32_t k, uint8_t* q,
+                                   float* scales, bq_stream_t stream);
+
+/* ------------------------------------------------------------------ FP8 x FP8 products
+ * Products of FP8 rows (as bq_quant_fp8_b128 writes them) with FP8 weights
+ * of one scale per 128 x 128 block (as bq_dequant_fp8_b128 reads them; no
+ * repack):
+ *   y[r][c] = sum_b xscales[r][b] * wscales[c/128][b]
+ *                   * sum_{i in block b of 128} e4m3(x[r][i]) * e4m3(w[c][i])
+ * Products and sums in fp32, the scales applied in fp32 to each block's sum;
+ * the result is rounded once to `ydtype` (bq_dtype).  NaN codes, NaN and
+ * infinite scales propagate.
+ * swiglu = 1: w holds n/2 gate rows, then n/2 up rows (n a multiple of 256);
+ * y has n/2 columns, silu(gate) * up with silu(g) = g / (1 + exp(-g)).
+ *
+ * bq_mm_fp8_b128: one weight w [n][k], x [m][k].
+ * bq_moe_mm_fp8_b128: rows sorted by expert: rows [offsets[e],
+ * offsets[e + 1]) of x take matrix e of w [E][n][k] (offsets: device int32
+ * [E + 1], as bq_moe_permute writes it).  Rows outside [offsets[0],
+ * offsets[E]) are not written.  Offsets that descend or leave [0, rows] set
+ * BQ_DEV_BAD_ROW; the experts concerned are skipped.
+ *
+ * x: device uint8 [rows][k]; xscales: device fp32 [rows][ceil(k/128)];
+ * w: device uint8 [E][n][k]; wscales: device fp32 [E][ceil(n/128)]
+ * [ceil(k/128)]; y: device rows of n (swiglu: n/2) elements of `ydtype`,
+ * ldy elements apart.  k a multiple of 16 (a short last block is fine),
+ * n >= 1 of any value (without swiglu), E * n <= 2^31 - 1, E <= 1024.  x, w
+ * 16-byte aligned; scales and offsets 4-byte aligned; y aligned to its
+ * element.
+ * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_FORMAT, BQ_ERR_ALIGN,
+ * BQ_ERR_CUDA.  No rows: a no-op.
+ */
+bq_status bq_mm_fp8_b128(const uint8_t* x, const float* xscales, int32_t m, const uint8_t* w,
+                         const float* wscales, int32_t n, int32_t k, int32_t swiglu, void* y,
+                         int32_t ydtype, int64_t ldy, bq_stream_t stream);
+bq_status bq_moe_mm_fp8_b128(const uint8_t* x, const float* xscales, int32_t rows,
+                             const int32_t* offsets, int32_t E, const uint8_t* w,
+                             const float* wscales, int32_t n, int32_t k, int32_t swiglu, void* y,
+                             int32_t ydtype, int64_t ldy, bq_stream_t stream);
 
 /* ------------------------------------------------------------------ observability
  * Stage timing: while set, every bq_moe_gather_qmm call on this host thread

@@ -56,7 +56,8 @@ import numpy as np
 
 __all__ = [
     "dequant_q8_0", "dequant_q2_k", "dequant_int4", "dequant_mxfp4", "MXFP4_VALUES",
-    "e4m3_value", "dequant_fp8_block", "FP8_BLOCK", "rmsnorm", "qmm", "route",
+    "e4m3_value", "dequant_fp8_block", "FP8_BLOCK", "e4m3_round",
+    "quant_fp8_rows", "mm_fp8_block", "dispatch_rows", "combine_rows", "combine_rows_backward", "rmsnorm", "qmm", "route",
     "SCORINGS", "softplus", "route_scored",
     "permute", "silu", "swiglu_ffn", "moe_ffn", "moe_ffn_tokens",
 ]
@@ -206,6 +207,85 @@ def dequant_fp8_block(weight: np.ndarray, scales: np.ndarray) -> np.ndarray:
     assert sc.shape[-2:] == (nb, kb), (sc.shape, (nb, kb))
     full = np.repeat(np.repeat(sc, FP8_BLOCK, axis=-2), FP8_BLOCK, axis=-1)[..., :n, :k]
     return e4m3_value(w) * full
+
+
+def e4m3_round(values: np.ndarray) -> np.ndarray:
+    """fp64 values rounded to the nearest e4m3 value (fp64), ties to the value of
+    even code, magnitudes above 448 to 448; NaN stays NaN."""
+    table = e4m3_value(np.arange(127, dtype=np.uint8))
+    v = np.asarray(values, dtype=np.float64)
+    a = np.minimum(np.abs(v), 448.0)
+    above = np.clip(np.searchsorted(table, a, side="left"), 1, 126)      # table[above - 1] < a <= table[above]
+    low, high = table[above - 1], table[above]
+    up = (high - a < a - low) | ((high - a == a - low) & (above % 2 == 0))
+    out = np.where(a == 0, 0.0, np.where(up, high, low))
+    return np.where(np.isnan(v), np.nan, np.copysign(out, v))
+
+
+def quant_fp8_rows(x: np.ndarray):
+    """Rows quantised to e4m3 with one fp32 scale per 128 values:
+    ``amax = max|v|``, ``scale = fp32(max(amax / 448, 2^-126))``,
+    ``code = e4m3(448 * v / max(amax, 448 * 2^-126))`` (the activation side of the
+    128 x 128 block-scaled FP8 weights).
+
+    x: [rows, k] (any float dtype, widened exactly).  Returns the codes' values
+    (fp64 [rows, k]) and the scales (fp32 [rows, ceil(k / 128)]).  448 * v is
+    exact in fp64, and so is every tie of the quotient.
+    """
+    v = np.asarray(x, dtype=np.float64)
+    rows, k = v.shape
+    values = np.empty((rows, k))
+    scales = np.empty((rows, -(-k // FP8_BLOCK)), dtype=np.float32)
+    tiny = 2.0 ** -126
+    for b in range(scales.shape[1]):
+        g = v[:, b * FP8_BLOCK:(b + 1) * FP8_BLOCK]
+        amax = np.abs(g).max(axis=1)                                       # NaN if any is
+        with np.errstate(invalid="ignore", over="ignore"):
+            scales[:, b] = np.maximum(amax / 448.0, tiny).astype(np.float32)
+            values[:, b * FP8_BLOCK:(b + 1) * FP8_BLOCK] = e4m3_round(
+                448.0 * g / np.maximum(amax, 448.0 * tiny)[:, None])
+    return values, scales
+
+
+def mm_fp8_block(x: np.ndarray, x_scales: np.ndarray, w: np.ndarray, w_scales: np.ndarray) -> np.ndarray:
+    """``y[r, c] = sum_b xs[r, b] ws[c // 128, b] sum_{i in block b} x[r, i] w[c, i]`` in
+    fp64.  x: fp64 e4m3 values [m, k]; w: uint8 e4m3 codes [n, k]."""
+    k = x.shape[1]
+    xs = np.repeat(np.asarray(x_scales, dtype=np.float64), FP8_BLOCK, axis=1)[:, :k]
+    return (np.asarray(x, dtype=np.float64) * xs) @ dequant_fp8_block(w, w_scales).T
+
+
+# --------------------------------------------------------------------------
+# Rows into expert order and back
+# --------------------------------------------------------------------------
+
+def dispatch_rows(x: np.ndarray, inv: np.ndarray, into: np.ndarray) -> np.ndarray:
+    """``into[inv[t, j]] = x[t]`` (inv [T, k]; -1: dropped); the other rows stay."""
+    out = np.array(into)
+    for t, j in np.argwhere(inv >= 0):
+        out[inv[t, j]] = x[t]
+    return out
+
+
+def combine_rows(ys: np.ndarray, inv: np.ndarray, weights) -> np.ndarray:
+    """``y[t] = sum_j weights[t, j] * ys[inv[t, j]]`` in fp64 over the pairs that
+    were not dropped (weights None: 1, the gradient of ``dispatch_rows``)."""
+    y = np.zeros((inv.shape[0], ys.shape[1]))
+    for t, j in np.argwhere(inv >= 0):
+        y[t] += (1.0 if weights is None else float(weights[t, j])) * ys[inv[t, j]].astype(np.float64)
+    return y
+
+
+def combine_rows_backward(dy: np.ndarray, ys: np.ndarray, inv: np.ndarray, weights: np.ndarray, into: np.ndarray):
+    """Gradients of ``combine_rows`` in fp64: ``dys[inv[t, j]] = weights[t, j] * dy[t]``
+    (the other rows as in ``into``) and ``dweights[t, j] = <dy[t], ys[inv[t, j]]>``
+    (0 for a dropped pair)."""
+    dys, dw = np.array(into, dtype=np.float64), np.zeros(inv.shape)
+    for t, j in np.argwhere(inv >= 0):
+        r = inv[t, j]
+        dys[r] = float(weights[t, j]) * dy[t].astype(np.float64)
+        dw[t, j] = np.dot(dy[t].astype(np.float64), ys[r].astype(np.float64))
+    return dys, dw
 
 
 # --------------------------------------------------------------------------
