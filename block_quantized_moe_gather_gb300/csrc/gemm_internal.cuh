@@ -6,6 +6,14 @@
 
 namespace bq {
 
+// Bound of every barrier wait of a tensor-core launch made now, and the test
+// hook's "no weight copies" switch (bq_test_set_wait_probe).
+struct WaitProbe {
+    unsigned long long limit_ns;
+    int skip_weight_copies;
+};
+WaitProbe wait_probe();
+
 // True when the tcgen05 GEMM handles weights of this format.
 bool gemm_supported(int fmt);
 // Extra MoE workspace the GEMM path needs beyond the common carve-up.

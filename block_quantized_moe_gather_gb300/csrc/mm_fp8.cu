@@ -3,111 +3,509 @@
 //
 //   y[r][c] = sum_b xs[r][b] ws[c/128][b] * sum_{i in block b} x[r][i] w[c][i]
 //
-// Simple form: a CTA of 256 threads computes a 64 x 64 tile of y from values
-// decoded to fp32 in shared memory; a block's sum is scaled before it joins
-// the total.
+// The sum over one block of 128 is a tcgen05 product of e4m3 operands into
+// fp32 TMEM columns (K = 128 = four MMAs of 32).  The scales differ from block
+// to block and are not powers of two, so they cannot be part of the MMA: every
+// block gets TMEM columns of its own from a ring, and the epilogue warps read
+// it and add it, scaled, to fp32 sums in registers while the tensor cores work
+// on the next blocks.
 #include <algorithm>
+#include <atomic>
 
+#include "gemm_internal.cuh"
 #include "row_types.cuh"
+#include "tc_ptx.cuh"
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 64;
-constexpr int kBlock = 128;
-constexpr int kStep = 32;
+using namespace bq::tc;
+
+constexpr int kBlock = 128;        // K per scale, per TMA box (one 128-byte swizzle row) and per TMEM stage
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxCluster = 8;
 
 struct Args {
-    const uint8_t* x;
     const float* xs;
     int rows;
     const int32_t* offsets;   // [E + 1], or NULL: all rows take matrix 0
     int E;
-    const uint8_t* w;
     const float* ws;
-    int n, k, kb, nb;
+    int n, k, kb, nb;         // kb, nb: blocks along k and n
+    int cols;                 // columns of y: n, or n/2 with SwiGLU
     void* y;
     int ydtype;
     int64_t ldy;
     int32_t* status;
+    unsigned long long wait_limit_ns;
+    int skip_copies;          // test only: the producer issues no copies (waits run out)
+    int max_chunks;           // row chunks that offsets in order can make (more: overlapping, so descending, ones)
 };
 
-__device__ __forceinline__ float e4m3_value(uint8_t b) {
-    return __low2float(bq::e4m3x2_to_half2(b));
+// ---------------------------------------------------------------- PTX used here only
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 
-// Expert e's rows [lo, hi); none (and the error recorded) where the offsets are not in order.
-__device__ void expert_rows(const Args& a, int e, int* lo, int* hi) {
-    const int l = __ldg(a.offsets + e), h = __ldg(a.offsets + e + 1);
-    const bool ok = 0 <= l && l <= h && h <= a.rows;
-    if (!ok) bq::set_device_error(a.status, BQ_DEV_BAD_ROW);
-    *lo = ok ? l : 0;
-    *hi = ok ? h : 0;
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
 }
 
-template <bool SWIGLU>
-__global__ void __launch_bounds__(kThreads) mm_kernel(const Args a) {
-    __shared__ float sx[kStep][kTile + 1], sw[SWIGLU ? 2 : 1][kStep][kTile + 1];
-    __shared__ int s_where[3];   // expert, first row, end of its rows
-    if (threadIdx.x == 0) {
-        int e = 0, lo = 0, hi = a.rows, tile = blockIdx.y;
-        if (a.offsets) {
-            for (; e < a.E; ++e) {
-                expert_rows(a, e, &lo, &hi);
-                const int tiles = (hi - lo + kTile - 1) / kTile;
-                if (tile < tiles) break;
-                tile -= tiles;
+__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// The barrier gets this thread's arrival once its copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// kind::f8f6f4, e4m3 (format 0) A and B, fp32 D, both K-major, M = 128, N = n:
+// the same fields as the fp16 descriptor.
+__device__ __forceinline__ uint32_t idesc_e4m3(int n) { return idesc_f16(n); }
+
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float peer_load(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
+                 : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.f + expf(-g)); }
+
+// ---------------------------------------------------------------- work items
+// The row chunks of every expert: s_tiles[e] = chunks of the experts before e,
+// s_tiles[E] their total.  A chunk is at most `most` rows; an expert's rows are
+// cut into chunks of near-equal size.
+__device__ __forceinline__ int chunks_of(const Args& a, int e, int most) {
+    const int lo = __ldg(a.offsets + e), hi = __ldg(a.offsets + e + 1);
+    if (!(0 <= lo && lo <= hi && hi <= a.rows)) {
+        bq::set_device_error(a.status, BQ_DEV_BAD_ROW);
+        return 0;
+    }
+    return (hi - lo + most - 1) / most;
+}
+
+// Fills s_tiles (all threads of the CTA; ends with a barrier).
+__device__ __forceinline__ void count_chunks(const Args& a, int most, int32_t* s_tiles) {
+    if (!a.offsets) {
+        if (threadIdx.x == 0) {
+            s_tiles[0] = 0;
+            s_tiles[1] = (a.rows + most - 1) / most;
+        }
+    } else if (threadIdx.x < 32) {
+        // one warp: 32 experts at a time, all loads of a group of four issued together
+        int total = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 128) {
+            int c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = e0 + 32 * i + (int)threadIdx.x;
+                c[i] = e < a.E ? chunks_of(a, e, most) : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = e0 + 32 * i + (int)threadIdx.x;
+                int incl = c[i];
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, incl, off);
+                    if ((int)threadIdx.x >= off) incl += v;
+                }
+                if (e < a.E) s_tiles[e] = total + incl - c[i];
+                total += __shfl_sync(0xffffffffu, incl, 31);
             }
         }
-        s_where[0] = e;
-        s_where[1] = lo + tile * kTile;
-        s_where[2] = hi;
+        if (threadIdx.x == 0) s_tiles[a.E] = total;
     }
     __syncthreads();
-    const int e = s_where[0], r0 = s_where[1], end = s_where[2];
-    if (e >= a.E || r0 >= end) return;
-    const int cols = SWIGLU ? a.n / 2 : a.n, c0 = blockIdx.x * kTile;
-    const int tr = threadIdx.x / 16, tc = threadIdx.x % 16;
-    float total[SWIGLU ? 2 : 1][4][4] = {}, part[SWIGLU ? 2 : 1][4][4] = {};
-    for (int k0 = 0; k0 < a.k; k0 += kStep) {
-        for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-            const int r = i / kStep, c = i % kStep;
-            const bool in_k = k0 + c < a.k;
-            sx[c][r] = in_k && r0 + r < end ? e4m3_value(a.x[(int64_t)(r0 + r) * a.k + k0 + c]) : 0.f;
-            for (int h = 0; h < (SWIGLU ? 2 : 1); ++h)
-                sw[h][c][r] = in_k && c0 + r < cols
-                                  ? e4m3_value(a.w[((int64_t)e * a.n + h * cols + c0 + r) * a.k + k0 + c]) : 0.f;
-        }
-        __syncthreads();
-        for (int c = 0; c < kStep; ++c)
-            for (int h = 0; h < (SWIGLU ? 2 : 1); ++h)
-                for (int i = 0; i < 4; ++i)
-                    for (int j = 0; j < 4; ++j)
-                        part[h][i][j] = __fmaf_rn(sx[c][tr + 16 * i], sw[h][c][tc + 16 * j], part[h][i][j]);
-        __syncthreads();
-        if ((k0 + kStep) % kBlock == 0 || k0 + kStep >= a.k) {
-            const int b = k0 / kBlock;
-            for (int h = 0; h < (SWIGLU ? 2 : 1); ++h)
-                for (int i = 0; i < 4; ++i)
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = r0 + tr + 16 * i, c = c0 + tc + 16 * j;
-                        if (r < end && c < cols) {
-                            const float s = a.xs[(int64_t)r * a.kb + b] *
-                                            a.ws[((int64_t)e * a.nb + (h * cols + c) / kBlock) * a.kb + b];
-                            total[h][i][j] = __fmaf_rn(part[h][i][j], s, total[h][i][j]);
-                        }
-                        part[h][i][j] = 0.f;
+}
+
+struct Item {
+    int e;       // matrix
+    int tile;    // tile of weight rows
+    int row0;    // first row of the chunk
+    int rows;    // its rows
+};
+
+// Item i: experts in order, their weight tiles, then the chunks of rows that
+// share such a tile (so that a tile's second reader finds it in the L2).
+__device__ __forceinline__ Item find_item(const Args& a, const int32_t* s_tiles, int w_tiles, int i) {
+    Item it;
+    int lo = 0, hi = a.E - 1;   // the last expert with s_tiles[e] * w_tiles <= i
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int64_t)s_tiles[mid] * w_tiles <= i) lo = mid; else hi = mid - 1;
+    }
+    it.e = lo;
+    const int chunks = s_tiles[lo + 1] - s_tiles[lo], local = i - s_tiles[lo] * w_tiles;
+    it.tile = local / chunks;
+    const int c = local - it.tile * chunks;
+    const int first = a.offsets ? __ldg(a.offsets + lo) : 0;
+    const int count = (a.offsets ? __ldg(a.offsets + lo + 1) : a.rows) - first;
+    const int size = (count + chunks - 1) / chunks;
+    it.row0 = first + c * size;
+    it.rows = min(size, count - c * size);
+    return it;
+}
+
+// ---------------------------------------------------------------- weights on the lanes
+//
+// Tile = 128 weight rows (MMA M, TMEM lanes) x up to NT rows of x (MMA N,
+// TMEM columns).  For few rows the time is that of reading the weights once:
+// they go from HBM to shared memory by TMA and from there into the tensor
+// cores, through no register, and the N side costs nothing where it is short.
+// With SwiGLU a tile holds 64 gate rows and their 64 up rows, 16 + 16 in each
+// lane quarter, so that a gate value and its up value are 16 lanes apart.
+//
+// 224 threads, one CTA per SM, persistent over the items:
+//   warp 0     TMA producer: 128 x 128 bytes of weights and the rows' 128
+//              bytes into a ring of S stages (one stage = one block of K);
+//   warp 1     owns the TMEM, issues the MMAs of a stage into the next slot of
+//              the accumulator ring;
+//   warp 2     copies the slot's scales (xs of every row, ws) into the ring;
+//   warps 3-6  add slot by slot to their sums, then write y.
+// With few items K is split over a cluster: the CTAs leave their sums in
+// shared memory and each finishes a share of the rows, in rank order.
+template <int NT> struct Lanes;
+template <> struct Lanes<32>  { static constexpr int S = 10, A = 8, BOX = 16; };
+template <> struct Lanes<64>  { static constexpr int S = 8,  A = 8, BOX = 32; };
+template <> struct Lanes<128> { static constexpr int S = 6,  A = 4, BOX = 32; };
+
+constexpr int kLaneThreads = 224;
+
+template <int NT>
+struct LaneSmem {
+    using L = Lanes<NT>;
+    static constexpr int kWBytes = kBlock * 128;
+    static constexpr int kStage = kWBytes + NT * 128;
+    static constexpr int kScaleSlot = NT + 4;                     // xs of the rows, ws of gate and up
+    static constexpr int kScales = L::S * kStage;
+    static constexpr int kTiles = kScales + L::A * kScaleSlot * 4;
+    static constexpr int kBars = kTiles + (kMaxExperts + 2) * 4;
+    static constexpr int kNumBars = 2 * L::S + 3 * L::A + 1;
+    static constexpr int kBytes = 1024 + kBars + 8 * kNumBars + 16;
+};
+static_assert(LaneSmem<32>::kBytes <= 232448 && LaneSmem<64>::kBytes <= 232448 && LaneSmem<128>::kBytes <= 232448, "smem");
+static_assert(LaneSmem<32>::kBars % 8 == 0 && LaneSmem<64>::kBars % 8 == 0 && LaneSmem<128>::kBars % 8 == 0, "bars");
+
+template <int NT, bool SWIGLU>
+__global__ void __launch_bounds__(kLaneThreads, 1)
+mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a,
+                int split) {
+    using L = Lanes<NT>;
+    using M = LaneSmem<NT>;
+    constexpr int S = L::S, A = L::A;
+    constexpr uint32_t kCols = NT * A;
+    static_assert(kCols == 256 || kCols == 512, "TMEM columns");
+    extern __shared__ uint8_t smem_dyn[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+    float* scales = reinterpret_cast<float*>(smem + M::kScales);
+    int32_t* s_tiles = reinterpret_cast<int32_t*>(smem + M::kTiles);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::kBars);
+    const uint32_t bar0 = smem_u32(bars), ring = smem_u32(smem);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (S + s); };
+    auto acc_full = [&](int q) { return bar0 + 8u * (2 * S + q); };
+    auto acc_empty = [&](int q) { return bar0 + 8u * (2 * S + A + q); };
+    auto sc_full = [&](int q) { return bar0 + 8u * (2 * S + 2 * A + q); };
+    const uint32_t drain = bar0 + 8u * (2 * S + 3 * A);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + M::kNumBars);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) { mbar_init(full(i), 1); mbar_init(empty(i), 1); }
+        for (int i = 0; i < A; ++i) { mbar_init(acc_full(i), 1); mbar_init(acc_empty(i), 128); mbar_init(sc_full(i), 32); }
+        mbar_init(drain, 1);
+        *abort_flag = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(tmem_slot)), "r"(kCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // launched behind whatever precedes it on the stream: nothing before this line touches global memory
+    bq::grid_dependency_wait();
+    bq::allow_dependents();
+    count_chunks(a, NT, s_tiles);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    constexpr int kTileCols = SWIGLU ? 64 : 128;
+    const int w_tiles = (a.cols + kTileCols - 1) / kTileCols;
+    const int64_t items = (int64_t)min(s_tiles[a.E], a.max_chunks) * w_tiles;
+    const int rank = split > 1 ? (int)cluster_rank() : 0;
+    const int first = blockIdx.x / split, step = gridDim.x / split;
+    const int b0 = a.kb * rank / split, b1 = a.kb * (rank + 1) / split;
+    const unsigned long long limit = a.wait_limit_ns;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = !a.skip_copies;
+            for (int64_t i = first; ok && i < items; i += step) {
+                const Item it = find_item(a, s_tiles, w_tiles, (int)i);
+                const int boxes = (it.rows + L::BOX - 1) / L::BOX;
+                for (int b = b0; b < b1; ++b) {
+                    if (issued >= S && !(ok = mbar_wait(empty(s), ph ^ 1u, abort_flag, a.status, limit))) break;
+                    const uint32_t dst = ring + s * M::kStage;
+                    mbar_expect_tx(full(s), M::kWBytes + boxes * L::BOX * 128);
+                    if (SWIGLU) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            tma_load_4d(dst + q * 4096, &map_w, b * kBlock, 64 * it.tile + 16 * q, 0, it.e, full(s));
+                    } else {
+                        tma_load_3d(dst, &map_w, b * kBlock, 128 * it.tile, it.e, full(s));
                     }
+                    for (int q = 0; q < boxes; ++q)
+                        tma_load_2d(dst + M::kWBytes + q * L::BOX * 128, &map_x, b * kBlock, it.row0 + q * L::BOX, full(s));
+                    ++issued;
+                    if (++s == S) { s = 0; ph ^= 1u; }
+                }
+            }
+            if (!ok) {   // let our own copies land before the CTA leaves (bounded)
+                volatile uint32_t no_abort = 0;
+                for (int u = max(0, issued - S); u < issued; ++u)
+                    mbar_wait(full(u % S), (u / S) & 1, &no_abort, a.status, limit);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int s = 0, q = 0;
+            uint32_t ph = 0, aph = 0;
+            bool ok = true, wrapped = false;
+            for (int64_t i = first; ok && i < items; i += step) {
+                const Item it = find_item(a, s_tiles, w_tiles, (int)i);
+                const uint32_t idesc = idesc_e4m3((it.rows + 15) & ~15);
+                for (int b = b0; b < b1; ++b) {
+                    if (wrapped && !(ok = mbar_wait(acc_empty(q), aph ^ 1u, abort_flag, a.status, limit))) break;
+                    if (!(ok = mbar_wait(full(s), ph, abort_flag, a.status, limit))) break;
+                    tc_fence_after();
+                    const uint64_t wd = smem_desc_sw128(ring + s * M::kStage);
+                    const uint64_t xd = smem_desc_sw128(ring + s * M::kStage + M::kWBytes);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)     // +32 bytes along K
+                        mma_e4m3(tmem + q * NT, wd + 2 * j, xd + 2 * j, idesc, j != 0);
+                    mma_commit(empty(s));
+                    mma_commit(acc_full(q));
+                    if (++s == S) { s = 0; ph ^= 1u; }
+                    if (++q == A) { q = 0; aph ^= 1u; wrapped = true; }
+                }
+            }
+            if (!ok) {   // our MMAs end before the TMEM is freed (bounded)
+                volatile uint32_t no_abort = 0;
+                mma_commit(drain);
+                mbar_wait(drain, 0, &no_abort, a.status, limit);
+            }
+        }
+    } else if (warp == 2) {
+        int q = 0;
+        uint32_t aph = 0;
+        bool ok = true, wrapped = false;
+        for (int64_t i = first; ok && i < items; i += step) {
+            const Item it = find_item(a, s_tiles, w_tiles, (int)i);
+            const float* xs = a.xs + (int64_t)it.row0 * a.kb;
+            // weight rows 128 tile.. are scale row `tile`; of a gate/up weight, gate rows 64 tile.. are scale row
+            // tile / 2 and their up rows n/2 further on
+            const int wrow = lane == 0 ? (SWIGLU ? it.tile / 2 : it.tile) : it.tile / 2 + a.nb / 2;
+            const float* ws = a.ws + ((int64_t)it.e * a.nb + wrow) * a.kb;
+            for (int b = b0; b < b1; ++b) {
+                if (wrapped && !(ok = warp_wait_all(acc_empty(q), aph ^ 1u, abort_flag, a.status, limit))) break;
+                const uint32_t dst = smem_u32(scales + q * M::kScaleSlot);
+                for (int r = lane; r < it.rows; r += 32) copy4_async(dst + 4 * r, xs + (int64_t)r * a.kb + b);
+                if (lane < (SWIGLU ? 2 : 1)) copy4_async(dst + 4 * (NT + lane), ws + b);
+                copies_arrive(sc_full(q));
+                if (++q == A) { q = 0; aph ^= 1u; wrapped = true; }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+        const int quarter = warp & 3, p = 32 * quarter + lane;
+        const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
+        int q = 0;
+        uint32_t aph = 0;
+        bool ok = true;
+        for (int64_t i = first; ok && i < items; i += step) {
+            const Item it = find_item(a, s_tiles, w_tiles, (int)i);
+            float acc[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] = 0.f;
+            for (int b = b0; b < b1; ++b) {
+                if (!(ok = warp_wait_all(sc_full(q), aph, abort_flag, a.status, limit))) break;
+                if (!(ok = warp_wait_all(acc_full(q), aph, abort_flag, a.status, limit))) break;
+                tc_fence_after();
+                const float* sc = scales + q * M::kScaleSlot;
+                const float ws = sc[NT + (SWIGLU ? (lane >> 4) : 0)];
+#pragma unroll
+                for (int c = 0; c < NT; c += 32) {
+                    if (c < it.rows) {
+                        uint32_t v[32];
+                        tmem_ld32(tmem + lane_base + q * NT + c, v);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 x4 = *reinterpret_cast<const float4*>(sc + c + j);
+                            acc[c + j] = __fmaf_rn(__uint_as_float(v[j]), x4.x * ws, acc[c + j]);
+                            acc[c + j + 1] = __fmaf_rn(__uint_as_float(v[j + 1]), x4.y * ws, acc[c + j + 1]);
+                            acc[c + j + 2] = __fmaf_rn(__uint_as_float(v[j + 2]), x4.z * ws, acc[c + j + 2]);
+                            acc[c + j + 3] = __fmaf_rn(__uint_as_float(v[j + 3]), x4.w * ws, acc[c + j + 3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(acc_empty(q));
+                if (++q == A) { q = 0; aph ^= 1u; }
+            }
+            if (!ok) break;
+            if (split > 1) {   // sums to shared memory (every copy and MMA of this CTA has ended): [row][lane]
+                float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (t < it.rows) red[t * 128 + p] = acc[t];
+                break;         // one item per cluster
+            }
+            const int c = SWIGLU ? 64 * it.tile + 16 * quarter + (lane & 15) : 128 * it.tile + p;
+            if (SWIGLU) {
+                // lanes 0-15 hold gate rows, 16-31 their up rows; each half finishes every other row of x
+#pragma unroll
+                for (int t = 0; t < NT; t += 2) {
+                    if (t < it.rows) {
+                        const float recv = __shfl_xor_sync(0xffffffffu, lane < 16 ? acc[t + 1] : acc[t], 16);
+                        const float g = lane < 16 ? acc[t] : recv, u = lane < 16 ? recv : acc[t + 1];
+                        const int r = t + (lane >> 4);
+                        if (r < it.rows) bq::store_value(a.y, (int64_t)(it.row0 + r) * a.ldy + c, a.ydtype, silu_f(g) * u);
+                    }
+                }
+            } else if (c < a.cols) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (t < it.rows) bq::store_value(a.y, (int64_t)(it.row0 + t) * a.ldy + c, a.ydtype, acc[t]);
+            }
         }
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int r = r0 + tr + 16 * i, c = c0 + tc + 16 * j;
-            if (r >= end || c >= cols) continue;
-            float v = total[0][i][j];
-            if (SWIGLU) v = __fdiv_rn(v, 1.f + expf(-v)) * total[SWIGLU ? 1 : 0][i][j];
-            bq::store_value(a.y, (int64_t)r * a.ldy + c, a.ydtype, v);
+
+    if (split > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 3 && first < items && !*abort_flag) {
+            const int quarter = warp & 3, p = 32 * quarter + lane;
+            const Item it = find_item(a, s_tiles, w_tiles, first);
+            const int c = SWIGLU ? 64 * it.tile + 16 * quarter + (lane & 15) : 128 * it.tile + p;
+            for (int t = rank; t < it.rows; t += split) {
+                float part[kMaxCluster];
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r)
+                    part[r] = r < split ? peer_load(smem_u32(smem) + 4 * (t * 128 + p), r) : 0.f;
+                float v = part[0];
+#pragma unroll
+                for (int r = 1; r < kMaxCluster; ++r) v += part[r];
+                if (SWIGLU) {
+                    const float u = __shfl_xor_sync(0xffffffffu, v, 16);
+                    v = silu_f(v) * u;
+                }
+                if (c < a.cols && (!SWIGLU || lane < 16))
+                    bq::store_value(a.y, (int64_t)(it.row0 + t) * a.ldy + c, a.ydtype, v);
+            }
         }
+        __syncwarp();
+        cluster_sync();   // peers may still be reading this CTA's sums
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- host side
+bool encode(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+            const uint32_t* box) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, ones,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows [rows][k] in boxes of 128 bytes x `box` rows.
+bool row_map(CUtensorMap* map, const uint8_t* x, int rows, int k, int box) {
+    const uint64_t dims[2] = {(uint64_t)k, (uint64_t)rows}, strides[1] = {(uint64_t)k};
+    const uint32_t b[2] = {kBlock, (uint32_t)box};
+    return encode(map, x, 2, dims, strides, b);
+}
+
+// Weights [E][n][k] in boxes of 128 bytes x 128 rows; of a gate/up weight
+// [E][2][n/2][k] in boxes of 16 gate rows and their 16 up rows.
+bool weight_map(CUtensorMap* map, const uint8_t* w, int E, int n, int k, bool swiglu) {
+    if (!swiglu) {
+        const uint64_t dims[3] = {(uint64_t)k, (uint64_t)n, (uint64_t)E}, strides[2] = {(uint64_t)k, (uint64_t)n * k};
+        const uint32_t b[3] = {kBlock, 128, 1};
+        return encode(map, w, 3, dims, strides, b);
+    }
+    const uint64_t h = n / 2;
+    const uint64_t dims[4] = {(uint64_t)k, h, 2, (uint64_t)E}, strides[3] = {(uint64_t)k, h * k, (uint64_t)n * k};
+    const uint32_t b[4] = {kBlock, 16, 2, 1};
+    return encode(map, w, 4, dims, strides, b);
+}
+
+constexpr int kSms = 152;
+
+template <int NT, bool SWIGLU>
+cudaError_t launch_lanes(const CUtensorMap& map_w, const CUtensorMap& map_x, const Args& a, int64_t items, int split,
+                         cudaStream_t st) {
+    // per device: the attribute is a property of the function on the current device
+    static std::atomic<bool> attr_set[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(mm_lanes_kernel<NT, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   LaneSmem<NT>::kBytes);
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(true, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(split > 1 ? items * split : std::min<int64_t>(items, kSms)));
+    cfg.blockDim = dim3(kLaneThreads);
+    cfg.dynamicSmemBytes = LaneSmem<NT>::kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, mm_lanes_kernel<NT, SWIGLU>, map_w, map_x, a, split);
 }
 
 bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32_t rows, const int32_t* offsets,
@@ -121,7 +519,7 @@ bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32
                         n, k);
     if (swiglu && n % 256)
         return bq::fail(BQ_ERR_SHAPE, "%s: a gate/up weight needs n = %d to be a multiple of 256", name, n);
-    if (E < 1 || E > 1024 || (int64_t)E * n > (int64_t)INT32_MAX)
+    if (E < 1 || E > kMaxExperts || (int64_t)E * n > (int64_t)INT32_MAX)
         return bq::fail(BQ_ERR_SHAPE, "%s: E = %d outside [1, 1024], or E * n beyond %d", name, E, INT32_MAX);
     if (rows == 0) return BQ_OK;
     if (!x || !xscales || !w || !wscales || !y) return bq::fail(BQ_ERR_NULL, "%s: NULL pointer", name);
@@ -133,15 +531,34 @@ bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32
         !bq::aligned(offsets, 4) || !bq::aligned(y, es))
         return bq::fail(BQ_ERR_ALIGN, "%s: x and w must be 16-byte aligned, scales and offsets 4-byte, y to its element",
                         name);
-    const int64_t row_tiles = (int64_t)(rows + kTile - 1) / kTile + (offsets ? std::min(E, rows) : 0);
-    if (row_tiles > 65535) return bq::fail(BQ_ERR_SHAPE, "%s: %d rows are too many", name, rows);
+    // most items there can be, for the grid and (as an int) inside the kernel
+    const int nt = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    const int64_t w_tiles = (cols + (swiglu ? 63 : 127)) / (swiglu ? 64 : 128);
+    const int64_t chunks = (int64_t)(rows + nt - 1) / nt + (offsets ? std::min(E, rows) : 0);
+    const int64_t items = chunks * w_tiles;
+    if (items > INT32_MAX / 2) return bq::fail(BQ_ERR_SHAPE, "%s: %d rows x %d columns are too many", name, rows, cols);
     bq_status s = bq::check_arch();
     if (s != BQ_OK) return s;
-    Args a{x, xscales, rows, offsets, E, w, wscales, n, k, (k + kBlock - 1) / kBlock, (n + kBlock - 1) / kBlock,
-           y, ydtype, ldy, bq::device_status_ptr()};
-    const dim3 grid((cols + kTile - 1) / kTile, (unsigned)row_tiles);
-    if (swiglu) mm_kernel<true><<<grid, kThreads, 0, st>>>(a);
-    else mm_kernel<false><<<grid, kThreads, 0, st>>>(a);
+    const bq::WaitProbe probe = bq::wait_probe();
+    const Args a{xscales, rows, offsets, E, wscales, n, k, (k + kBlock - 1) / kBlock, (n + kBlock - 1) / kBlock, cols,
+                 y, ydtype, ldy, bq::device_status_ptr(), probe.limit_ns, probe.skip_weight_copies,
+                 (int)chunks};
+    int split = 1;
+    while (split < kMaxCluster && items * split * 2 <= kSms && a.kb >= 4 * split) split *= 2;
+    CUtensorMap map_w, map_x;
+    if (!weight_map(&map_w, w, E, n, k, swiglu) || !row_map(&map_x, x, rows, k, nt == 32 ? 16 : 32))
+        return bq::fail(BQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", name);
+    cudaError_t e;
+    if (swiglu) {
+        e = nt == 32 ? launch_lanes<32, true>(map_w, map_x, a, items, split, st)
+          : nt == 64 ? launch_lanes<64, true>(map_w, map_x, a, items, split, st)
+                     : launch_lanes<128, true>(map_w, map_x, a, items, split, st);
+    } else {
+        e = nt == 32 ? launch_lanes<32, false>(map_w, map_x, a, items, split, st)
+          : nt == 64 ? launch_lanes<64, false>(map_w, map_x, a, items, split, st)
+                     : launch_lanes<128, false>(map_w, map_x, a, items, split, st);
+    }
+    if (e != cudaSuccess) return bq::fail(BQ_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
     bq::note_launch();
     return bq::check_launch(name);
 }

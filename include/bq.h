@@ -549,12 +549,13 @@ bq_status bq_set_stage_events(int32_t stage, void* start_event, void* stop_event
 uint64_t bq_launch_count(void);
 
 /*
- * Test hook for the bounded waits of the tensor-core GEMM (the failure
+ * Test hook for the bounded waits of the tensor-core kernels (the failure
  * detection path; the pages have no counterpart).  Every barrier wait in
- * that kernel gives up after a time limit, sets BQ_DEV_WAIT_TIMEOUT in the
+ * such a kernel gives up after a time limit, sets BQ_DEV_WAIT_TIMEOUT in the
  * device status word, lets its own copies in flight land, frees its TMEM
  * and returns.  Normally nothing makes a wait run out.  While set, GEMM
- * launches (bq_qmm above the GEMV range, the prefill MoE layer) take
+ * launches (bq_qmm above the GEMV range, the prefill MoE layer, the FP8
+ * products) take
  * `wait_limit_ns` as that limit (1 ms .. 2 s; 0 restores the 2 s default)
  * and, if `skip_weight_copies` is 1, their weight producer issues no copies,
  * so the waits for weights run out: the call then returns BQ_OK, its output

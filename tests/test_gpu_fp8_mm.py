@@ -352,3 +352,21 @@ def test_fp8_layer_captured_replayed_and_on_another_stream(lib):
     other.synchronize()
     check_layer(a, *shape)
     assert lib.device_status() == lib.DEV_OK
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 256, 1024), (300, 512, 1024), (2048, 2048, 512)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(lib, m, n, k):
+    import torch
+    g = np.random.default_rng(30)
+    codes, x, xs = fp8_rows(g, m, k)
+    w, ws = fp8_weight(g, 1, n, k)
+    a = [dev(codes), dev(xs), dev(w[0]), dev(ws[0]), torch.empty(m, n, device="cuda")]
+    lib.test_set_wait_probe(True, 2_000_000)
+    try:
+        lib.mm_fp8_b128(*a)
+        assert lib.device_status() == lib.DEV_WAIT_TIMEOUT
+    finally:
+        lib.test_set_wait_probe(False)
+    lib.mm_fp8_b128(*a)
+    assert lib.device_status() == lib.DEV_OK
+    check(a[-1], *expected(x, xs, w[0], ws[0], "f32"))
