@@ -118,11 +118,20 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_raw_stream = None   # handle of the current stream of a device
+
+
 def _stream(stream):
-    if stream is None:
-        import torch
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    """Handle of `stream`, or of the current stream of the current device."""
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    if _raw_stream is None:
+        # the handle alone; a torch.cuda.Stream object costs 3 us to make
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
 
 
 def status_string(s: int) -> str:
@@ -360,15 +369,19 @@ def moe_gather_qmm_hidden(layer: MoELayer, router: QWeight, hidden, gamma, eps: 
 # ---------------------------------------------------------------- rows by expert, FP8 rows and products
 # These calls read shapes, strides and types from their tensors, so the tensors
 # are checked here: a call that does not fit raises BQError and launches nothing.
-_DT = None   # torch dtype -> bq_dtype, filled in on first use (torch is imported lazily)
+# A small call lasts a few microseconds on the GPU, so the checks read each
+# attribute once, and torch (imported lazily by this package) is looked up once.
+_DT = None          # torch dtype -> bq_dtype
+_KINDS = None       # _dense's kinds -> the torch dtypes they take
+_get_device = None  # ordinal of the current CUDA device
 
 
-def _dtypes():
-    global _DT
-    if _DT is None:
-        import torch
-        _DT = {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}
-    return _DT
+def _load_torch():
+    global _DT, _KINDS, _get_device
+    import torch
+    _DT = {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}
+    _KINDS = {"f32": (torch.float32,), "i32": (torch.int32,), "fp8": (torch.float8_e4m3fn, torch.uint8)}
+    _get_device = torch.cuda.current_device
 
 
 def _refuse(status: int, where: str, msg: str):
@@ -377,56 +390,60 @@ def _refuse(status: int, where: str, msg: str):
 
 def _same_device(where: str, *tensors):
     """Every tensor on the current CUDA device (the one the stream belongs to)."""
-    import torch
-    cur = None
+    if _DT is None:
+        _load_torch()
+    first = tensors[0].get_device()
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            _refuse(2, where, f"a tensor is on {t.device}, not on a CUDA device")
-        if cur is None:
-            cur = torch.cuda.current_device()
-        if t.device.index != cur:
-            _refuse(2, where, f"a tensor is on {t.device}, the current device is cuda:{cur}")
+        if t is not None and (t.get_device() != first or first < 0):
+            if not t.is_cuda:
+                _refuse(2, where, f"a tensor is on {t.device}, not on a CUDA device")
+            _refuse(2, where, f"tensors are on cuda:{first} and {t.device}")
+    if first != _get_device():
+        _refuse(2, where, f"the tensors are on cuda:{first}, the current device is cuda:{_get_device()}")
 
 
 def _rows_of(where: str, what: str, t, rows=None, cols=None, dtype=None):
     """(pointer, bq_dtype, rows, cols, row stride) of a matrix whose rows are dense."""
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+    if _DT is None:
+        _load_torch()
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape != (rows, cols or shape[1])):
         want = f"[{'rows' if rows is None else rows}, {'columns' if cols is None else cols}]"
-        _refuse(2, where, f"{what} has shape {list(t.shape)}, expected {want}")
-    dt = _dtypes().get(t.dtype)
+        _refuse(2, where, f"{what} has shape {list(shape)}, expected {want}")
+    dt = _DT.get(t.dtype)
     if dt is None or (dtype is not None and dt != dtype):
         _refuse(4, where, f"{what} has type {t.dtype}")
-    r, c = t.shape
-    if c > 1 and t.stride(1) != 1:
-        _refuse(3, where, f"the rows of {what} are not contiguous (strides {tuple(t.stride())})")
-    if max(r, c) > 0x7fffffff:
-        _refuse(2, where, f"{what} has shape {list(t.shape)}")
-    return t.data_ptr(), dt, r, c, t.stride(0) if r > 1 else c
+    r, c = shape
+    ld, step = t.stride()
+    if step != 1 and c > 1:
+        _refuse(3, where, f"the rows of {what} are not contiguous (strides {(ld, step)})")
+    if r > 0x7fffffff or c > 0x7fffffff:
+        _refuse(2, where, f"{what} has shape {list(shape)}")
+    return t.data_ptr(), dt, r, c, ld if r > 1 else c
 
 
 def _dense(where: str, what: str, t, shape, kind: str):
     """Pointer of a contiguous tensor of the given shape; kind: f32, i32 or fp8 (e4m3 bytes)."""
-    import torch
-    ok = {"f32": (torch.float32,), "i32": (torch.int32,), "fp8": (torch.float8_e4m3fn, torch.uint8)}[kind]
-    if t.dtype not in ok:
+    if _DT is None:
+        _load_torch()
+    if t.dtype not in _KINDS[kind]:
         _refuse(4, where, f"{what} has type {t.dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         _refuse(2, where, f"{what} has shape {list(t.shape)} and strides {tuple(t.stride())}, "
                           f"expected contiguous {list(shape)}")
     return t.data_ptr()
 
 
 def _pairs(where: str, inv, t: int):
-    """(pointer, k) of inv, int32 [T, k] or flat [T * k] as moe_permute writes it."""
-    import torch
-    if inv.dtype != torch.int32:
+    """(pointer, k) of inv, int32 [T, k] or flat [T * k] as moe_permute writes it (T > 0)."""
+    if _DT is None:
+        _load_torch()
+    if inv.dtype not in _KINDS["i32"]:
         _refuse(4, where, f"inv has type {inv.dtype}")
-    n = inv.numel()
-    k = n // t
-    if k * t != n or not inv.is_contiguous() or inv.dim() > 2 or (inv.dim() == 2 and inv.shape[0] != t):
-        _refuse(2, where, f"inv has shape {list(inv.shape)} and strides {tuple(inv.stride())} for {t} tokens")
+    shape = inv.shape
+    k, rest = (shape[1], shape[0] - t) if len(shape) == 2 else divmod(shape[0], t) if len(shape) == 1 else (0, 1)
+    if rest or not inv.is_contiguous():
+        _refuse(2, where, f"inv has shape {list(shape)} and strides {tuple(inv.stride())} for {t} tokens")
     return inv.data_ptr(), k
 
 
@@ -526,19 +543,20 @@ def moe_dispatch_fp8_b128(x, inv, q, scales, stream=None):
 
 
 def _product(where, x, x_scales, w, w_scales, y, swiglu, grouped):
-    if x.dim() != 2 or w.dim() != (3 if grouped else 2):
-        _refuse(2, where, f"x has shape {list(x.shape)}, w {list(w.shape)}")
+    wshape = w.shape
+    if len(x.shape) != 2 or len(wshape) != (3 if grouped else 2):
+        _refuse(2, where, f"x has shape {list(x.shape)}, w {list(wshape)}")
     m, k = x.shape
-    n = w.shape[-2]
-    lead = tuple(w.shape[:1]) if grouped else ()
+    n = wshape[-2]
+    if max(m, k, *wshape) > 0x7fffffff:
+        _refuse(2, where, f"x has shape {list(x.shape)}, w {list(wshape)}")
+    kb, nb = (k + 127) // 128, (n + 127) // 128
     px = _dense(where, "x", x, (m, k), "fp8")
-    pxs = _dense(where, "x_scales", x_scales, (m, -(-k // 128)), "f32")
-    pw = _dense(where, "w", w, lead + (n, k), "fp8")
-    pws = _dense(where, "w_scales", w_scales, lead + (-(-n // 128), -(-k // 128)), "f32")
+    pxs = _dense(where, "x_scales", x_scales, (m, kb), "f32")
+    pw = _dense(where, "w", w, (wshape[0], n, k) if grouped else (n, k), "fp8")
+    pws = _dense(where, "w_scales", w_scales, (wshape[0], nb, kb) if grouped else (nb, kb), "f32")
     py, dt, _, _, ldy = _rows_of(where, "y", y, m, n // 2 if swiglu else n)
-    if max(m, n, k, *lead) > 0x7fffffff:
-        _refuse(2, where, f"x has shape {list(x.shape)}, w {list(w.shape)}")
-    return px, pxs, m, pw, pws, n, k, int(bool(swiglu)), py, dt, ldy
+    return px, pxs, m, pw, pws, n, k, 1 if swiglu else 0, py, dt, ldy
 
 
 def mm_fp8_b128(x, x_scales, w, w_scales, y, swiglu: bool = False, stream=None):

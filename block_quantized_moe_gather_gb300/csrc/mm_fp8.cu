@@ -11,6 +11,7 @@
 // on the next blocks.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "gemm_internal.cuh"
 #include "row_types.cuh"
@@ -445,6 +446,279 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     }
 }
 
+// ---------------------------------------------------------------- rows on the lanes
+//
+// Tile = 128 rows of x (MMA M, TMEM lanes) x 256 weight rows (MMA N, TMEM
+// columns), for many rows: there the tensor cores bound it, and with the rows
+// on the lanes a block's scale is one number per thread and column half, so
+// that adding a block costs one packed multiply-add per two values (against a
+// scale fetched per column above).  With SwiGLU the columns are 128 gate rows
+// and their 128 up rows, and a thread holds both of each.
+//
+// 320 threads, one CTA per SM, persistent over the items:
+//   warp 0     TMA producer: 128 bytes of 128 rows and of 256 weight rows into
+//              a ring of 4 stages (48 KB each);
+//   warp 1     owns the TMEM (two slots of 256 columns), issues the MMAs;
+//   warps 2-9  one thread per row and column half: 128 fp32 sums in registers,
+//              scales read one block ahead, then y.
+constexpr int kWideThreads = 320;
+
+struct WideSmem {
+    static constexpr int S = 4, A = 2, N = 256;
+    static constexpr int kXBytes = 128 * 128;
+    static constexpr int kStage = kXBytes + N * 128;
+    static constexpr int kTiles = S * kStage;
+    static constexpr int kBars = kTiles + (kMaxExperts + 2) * 4;
+    static constexpr int kNumBars = 2 * S + 2 * A + 1;
+    static constexpr int kBytes = 1024 + kBars + 8 * kNumBars + 16;
+};
+static_assert(WideSmem::kBytes <= 232448 && WideSmem::kBars % 8 == 0, "smem");
+
+// Waits for this warp's TMEM loads; the values pass through so that no use of them moves before the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 ::"memory");
+}
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+
+// acc[i] += v[2i, 2i+1] * s, sixteen pairs
+__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&v)[32], uint64_t s) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        uint64_t x;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(v[2 * i]), "r"(v[2 * i + 1]));
+        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i]) : "l"(x), "l"(s));
+    }
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// 16 values f of a row of y from column c on: 32-byte stores where they lie in y and on 32-byte boundaries.
+__device__ __forceinline__ void store16(const Args& a, int64_t row, int c, const float (&f)[16], bool wide) {
+    if (wide && c + 16 <= a.cols) {
+        uint8_t* p = static_cast<uint8_t*>(a.y) + (row * a.ldy + c) * (a.ydtype == BQ_DT_F32 ? 4 : 2);
+        uint32_t w[8];
+        if (a.ydtype == BQ_DT_F32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(f[8 * h + i]);
+                store32(p + 32 * h, w);
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (a.ydtype == BQ_DT_F16) {
+                w[i] = bq::h2_as_u32(__floats2half2_rn(f[2 * i], f[2 * i + 1]));
+            } else {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+        }
+        store32(p, w);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (c + i < a.cols) bq::store_value(a.y, row * a.ldy + c + i, a.ydtype, f[i]);
+}
+
+template <bool SWIGLU>
+__global__ void __launch_bounds__(kWideThreads, 1)
+mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a) {
+    using M = WideSmem;
+    constexpr int S = M::S, A = M::A, N = M::N, kTileCols = SWIGLU ? 128 : 256;
+    extern __shared__ uint8_t smem_dyn[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+    int32_t* s_tiles = reinterpret_cast<int32_t*>(smem + M::kTiles);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::kBars);
+    const uint32_t bar0 = smem_u32(bars), ring = smem_u32(smem);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (S + s); };
+    auto acc_full = [&](int q) { return bar0 + 8u * (2 * S + q); };
+    auto acc_empty = [&](int q) { return bar0 + 8u * (2 * S + A + q); };
+    const uint32_t drain = bar0 + 8u * (2 * S + 2 * A);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + M::kNumBars);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) { mbar_init(full(i), 1); mbar_init(empty(i), 1); }
+        for (int i = 0; i < A; ++i) { mbar_init(acc_full(i), 1); mbar_init(acc_empty(i), 256); }
+        mbar_init(drain, 1);
+        *abort_flag = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(tmem_slot)), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // launched behind whatever precedes it on the stream: nothing before this line touches global memory
+    bq::grid_dependency_wait();
+    bq::allow_dependents();
+    count_chunks(a, 128, s_tiles);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int w_tiles = (a.cols + kTileCols - 1) / kTileCols;
+    const int64_t items = (int64_t)min(s_tiles[a.E], a.max_chunks) * w_tiles;
+    const unsigned long long limit = a.wait_limit_ns;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = !a.skip_copies;
+            for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+                const Item it = find_item(a, s_tiles, w_tiles, (int)i);
+                const int boxes = (it.rows + 31) / 32;
+                // the two boxes of 128 weight rows
+                const int w0 = kTileCols * it.tile, w1 = SWIGLU ? a.n / 2 + w0 : w0 + 128;
+                for (int b = 0; b < a.kb; ++b) {
+                    if (issued >= S && !(ok = mbar_wait(empty(s), ph ^ 1u, abort_flag, a.status, limit))) break;
+                    const uint32_t dst = ring + s * M::kStage;
+                    mbar_expect_tx(full(s), boxes * 4096 + N * 128);
+                    for (int q = 0; q < boxes; ++q)
+                        tma_load_2d(dst + q * 4096, &map_x, b * kBlock, it.row0 + 32 * q, full(s));
+                    tma_load_3d(dst + M::kXBytes, &map_w, b * kBlock, w0, it.e, full(s));
+                    tma_load_3d(dst + M::kXBytes + 16384, &map_w, b * kBlock, w1, it.e, full(s));
+                    ++issued;
+                    if (++s == S) { s = 0; ph ^= 1u; }
+                }
+            }
+            if (!ok) {   // let our own copies land before the CTA leaves (bounded)
+                volatile uint32_t no_abort = 0;
+                for (int u = max(0, issued - S); u < issued; ++u)
+                    mbar_wait(full(u % S), (u / S) & 1, &no_abort, a.status, limit);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_e4m3(N);
+            int s = 0, q = 0;
+            uint32_t ph = 0, aph = 0;
+            bool ok = true, wrapped = false;
+            for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+                for (int b = 0; b < a.kb; ++b) {
+                    if (wrapped && !(ok = mbar_wait(acc_empty(q), aph ^ 1u, abort_flag, a.status, limit))) break;
+                    if (!(ok = mbar_wait(full(s), ph, abort_flag, a.status, limit))) break;
+                    tc_fence_after();
+                    const uint64_t xd = smem_desc_sw128(ring + s * M::kStage);
+                    const uint64_t wd = smem_desc_sw128(ring + s * M::kStage + M::kXBytes);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)     // +32 bytes along K
+                        mma_e4m3(tmem + q * N, xd + 2 * j, wd + 2 * j, idesc, j != 0);
+                    mma_commit(empty(s));
+                    mma_commit(acc_full(q));
+                    if (++s == S) { s = 0; ph ^= 1u; }
+                    if (++q == A) { q = 0; aph ^= 1u; wrapped = true; }
+                }
+            }
+            if (!ok) {   // our MMAs end before the TMEM is freed (bounded)
+                volatile uint32_t no_abort = 0;
+                mma_commit(drain);
+                mbar_wait(drain, 0, &no_abort, a.status, limit);
+            }
+        }
+    } else {
+        const int quarter = warp & 3, half = (warp - 2) >> 2, p = 32 * quarter + lane;
+        // this thread's columns: 64 from c_lo on and 64 from c_hi on (with SwiGLU gate columns and their up columns)
+        const uint32_t c_lo = SWIGLU ? 64 * half : 128 * half, c_hi = SWIGLU ? 128 + 64 * half : 128 * half + 64;
+        const uint32_t base = tmem + ((uint32_t)(32 * quarter) << 16);
+        const int es = a.ydtype == BQ_DT_F32 ? 4 : 2;
+        const bool wide = (reinterpret_cast<uintptr_t>(a.y) | (uintptr_t)(a.ldy * es)) % 32 == 0;
+        int q = 0;
+        uint32_t aph = 0;
+        bool ok = true;
+        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            const Item it = find_item(a, s_tiles, w_tiles, (int)i);
+            const float* xs = a.xs + (int64_t)(it.row0 + min(p, it.rows - 1)) * a.kb;
+            const int wb_lo = SWIGLU ? it.tile : min(2 * it.tile + half, a.nb - 1);
+            const float* ws_lo = a.ws + ((int64_t)it.e * a.nb + wb_lo) * a.kb;
+            const float* ws_hi = SWIGLU ? ws_lo + (int64_t)(a.nb / 2) * a.kb : ws_lo;
+            uint64_t acc[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = 0ull;
+            float x_next = __ldg(xs), lo_next = __ldg(ws_lo), hi_next = SWIGLU ? __ldg(ws_hi) : 0.f;
+            for (int b = 0; b < a.kb; ++b) {
+                const float s_lo = x_next * lo_next, s_hi = SWIGLU ? x_next * hi_next : s_lo;
+                const uint64_t lo2 = pack2(s_lo, s_lo), hi2 = pack2(s_hi, s_hi);
+                const int bn = min(b + 1, a.kb - 1);
+                x_next = __ldg(xs + bn);
+                lo_next = __ldg(ws_lo + bn);
+                if (SWIGLU) hi_next = __ldg(ws_hi + bn);
+                if (!(ok = warp_wait_all(acc_full(q), aph, abort_flag, a.status, limit))) break;
+                tc_fence_after();
+                uint32_t v0[32], v1[32];
+                const uint32_t t = base + q * N;
+                tmem_ld32(t + c_lo, v0);
+                tmem_wait_ld(v0);
+                tmem_ld32(t + c_lo + 32, v1);
+                add_scaled(acc, v0, lo2);
+                tmem_wait_ld(v1);
+                tmem_ld32(t + c_hi, v0);
+                add_scaled(acc + 16, v1, lo2);
+                tmem_wait_ld(v0);
+                tmem_ld32(t + c_hi + 32, v1);
+                add_scaled(acc + 32, v0, hi2);
+                tmem_wait_ld(v1);
+                tc_fence_before();
+                mbar_arrive(acc_empty(q));
+                add_scaled(acc + 48, v1, hi2);
+                if (++q == A) { q = 0; aph ^= 1u; }
+            }
+            if (!ok) break;
+            if (p < it.rows) {
+                const int c0 = kTileCols * it.tile + (SWIGLU ? 64 : 128) * half;
+#pragma unroll
+                for (int g = 0; g < (SWIGLU ? 4 : 8); ++g) {
+                    float f[16];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 v = unpack2(acc[8 * g + j]);
+                        f[2 * j] = v.x;
+                        f[2 * j + 1] = v.y;
+                        if (SWIGLU) {
+                            const float2 u = unpack2(acc[32 + ((8 * g + j) & 31)]);
+                            f[2 * j] = silu_f(v.x) * u.x;
+                            f[2 * j + 1] = silu_f(v.y) * u.y;
+                        }
+                    }
+                    store16(a, it.row0 + p, c0 + 16 * g, f, wide);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
+}
+
 // ---------------------------------------------------------------- host side
 bool encode(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
             const uint32_t* box) {
@@ -508,6 +782,22 @@ cudaError_t launch_lanes(const CUtensorMap& map_w, const CUtensorMap& map_x, con
     return cudaLaunchKernelEx(&cfg, mm_lanes_kernel<NT, SWIGLU>, map_w, map_x, a, split);
 }
 
+template <bool SWIGLU>
+cudaError_t launch_wide(const CUtensorMap& map_w, const CUtensorMap& map_x, const Args& a, int64_t items,
+                        cudaStream_t st) {
+    static std::atomic<bool> attr_set[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(mm_wide_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideSmem::kBytes);
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(true, std::memory_order_release);
+    }
+    return bq::launch_after(mm_wide_kernel<SWIGLU>, dim3((unsigned)std::min<int64_t>(items, kSms)), dim3(kWideThreads),
+                            WideSmem::kBytes, st, map_w, map_x, a);
+}
+
 bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32_t rows, const int32_t* offsets,
                  int32_t E, const uint8_t* w, const float* wscales, int32_t n, int32_t k, int32_t swiglu, void* y,
                  int32_t ydtype, int64_t ldy, cudaStream_t st) {
@@ -531,32 +821,36 @@ bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32
         !bq::aligned(offsets, 4) || !bq::aligned(y, es))
         return bq::fail(BQ_ERR_ALIGN, "%s: x and w must be 16-byte aligned, scales and offsets 4-byte, y to its element",
                         name);
-    // most items there can be, for the grid and (as an int) inside the kernel
+    const int experts = offsets ? std::min(E, rows) : 1;   // that can have rows
+    // most row chunks and items there can be, for the grid and (as an int) inside the kernel
+    auto chunks_of = [&](int most) { return (int64_t)(rows + most - 1) / most + (offsets ? experts : 0); };
+    auto tiles_of = [&](int width) { return (int64_t)(cols + width - 1) / width; };
+    const bool wide = rows / experts >= 96 && chunks_of(128) * tiles_of(swiglu ? 128 : 256) >= 100;
     const int nt = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    const int64_t w_tiles = (cols + (swiglu ? 63 : 127)) / (swiglu ? 64 : 128);
-    const int64_t chunks = (int64_t)(rows + nt - 1) / nt + (offsets ? std::min(E, rows) : 0);
-    const int64_t items = chunks * w_tiles;
+    const int64_t chunks = chunks_of(wide ? 128 : nt);
+    const int64_t items = chunks * (wide ? tiles_of(swiglu ? 128 : 256) : tiles_of(swiglu ? 64 : 128));
     if (items > INT32_MAX / 2) return bq::fail(BQ_ERR_SHAPE, "%s: %d rows x %d columns are too many", name, rows, cols);
     bq_status s = bq::check_arch();
     if (s != BQ_OK) return s;
     const bq::WaitProbe probe = bq::wait_probe();
     const Args a{xscales, rows, offsets, E, wscales, n, k, (k + kBlock - 1) / kBlock, (n + kBlock - 1) / kBlock, cols,
-                 y, ydtype, ldy, bq::device_status_ptr(), probe.limit_ns, probe.skip_weight_copies,
-                 (int)chunks};
-    int split = 1;
-    while (split < kMaxCluster && items * split * 2 <= kSms && a.kb >= 4 * split) split *= 2;
+                 y, ydtype, ldy, bq::device_status_ptr(), probe.limit_ns, probe.skip_weight_copies, (int)chunks};
     CUtensorMap map_w, map_x;
-    if (!weight_map(&map_w, w, E, n, k, swiglu) || !row_map(&map_x, x, rows, k, nt == 32 ? 16 : 32))
+    if (!weight_map(&map_w, w, E, n, k, swiglu && !wide) || !row_map(&map_x, x, rows, k, !wide && nt == 32 ? 16 : 32))
         return bq::fail(BQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", name);
     cudaError_t e;
-    if (swiglu) {
-        e = nt == 32 ? launch_lanes<32, true>(map_w, map_x, a, items, split, st)
-          : nt == 64 ? launch_lanes<64, true>(map_w, map_x, a, items, split, st)
-                     : launch_lanes<128, true>(map_w, map_x, a, items, split, st);
+    if (wide) {
+        e = swiglu ? launch_wide<true>(map_w, map_x, a, items, st) : launch_wide<false>(map_w, map_x, a, items, st);
     } else {
-        e = nt == 32 ? launch_lanes<32, false>(map_w, map_x, a, items, split, st)
-          : nt == 64 ? launch_lanes<64, false>(map_w, map_x, a, items, split, st)
-                     : launch_lanes<128, false>(map_w, map_x, a, items, split, st);
+        int split = 1;
+        while (split < kMaxCluster && items * split * 2 <= kSms && a.kb >= 4 * split) split *= 2;
+        auto go = [&](auto width) {
+            constexpr int NT = decltype(width)::value;
+            return swiglu ? launch_lanes<NT, true>(map_w, map_x, a, items, split, st)
+                          : launch_lanes<NT, false>(map_w, map_x, a, items, split, st);
+        };
+        e = nt == 32 ? go(std::integral_constant<int, 32>()) : nt == 64 ? go(std::integral_constant<int, 64>())
+                                                                          : go(std::integral_constant<int, 128>());
     }
     if (e != cudaSuccess) return bq::fail(BQ_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
     bq::note_launch();
