@@ -11,7 +11,6 @@
 // on the next blocks.
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "gemm_internal.cuh"
 #include "row_types.cuh"
@@ -77,6 +76,50 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
         ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
+// One lane of a converged warp.  A warp that runs its loop as a whole and lets one lane issue keeps addresses and
+// descriptors in uniform registers, which the MMA and TMA instructions take them from.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
+// Bounded wait of a converged warp for a phase of each of two barriers, tested together (one test latency instead of
+// two); false if the CTA is aborting or the wait ran out.
+__device__ __forceinline__ bool warp_wait_both(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
+                                               volatile uint32_t* abort_flag, int32_t* status,
+                                               unsigned long long limit_ns) {
+    unsigned long long t0 = 0;
+    for (int i = 1;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p, q;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n and.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok) : "r"(bar0), "r"(parity0), "r"(bar1), "r"(parity1) : "memory");
+        if (__all_sync(0xffffffffu, ok != 0)) return true;
+        if (i % 32 == 0) {
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+            const unsigned long long t = __shfl_sync(0xffffffffu, global_ns(), 0);
+            if (t0 == 0) t0 = t;
+            if (t - t0 > limit_ns) {
+                *abort_flag = 1u;
+                bq::set_device_error(status, BQ_DEV_WAIT_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
+// Waits for this warp's TMEM loads; the values pass through so that no use of them moves before the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 ::"memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -97,9 +140,8 @@ __device__ __forceinline__ float peer_load(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.f + expf(-g)); }
 
 // ---------------------------------------------------------------- work items
-// The row chunks of every expert: s_tiles[e] = chunks of the experts before e,
-// s_tiles[E] their total.  A chunk is at most `most` rows; an expert's rows are
-// cut into chunks of near-equal size.
+// The row chunks of every expert: a chunk is at most `most` rows, an expert's
+// rows are cut into chunks of near-equal size.
 __device__ __forceinline__ int chunks_of(const Args& a, int e, int most) {
     const int lo = __ldg(a.offsets + e), hi = __ldg(a.offsets + e + 1);
     if (!(0 <= lo && lo <= hi && hi <= a.rows)) {
@@ -109,12 +151,21 @@ __device__ __forceinline__ int chunks_of(const Args& a, int e, int most) {
     return (hi - lo + most - 1) / most;
 }
 
-// Fills s_tiles (all threads of the CTA; ends with a barrier).
-__device__ __forceinline__ void count_chunks(const Args& a, int most, int32_t* s_tiles) {
+// What the CTA keeps of it in shared memory.
+struct Chunks {
+    int32_t before[kMaxExperts + 1];   // [e]: chunks of the experts before e, [E]: of all
+    int32_t first[kMaxExperts + 1];    // [e]: first row of expert e, [E]: end of the last
+    int32_t pad[2];                    // to a multiple of 16 bytes
+};
+static_assert(sizeof(Chunks) % 16 == 0, "what lies behind it is 16-byte aligned");
+
+// Fills it (all threads of the CTA; ends with a barrier).
+__device__ __forceinline__ void count_chunks(const Args& a, int most, Chunks* ch) {
     if (!a.offsets) {
         if (threadIdx.x == 0) {
-            s_tiles[0] = 0;
-            s_tiles[1] = (a.rows + most - 1) / most;
+            ch->before[0] = ch->first[0] = 0;
+            ch->before[1] = (a.rows + most - 1) / most;
+            ch->first[1] = a.rows;
         }
     } else if (threadIdx.x < 32) {
         // one warp: 32 experts at a time, all loads of a group of four issued together
@@ -125,6 +176,7 @@ __device__ __forceinline__ void count_chunks(const Args& a, int most, int32_t* s
             for (int i = 0; i < 4; ++i) {
                 const int e = e0 + 32 * i + (int)threadIdx.x;
                 c[i] = e < a.E ? chunks_of(a, e, most) : 0;
+                if (e <= a.E) ch->first[e] = __ldg(a.offsets + e);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -135,11 +187,14 @@ __device__ __forceinline__ void count_chunks(const Args& a, int most, int32_t* s
                     const int v = __shfl_up_sync(0xffffffffu, incl, off);
                     if ((int)threadIdx.x >= off) incl += v;
                 }
-                if (e < a.E) s_tiles[e] = total + incl - c[i];
+                if (e < a.E) ch->before[e] = total + incl - c[i];
                 total += __shfl_sync(0xffffffffu, incl, 31);
             }
         }
-        if (threadIdx.x == 0) s_tiles[a.E] = total;
+        if (threadIdx.x == 0) {
+            ch->before[a.E] = total;
+            ch->first[a.E] = __ldg(a.offsets + a.E);
+        }
     }
     __syncthreads();
 }
@@ -151,80 +206,99 @@ struct Item {
     int rows;    // its rows
 };
 
-// Item i: experts in order, their weight tiles, then the chunks of rows that
-// share such a tile (so that a tile's second reader finds it in the L2).
-__device__ __forceinline__ Item find_item(const Args& a, const int32_t* s_tiles, int w_tiles, int i) {
-    Item it;
-    int lo = 0, hi = a.E - 1;   // the last expert with s_tiles[e] * w_tiles <= i
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)s_tiles[mid] * w_tiles <= i) lo = mid; else hi = mid - 1;
+// A CTA's items i = first, first + step, ... of `count`: experts in order,
+// their weight tiles, then the chunks of rows that share such a tile (so that
+// a tile's second reader finds it in the L2).  A whole warp steps through them;
+// i is kept as chunk * w_tiles + rest, and the expert is found in two ballots
+// (a serial search and its loads held every role up for 1000 cycles an item,
+// which small K did not hide).
+struct Items {
+    int i, count, step, w_tiles, chunk, rest, d_chunk, d_rest;
+
+    __device__ __forceinline__ Items(int first, int step_, int count_, int w_tiles_)
+        : i(first), count(count_), step(step_), w_tiles(w_tiles_), chunk(first / w_tiles_), rest(first % w_tiles_),
+          d_chunk(step_ / w_tiles_), d_rest(step_ % w_tiles_) {}
+    __device__ __forceinline__ bool more() const { return i < count; }
+    __device__ __forceinline__ void next() {
+        i += step;
+        chunk += d_chunk;
+        rest += d_rest;
+        if (rest >= w_tiles) { rest -= w_tiles; ++chunk; }
     }
-    it.e = lo;
-    const int chunks = s_tiles[lo + 1] - s_tiles[lo], local = i - s_tiles[lo] * w_tiles;
-    it.tile = local / chunks;
-    const int c = local - it.tile * chunks;
-    const int first = a.offsets ? __ldg(a.offsets + lo) : 0;
-    const int count = (a.offsets ? __ldg(a.offsets + lo + 1) : a.rows) - first;
-    const int size = (count + chunks - 1) / chunks;
-    it.row0 = first + c * size;
-    it.rows = min(size, count - c * size);
-    return it;
-}
+    __device__ __forceinline__ Item get(const Chunks* ch, int E) const {
+        const int lane = threadIdx.x & 31;
+        // the last expert with before[e] <= chunk: its group of 32, then itself
+        const int g = __popc(__ballot_sync(0xffffffffu, 32 * lane < E && ch->before[min(32 * lane, E)] <= chunk)) - 1;
+        const int at = 32 * g + lane;
+        const int e = 32 * g + __popc(__ballot_sync(0xffffffffu, at < E && ch->before[min(at, E)] <= chunk)) - 1;
+        Item it;
+        it.e = e;
+        it.row0 = ch->first[e];
+        it.rows = ch->first[e + 1] - it.row0;
+        it.tile = rest;
+        const int before = ch->before[e], chunks = ch->before[e + 1] - before;
+        if (chunks > 1) {   // chunks of near-equal size, fastest
+            const int local = (chunk - before) * w_tiles + rest, size = (it.rows + chunks - 1) / chunks;
+            it.tile = local / chunks;
+            const int skip = (local - it.tile * chunks) * size;
+            it.row0 += skip;
+            it.rows = min(size, it.rows - skip);
+        }
+        return it;
+    }
+};
 
 // ---------------------------------------------------------------- weights on the lanes
 //
-// Tile = 128 weight rows (MMA M, TMEM lanes) x up to NT rows of x (MMA N,
-// TMEM columns).  For few rows the time is that of reading the weights once:
-// they go from HBM to shared memory by TMA and from there into the tensor
-// cores, through no register, and the N side costs nothing where it is short.
-// With SwiGLU a tile holds 64 gate rows and their 64 up rows, 16 + 16 in each
-// lane quarter, so that a gate value and its up value are 16 lanes apart.
+// Tile = 128 weight rows (MMA M, TMEM lanes) x up to 32 rows of x (MMA N, TMEM
+// columns).  For few rows the time is that of reading the weights once: they
+// go from HBM to shared memory by TMA and from there into the tensor cores,
+// through no register, and the N side costs nothing where it is short.  With
+// SwiGLU a tile holds 64 gate rows and their 64 up rows, 16 + 16 in each lane
+// quarter, so that a gate value and its up value are 16 lanes apart.
 //
 // 224 threads, one CTA per SM, persistent over the items:
 //   warp 0     TMA producer: 128 x 128 bytes of weights and the rows' 128
-//              bytes into a ring of S stages (one stage = one block of K);
-//   warp 1     owns the TMEM, issues the MMAs of a stage into the next slot of
-//              the accumulator ring;
-//   warp 2     copies the slot's scales (xs of every row, ws) into the ring;
+//              bytes into a ring of 10 stages (one stage = one block of K);
+//   warp 1     owns the TMEM, issues the MMAs of a stage into the next of 8
+//              accumulator slots;
+//   warp 2     copies the slot's scales (xs of every row, ws) beside it;
 //   warps 3-6  add slot by slot to their sums, then write y.
 // With few items K is split over a cluster: the CTAs leave their sums in
 // shared memory and each finishes a share of the rows, in rank order.
-template <int NT> struct Lanes;
-template <> struct Lanes<32>  { static constexpr int S = 10, A = 8, BOX = 16; };
-template <> struct Lanes<64>  { static constexpr int S = 8,  A = 8, BOX = 32; };
-template <> struct Lanes<128> { static constexpr int S = 6,  A = 4, BOX = 32; };
-
+//
+// Measured: up to 48 of 256 experts with a row or two each, 4096 x 2048: 63.5
+// us, 5.9 TB/s (loops run by one lane 79.1; a serial search for each item's
+// expert 66.4); one row x 4096 x 4096 5.5 us (6.5), of which the weights take
+// 2.5: launch, first loads and the cluster's two barriers are the rest.
+constexpr int kLaneRows = 32;      // rows of x in a tile (the columns of a TMEM slot)
 constexpr int kLaneThreads = 224;
 
-template <int NT>
 struct LaneSmem {
-    using L = Lanes<NT>;
+    static constexpr int S = 10, A = 8, BOX = 16;                 // stages, TMEM slots, rows of a box
     static constexpr int kWBytes = kBlock * 128;
-    static constexpr int kStage = kWBytes + NT * 128;
-    static constexpr int kScaleSlot = NT + 4;                     // xs of the rows, ws of gate and up
-    static constexpr int kScales = L::S * kStage;
-    static constexpr int kTiles = kScales + L::A * kScaleSlot * 4;
-    static constexpr int kBars = kTiles + (kMaxExperts + 2) * 4;
-    static constexpr int kNumBars = 2 * L::S + 3 * L::A + 1;
+    static constexpr int kStage = kWBytes + kLaneRows * 128;
+    static constexpr int kScaleSlot = kLaneRows + 4;              // xs of the rows, ws of gate and up
+    static constexpr int kScales = S * kStage;
+    static constexpr int kTiles = kScales + A * kScaleSlot * 4;
+    static constexpr int kBars = kTiles + (int)sizeof(Chunks);
+    static constexpr int kNumBars = 2 * S + 3 * A + 1;
     static constexpr int kBytes = 1024 + kBars + 8 * kNumBars + 16;
 };
-static_assert(LaneSmem<32>::kBytes <= 232448 && LaneSmem<64>::kBytes <= 232448 && LaneSmem<128>::kBytes <= 232448, "smem");
-static_assert(LaneSmem<32>::kBars % 8 == 0 && LaneSmem<64>::kBars % 8 == 0 && LaneSmem<128>::kBars % 8 == 0, "bars");
+static_assert(LaneSmem::kBytes <= 232448 && LaneSmem::kTiles % 16 == 0, "smem");
 
-template <int NT, bool SWIGLU>
+template <bool SWIGLU>
 __global__ void __launch_bounds__(kLaneThreads, 1)
 mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a,
                 int split) {
-    using L = Lanes<NT>;
-    using M = LaneSmem<NT>;
-    constexpr int S = L::S, A = L::A;
+    using M = LaneSmem;
+    constexpr int S = M::S, A = M::A, NT = kLaneRows;
     constexpr uint32_t kCols = NT * A;
-    static_assert(kCols == 256 || kCols == 512, "TMEM columns");
+    static_assert(kCols == 256, "TMEM columns");
     extern __shared__ uint8_t smem_dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     float* scales = reinterpret_cast<float*>(smem + M::kScales);
-    int32_t* s_tiles = reinterpret_cast<int32_t*>(smem + M::kTiles);
+    Chunks* chunks = reinterpret_cast<Chunks*>(smem + M::kTiles);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::kBars);
     const uint32_t bar0 = smem_u32(bars), ring = smem_u32(smem);
     auto full = [&](int s) { return bar0 + 8u * s; };
@@ -239,7 +313,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) { mbar_init(full(i), 1); mbar_init(empty(i), 1); }
-        for (int i = 0; i < A; ++i) { mbar_init(acc_full(i), 1); mbar_init(acc_empty(i), 128); mbar_init(sc_full(i), 32); }
+        for (int i = 0; i < A; ++i) { mbar_init(acc_full(i), 1); mbar_init(acc_empty(i), 4); mbar_init(sc_full(i), 32); }
         mbar_init(drain, 1);
         *abort_flag = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -252,7 +326,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     // launched behind whatever precedes it on the stream: nothing before this line touches global memory
     bq::grid_dependency_wait();
     bq::allow_dependents();
-    count_chunks(a, NT, s_tiles);
+    count_chunks(a, 32, chunks);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -260,24 +334,26 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
 
     constexpr int kTileCols = SWIGLU ? 64 : 128;
     const int w_tiles = (a.cols + kTileCols - 1) / kTileCols;
-    const int64_t items = (int64_t)min(s_tiles[a.E], a.max_chunks) * w_tiles;
+    const int items = min(chunks->before[a.E], a.max_chunks) * w_tiles;   // the host made sure that it is an int
     const int rank = split > 1 ? (int)cluster_rank() : 0;
     const int first = blockIdx.x / split, step = gridDim.x / split;
     const int b0 = a.kb * rank / split, b1 = a.kb * (rank + 1) / split;
     const unsigned long long limit = a.wait_limit_ns;
 
+    const bool one = elect_one();
+    bool ok = !a.skip_copies;
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0, issued = 0;
-            uint32_t ph = 0;
-            bool ok = !a.skip_copies;
-            for (int64_t i = first; ok && i < items; i += step) {
-                const Item it = find_item(a, s_tiles, w_tiles, (int)i);
-                const int boxes = (it.rows + L::BOX - 1) / L::BOX;
-                for (int b = b0; b < b1; ++b) {
-                    if (issued >= S && !(ok = mbar_wait(empty(s), ph ^ 1u, abort_flag, a.status, limit))) break;
+        int s = 0, issued = 0;
+        uint32_t ph = 1;   // a fresh barrier passes for the phase before its first
+        for (Items i(first, step, items, w_tiles); ok && i.more(); i.next()) {
+            const Item it = i.get(chunks, a.E);
+            const int boxes = (it.rows + M::BOX - 1) / M::BOX;
+            const uint32_t bytes = M::kWBytes + boxes * M::BOX * 128;
+            for (int b = b0; b < b1; ++b) {
+                if (!(ok = warp_wait_all(empty(s), ph, abort_flag, a.status, limit))) break;
+                if (one) {
                     const uint32_t dst = ring + s * M::kStage;
-                    mbar_expect_tx(full(s), M::kWBytes + boxes * L::BOX * 128);
+                    mbar_expect_tx(full(s), bytes);
                     if (SWIGLU) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
@@ -286,102 +362,97 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                         tma_load_3d(dst, &map_w, b * kBlock, 128 * it.tile, it.e, full(s));
                     }
                     for (int q = 0; q < boxes; ++q)
-                        tma_load_2d(dst + M::kWBytes + q * L::BOX * 128, &map_x, b * kBlock, it.row0 + q * L::BOX, full(s));
-                    ++issued;
-                    if (++s == S) { s = 0; ph ^= 1u; }
+                        tma_load_2d(dst + M::kWBytes + q * M::BOX * 128, &map_x, b * kBlock, it.row0 + q * M::BOX, full(s));
                 }
-            }
-            if (!ok) {   // let our own copies land before the CTA leaves (bounded)
-                volatile uint32_t no_abort = 0;
-                for (int u = max(0, issued - S); u < issued; ++u)
-                    mbar_wait(full(u % S), (u / S) & 1, &no_abort, a.status, limit);
+                ++issued;
+                if (++s == S) { s = 0; ph ^= 1u; }
             }
         }
+        if (!ok) {   // copies in flight land before the CTA leaves (bounded)
+            volatile uint32_t no_abort = 0;
+            for (int u = max(0, issued - S); u < issued; ++u)
+                mbar_wait(full(u % S), (u / S) & 1, &no_abort, a.status, limit);
+        }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int s = 0, q = 0;
-            uint32_t ph = 0, aph = 0;
-            bool ok = true, wrapped = false;
-            for (int64_t i = first; ok && i < items; i += step) {
-                const Item it = find_item(a, s_tiles, w_tiles, (int)i);
-                const uint32_t idesc = idesc_e4m3((it.rows + 15) & ~15);
-                for (int b = b0; b < b1; ++b) {
-                    if (wrapped && !(ok = mbar_wait(acc_empty(q), aph ^ 1u, abort_flag, a.status, limit))) break;
-                    if (!(ok = mbar_wait(full(s), ph, abort_flag, a.status, limit))) break;
-                    tc_fence_after();
-                    const uint64_t wd = smem_desc_sw128(ring + s * M::kStage);
-                    const uint64_t xd = smem_desc_sw128(ring + s * M::kStage + M::kWBytes);
+        const uint64_t wd0 = smem_desc_sw128(ring), xd0 = smem_desc_sw128(ring + M::kWBytes);
+        int s = 0, q = 0;
+        uint32_t ph = 0, aph = 1;
+        ok = true;
+        for (Items i(first, step, items, w_tiles); ok && i.more(); i.next()) {
+            const Item it = i.get(chunks, a.E);
+            const uint32_t idesc = idesc_e4m3((it.rows + 15) & ~15);
+            for (int b = b0; b < b1; ++b) {
+                if (!(ok = warp_wait_both(full(s), ph, acc_empty(q), aph, abort_flag, a.status, limit))) break;
+                tc_fence_after();
+                if (one) {
+                    const uint32_t stage = s * (M::kStage >> 4);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)     // +32 bytes along K
-                        mma_e4m3(tmem + q * NT, wd + 2 * j, xd + 2 * j, idesc, j != 0);
-                    mma_commit(empty(s));
+                        mma_e4m3(tmem + q * NT, wd0 + stage + 2 * j, xd0 + stage + 2 * j, idesc, j != 0);
                     mma_commit(acc_full(q));
-                    if (++s == S) { s = 0; ph ^= 1u; }
-                    if (++q == A) { q = 0; aph ^= 1u; wrapped = true; }
+                    mma_commit(empty(s));
                 }
+                __syncwarp();
+                if (++s == S) { s = 0; ph ^= 1u; }
+                if (++q == A) { q = 0; aph ^= 1u; }
             }
-            if (!ok) {   // our MMAs end before the TMEM is freed (bounded)
-                volatile uint32_t no_abort = 0;
-                mma_commit(drain);
-                mbar_wait(drain, 0, &no_abort, a.status, limit);
-            }
+        }
+        if (!ok && one) {   // our MMAs end before the TMEM is freed (bounded)
+            volatile uint32_t no_abort = 0;
+            mma_commit(drain);
+            mbar_wait(drain, 0, &no_abort, a.status, limit);
         }
     } else if (warp == 2) {
         int q = 0;
-        uint32_t aph = 0;
-        bool ok = true, wrapped = false;
-        for (int64_t i = first; ok && i < items; i += step) {
-            const Item it = find_item(a, s_tiles, w_tiles, (int)i);
+        uint32_t aph = 1;
+        ok = true;
+        for (Items i(first, step, items, w_tiles); ok && i.more(); i.next()) {
+            const Item it = i.get(chunks, a.E);
             const float* xs = a.xs + (int64_t)it.row0 * a.kb;
             // weight rows 128 tile.. are scale row `tile`; of a gate/up weight, gate rows 64 tile.. are scale row
             // tile / 2 and their up rows n/2 further on
             const int wrow = lane == 0 ? (SWIGLU ? it.tile / 2 : it.tile) : it.tile / 2 + a.nb / 2;
             const float* ws = a.ws + ((int64_t)it.e * a.nb + wrow) * a.kb;
             for (int b = b0; b < b1; ++b) {
-                if (wrapped && !(ok = warp_wait_all(acc_empty(q), aph ^ 1u, abort_flag, a.status, limit))) break;
+                if (!(ok = warp_wait_all(acc_empty(q), aph, abort_flag, a.status, limit))) break;
                 const uint32_t dst = smem_u32(scales + q * M::kScaleSlot);
-                for (int r = lane; r < it.rows; r += 32) copy4_async(dst + 4 * r, xs + (int64_t)r * a.kb + b);
+                if (lane < it.rows) copy4_async(dst + 4 * lane, xs + lane * a.kb + b);
                 if (lane < (SWIGLU ? 2 : 1)) copy4_async(dst + 4 * (NT + lane), ws + b);
                 copies_arrive(sc_full(q));
-                if (++q == A) { q = 0; aph ^= 1u; wrapped = true; }
+                if (++q == A) { q = 0; aph ^= 1u; }
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         const int quarter = warp & 3, p = 32 * quarter + lane;
-        const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
+        const uint32_t base = tmem + ((uint32_t)(32 * quarter) << 16);
         int q = 0;
         uint32_t aph = 0;
-        bool ok = true;
-        for (int64_t i = first; ok && i < items; i += step) {
-            const Item it = find_item(a, s_tiles, w_tiles, (int)i);
+        ok = true;
+        for (Items i(first, step, items, w_tiles); ok && i.more(); i.next()) {
+            const Item it = i.get(chunks, a.E);
             float acc[NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[t] = 0.f;
             for (int b = b0; b < b1; ++b) {
-                if (!(ok = warp_wait_all(sc_full(q), aph, abort_flag, a.status, limit))) break;
-                if (!(ok = warp_wait_all(acc_full(q), aph, abort_flag, a.status, limit))) break;
+                if (!(ok = warp_wait_both(sc_full(q), aph, acc_full(q), aph, abort_flag, a.status, limit))) break;
                 tc_fence_after();
                 const float* sc = scales + q * M::kScaleSlot;
+                uint32_t v[32];
+                tmem_ld32(base + q * NT, v);
                 const float ws = sc[NT + (SWIGLU ? (lane >> 4) : 0)];
+                float x[NT];
 #pragma unroll
-                for (int c = 0; c < NT; c += 32) {
-                    if (c < it.rows) {
-                        uint32_t v[32];
-                        tmem_ld32(tmem + lane_base + q * NT + c, v);
-                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 x4 = *reinterpret_cast<const float4*>(sc + c + j);
-                            acc[c + j] = __fmaf_rn(__uint_as_float(v[j]), x4.x * ws, acc[c + j]);
-                            acc[c + j + 1] = __fmaf_rn(__uint_as_float(v[j + 1]), x4.y * ws, acc[c + j + 1]);
-                            acc[c + j + 2] = __fmaf_rn(__uint_as_float(v[j + 2]), x4.z * ws, acc[c + j + 2]);
-                            acc[c + j + 3] = __fmaf_rn(__uint_as_float(v[j + 3]), x4.w * ws, acc[c + j + 3]);
-                        }
-                    }
+                for (int j = 0; j < NT; j += 4) {
+                    const float4 x4 = *reinterpret_cast<const float4*>(sc + j);
+                    x[j] = x4.x * ws; x[j + 1] = x4.y * ws; x[j + 2] = x4.z * ws; x[j + 3] = x4.w * ws;
                 }
+                tmem_wait_ld(v);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) acc[j] = __fmaf_rn(__uint_as_float(v[j]), x[j], acc[j]);
                 tc_fence_before();
-                mbar_arrive(acc_empty(q));
+                __syncwarp();
+                if (one) mbar_arrive(acc_empty(q));
                 if (++q == A) { q = 0; aph ^= 1u; }
             }
             if (!ok) break;
@@ -417,7 +488,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         cluster_sync();
         if (warp >= 3 && first < items && !*abort_flag) {
             const int quarter = warp & 3, p = 32 * quarter + lane;
-            const Item it = find_item(a, s_tiles, w_tiles, first);
+            const Item it = Items(first, step, items, w_tiles).get(chunks, a.E);
             const int c = SWIGLU ? 64 * it.tile + 16 * quarter + (lane & 15) : 128 * it.tile + p;
             for (int t = rank; t < it.rows; t += split) {
                 float part[kMaxCluster];
@@ -448,62 +519,65 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
 
 // ---------------------------------------------------------------- rows on the lanes
 //
-// Tile = 128 rows of x (MMA M, TMEM lanes) x 256 weight rows (MMA N, TMEM
-// columns), for many rows: there the tensor cores bound it, and with the rows
-// on the lanes a block's scale is one number per thread and column half, so
-// that adding a block costs one packed multiply-add per two values (against a
-// scale fetched per column above).  With SwiGLU the columns are 128 gate rows
-// and their 128 up rows, and a thread holds both of each.
+// For many rows the tensor cores bound it.  With the rows of x on the lanes a
+// block's scale is one number per thread and scale block, so adding a block
+// costs one multiply-add per value and nothing else (against a scale fetched
+// per column above).  Tile = up to 128 rows of x (MMA M, TMEM lanes) x 256
+// weight rows (TMEM columns).
 //
-// 320 threads, one CTA per SM, persistent over the items:
-//   warp 0     TMA producer: 128 bytes of 128 rows and of 256 weight rows into
-//              a ring of 4 stages (48 KB each);
-//   warp 1     owns the TMEM (two slots of 256 columns), issues the MMAs;
-//   warps 2-9  one thread per row and column half: 128 fp32 sums in registers,
-//              scales read one block ahead, then y.
-constexpr int kWideThreads = 320;
+// A slot of TMEM is busy from its MMAs through the commit, the epilogue's
+// loads and the word back to the issuer.  There is room for two slots of 256
+// columns, so the tile's two halves of 128 columns (MMA N) are pipelines of
+// their own, with an issuing warp, two slots and four epilogue warps each: one
+// half's MMAs run while the other's slots change hands.  With SwiGLU each half
+// is 64 gate rows and their 64 up rows, and a thread holds both.
+//
+// 384 threads, one CTA per SM, persistent over the items:
+//   warp 0      TMA producer: 128 bytes of 128 rows and of 256 weight rows into
+//               a ring of 4 stages (48 KB each);
+//   warps 1-2   issue the MMAs of a half; warp 1 owns the TMEM;
+//   warp 3      idle (warpgroups give and take registers as a whole);
+//   warps 4-11  one thread per row and half: 128 fp32 sums in registers, then
+//               y.  They take the registers that the first warpgroup gives up:
+//               with fewer the sums spill, which made a block 2.4 times as
+//               long.
+// The MMAs of a block take 512 cycles; what bounds it is the instructions
+// around them, at two epilogue warps per scheduler (256 cycles of multiply-adds
+// a block).  Measured at 2048 x 4096 x 4096, each step on the one before: sums
+// not spilling 59.8 -> 37.7 us; loops that a whole warp runs with one lane
+// issuing, both barriers of a block tested together, plain instead of packed
+// multiply-adds (packed ones cost moves that pair the loaded registers) 37.7 ->
+// 37.3; a block's wait and first load before the last sums of the block before
+// it, scales loaded two blocks ahead 37.3 -> 30.7 (2.2 PFLOP/s; 8192 rows 2.7).
+// A pair of CTAs sharing the weight rows (cta_group::2) fills a third less
+// shared memory per block and took the same time (30.4; 8192 rows 103.6
+// against 101.4), so there is none.
+constexpr int kWideThreads = 384;
+constexpr int kWideRegs = 224, kControlRegs = 56;   // 256 * 224 + 128 * 56 = 384 * 168, what the launch holds
+static_assert(256 * kWideRegs + 128 * kControlRegs <= kWideThreads * 168, "registers");
 
 struct WideSmem {
-    static constexpr int S = 4, A = 2, N = 256;
+    static constexpr int S = 4, A = 2;                              // stages; slots of a half
     static constexpr int kXBytes = 128 * 128;
-    static constexpr int kStage = kXBytes + N * 128;
+    static constexpr int kHalfBytes = 128 * 128;                    // weight rows of a half
+    static constexpr int kStage = kXBytes + 2 * kHalfBytes;
     static constexpr int kTiles = S * kStage;
-    static constexpr int kBars = kTiles + (kMaxExperts + 2) * 4;
-    static constexpr int kNumBars = 2 * S + 2 * A + 1;
+    static constexpr int kBars = kTiles + (int)sizeof(Chunks);      // 16-byte aligned: the slots' barriers differ in bit 3
+    static constexpr int kNumBars = 2 * S + 4 * A + 1;
     static constexpr int kBytes = 1024 + kBars + 8 * kNumBars + 16;
 };
-static_assert(WideSmem::kBytes <= 232448 && WideSmem::kBars % 8 == 0, "smem");
+static_assert(WideSmem::kBytes <= 232448 && WideSmem::kBars % 16 == 0 && WideSmem::S % 2 == 0, "smem");
 
-// Waits for this warp's TMEM loads; the values pass through so that no use of them moves before the wait.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
-                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
-                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
-                 ::"memory");
+// A load that stays where it is written (the compiler would move it to its use, a block later, and wait there).
+__device__ __forceinline__ float load_early(const float* p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
 }
 
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-    return f;
-}
-
-// acc[i] += v[2i, 2i+1] * s, sixteen pairs
-__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&v)[32], uint64_t s) {
+__device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&v)[32], float f) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        uint64_t x;
-        asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(v[2 * i]), "r"(v[2 * i + 1]));
-        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i]) : "l"(x), "l"(s));
-    }
+    for (int i = 0; i < 32; ++i) acc[i] = __fmaf_rn(__uint_as_float(v[i]), f, acc[i]);
 }
 
 __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
@@ -547,25 +621,25 @@ template <bool SWIGLU>
 __global__ void __launch_bounds__(kWideThreads, 1)
 mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a) {
     using M = WideSmem;
-    constexpr int S = M::S, A = M::A, N = M::N, kTileCols = SWIGLU ? 128 : 256;
+    constexpr int S = M::S, A = M::A, kTileCols = SWIGLU ? 128 : 256;
     extern __shared__ uint8_t smem_dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
-    int32_t* s_tiles = reinterpret_cast<int32_t*>(smem + M::kTiles);
+    Chunks* chunks = reinterpret_cast<Chunks*>(smem + M::kTiles);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::kBars);
     const uint32_t bar0 = smem_u32(bars), ring = smem_u32(smem);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (S + s); };
-    auto acc_full = [&](int q) { return bar0 + 8u * (2 * S + q); };
-    auto acc_empty = [&](int q) { return bar0 + 8u * (2 * S + A + q); };
-    const uint32_t drain = bar0 + 8u * (2 * S + 2 * A);
+    auto acc_full = [&](int half, int q) { return bar0 + 8u * (2 * S + A * half + q); };
+    auto acc_empty = [&](int half, int q) { return bar0 + 8u * (2 * S + A * (2 + half) + q); };
+    const uint32_t drain = bar0 + 8u * (2 * S + 4 * A);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + M::kNumBars);
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S; ++i) { mbar_init(full(i), 1); mbar_init(empty(i), 1); }
-        for (int i = 0; i < A; ++i) { mbar_init(acc_full(i), 1); mbar_init(acc_empty(i), 256); }
-        mbar_init(drain, 1);
+        for (int i = 0; i < S; ++i) { mbar_init(full(i), 1); mbar_init(empty(i), 2); }
+        for (int i = 0; i < 2 * A; ++i) { mbar_init(acc_full(0, i), 1); mbar_init(acc_empty(0, i), 4); }
+        mbar_init(drain, 2);
         *abort_flag = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -577,136 +651,167 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     // launched behind whatever precedes it on the stream: nothing before this line touches global memory
     bq::grid_dependency_wait();
     bq::allow_dependents();
-    count_chunks(a, 128, s_tiles);
+    count_chunks(a, 128, chunks);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int w_tiles = (a.cols + kTileCols - 1) / kTileCols;
-    const int64_t items = (int64_t)min(s_tiles[a.E], a.max_chunks) * w_tiles;
-    const unsigned long long limit = a.wait_limit_ns;
+    const int items = min(chunks->before[a.E], a.max_chunks) * w_tiles;   // the host made sure that it is an int
+    const int first = blockIdx.x, step = gridDim.x;
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+        const bool one = elect_one();
+        bool ok = !a.skip_copies;
+        if (warp == 0) {
             int s = 0, issued = 0;
-            uint32_t ph = 0;
-            bool ok = !a.skip_copies;
-            for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-                const Item it = find_item(a, s_tiles, w_tiles, (int)i);
-                const int boxes = (it.rows + 31) / 32;
-                // the two boxes of 128 weight rows
-                const int w0 = kTileCols * it.tile, w1 = SWIGLU ? a.n / 2 + w0 : w0 + 128;
+            uint32_t ph = 1;   // a fresh barrier passes for the phase before its first
+            for (Items i(first, step, items, w_tiles); ok && i.more(); i.next()) {
+                const Item it = i.get(chunks, a.E);
+                const int w_row = kTileCols * it.tile;
                 for (int b = 0; b < a.kb; ++b) {
-                    if (issued >= S && !(ok = mbar_wait(empty(s), ph ^ 1u, abort_flag, a.status, limit))) break;
-                    const uint32_t dst = ring + s * M::kStage;
-                    mbar_expect_tx(full(s), boxes * 4096 + N * 128);
-                    for (int q = 0; q < boxes; ++q)
-                        tma_load_2d(dst + q * 4096, &map_x, b * kBlock, it.row0 + 32 * q, full(s));
-                    tma_load_3d(dst + M::kXBytes, &map_w, b * kBlock, w0, it.e, full(s));
-                    tma_load_3d(dst + M::kXBytes + 16384, &map_w, b * kBlock, w1, it.e, full(s));
+                    if (!(ok = warp_wait_all(empty(s), ph, abort_flag, a.status, a.wait_limit_ns))) break;
+                    if (one) {
+                        const uint32_t dst = ring + s * M::kStage;
+                        mbar_expect_tx(full(s), M::kStage);
+                        tma_load_2d(dst, &map_x, b * kBlock, it.row0, full(s));
+                        for (int h = 0; h < 2; ++h) {
+                            if (SWIGLU)   // 64 gate rows and their 64 up rows
+                                tma_load_4d(dst + M::kXBytes + h * M::kHalfBytes, &map_w, b * kBlock, w_row + 64 * h, 0, it.e,
+                                            full(s));
+                            else
+                                tma_load_3d(dst + M::kXBytes + h * M::kHalfBytes, &map_w, b * kBlock, w_row + 128 * h, it.e,
+                                            full(s));
+                        }
+                    }
                     ++issued;
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
             }
-            if (!ok) {   // let our own copies land before the CTA leaves (bounded)
+            if (!ok) {   // copies in flight land before the CTA leaves (bounded)
                 volatile uint32_t no_abort = 0;
                 for (int u = max(0, issued - S); u < issued; ++u)
-                    mbar_wait(full(u % S), (u / S) & 1, &no_abort, a.status, limit);
+                    mbar_wait(full(u % S), (u / S) & 1, &no_abort, a.status, a.wait_limit_ns);
             }
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_e4m3(N);
-            int s = 0, q = 0;
-            uint32_t ph = 0, aph = 0;
-            bool ok = true, wrapped = false;
-            for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-                for (int b = 0; b < a.kb; ++b) {
-                    if (wrapped && !(ok = mbar_wait(acc_empty(q), aph ^ 1u, abort_flag, a.status, limit))) break;
-                    if (!(ok = mbar_wait(full(s), ph, abort_flag, a.status, limit))) break;
-                    tc_fence_after();
-                    const uint64_t xd = smem_desc_sw128(ring + s * M::kStage);
-                    const uint64_t wd = smem_desc_sw128(ring + s * M::kStage + M::kXBytes);
+        } else if (warp < 3) {
+            // Lean: what one warp does per block, in order, bounds the MMA rate.
+            const int half = warp - 1;
+            const uint32_t idesc = idesc_e4m3(128);
+            const uint64_t xd0 = smem_desc_sw128(ring);
+            const uint64_t wd0 = smem_desc_sw128(ring + M::kXBytes + half * M::kHalfBytes);
+            int s = 0;
+            uint32_t ph = 0, aph = 1;   // phases of the stages, and of the slots (a fresh barrier passes)
+            uint32_t stage_full = full(0), stage_empty = empty(0), slot_full = acc_full(half, 0), slot_empty = acc_empty(half, 0);
+            uint32_t d = tmem + half * A * 128, stage = 0;   // stage: in units of a descriptor's address
+            ok = true;
+            const int64_t total = first < items ? (int64_t)((items - first + step - 1) / step) * a.kb : 0;
+#pragma unroll 1
+            for (int64_t j = 0; j < total; ++j) {   // the blocks of all items alike
+                if (!(ok = warp_wait_both(stage_full, ph, slot_empty, aph, abort_flag, a.status, a.wait_limit_ns))) break;
+                tc_fence_after();
+                if (one) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)     // +32 bytes along K
-                        mma_e4m3(tmem + q * N, xd + 2 * j, wd + 2 * j, idesc, j != 0);
-                    mma_commit(empty(s));
-                    mma_commit(acc_full(q));
-                    if (++s == S) { s = 0; ph ^= 1u; }
-                    if (++q == A) { q = 0; aph ^= 1u; wrapped = true; }
+                    for (int i = 0; i < 4; ++i)   // +32 bytes along K
+                        mma_e4m3(d, xd0 + stage + 2 * i, wd0 + stage + 2 * i, idesc, i != 0);
+                    mma_commit(slot_full);
+                    mma_commit(stage_empty);
+                }
+                __syncwarp();
+                aph ^= (slot_full >> 3) & 1u;   // after the second slot (the first one's barrier has bit 3 clear)
+                slot_full ^= 8u;
+                slot_empty ^= 8u;
+                d ^= 128u;
+                stage += M::kStage >> 4;
+                stage_full += 8u;
+                stage_empty += 8u;
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
+                    stage = 0;
+                    stage_full = full(0);
+                    stage_empty = empty(0);
                 }
             }
-            if (!ok) {   // our MMAs end before the TMEM is freed (bounded)
+            if (!ok && one) {   // our MMAs end before the TMEM is freed (bounded)
                 volatile uint32_t no_abort = 0;
                 mma_commit(drain);
-                mbar_wait(drain, 0, &no_abort, a.status, limit);
+                mbar_wait(drain, 0, &no_abort, a.status, a.wait_limit_ns);
             }
         }
     } else {
-        const int quarter = warp & 3, half = (warp - 2) >> 2, p = 32 * quarter + lane;
-        // this thread's columns: 64 from c_lo on and 64 from c_hi on (with SwiGLU gate columns and their up columns)
-        const uint32_t c_lo = SWIGLU ? 64 * half : 128 * half, c_hi = SWIGLU ? 128 + 64 * half : 128 * half + 64;
-        const uint32_t base = tmem + ((uint32_t)(32 * quarter) << 16);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWideRegs));
+        const int quarter = warp & 3, half = (warp - 4) >> 2, p = 32 * quarter + lane;
         const int es = a.ydtype == BQ_DT_F32 ? 4 : 2;
-        const bool wide = (reinterpret_cast<uintptr_t>(a.y) | (uintptr_t)(a.ldy * es)) % 32 == 0;
-        int q = 0;
-        uint32_t aph = 0;
+        const bool aligned = (reinterpret_cast<uintptr_t>(a.y) | (uintptr_t)(a.ldy * es)) % 32 == 0;
+        // The slot in turn: its barriers (the second's 8 bytes behind the first's) and its columns, flipped by a bit.
+        uint32_t bar_full = acc_full(half, 0), t = tmem + ((uint32_t)(32 * quarter) << 16) + half * A * 128, aph = 0;
+        uint32_t bar_free = acc_empty(half, 0);
+        const bool one = elect_one();
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item it = find_item(a, s_tiles, w_tiles, (int)i);
+        for (Items i(first, step, items, w_tiles); ok && i.more(); i.next()) {
+            const Item it = i.get(chunks, a.E);
             const float* xs = a.xs + (int64_t)(it.row0 + min(p, it.rows - 1)) * a.kb;
-            const int wb_lo = SWIGLU ? it.tile : min(2 * it.tile + half, a.nb - 1);
-            const float* ws_lo = a.ws + ((int64_t)it.e * a.nb + wb_lo) * a.kb;
-            const float* ws_hi = SWIGLU ? ws_lo + (int64_t)(a.nb / 2) * a.kb : ws_lo;
-            uint64_t acc[64];
+            const float* ws = a.ws + (int64_t)it.e * a.nb * a.kb;
+            // this half's first column and the scale row of its columns, with SwiGLU of its gate columns and up columns
+            const int c0 = kTileCols * it.tile + kTileCols / 2 * half;
+            const int o_lo = min(c0 / kBlock, a.nb - 1) * a.kb, o_hi = o_lo + a.nb / 2 * a.kb;
+            float acc[128];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[j] = 0ull;
-            float x_next = __ldg(xs), lo_next = __ldg(ws_lo), hi_next = SWIGLU ? __ldg(ws_hi) : 0.f;
+            for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+            // Scales are loaded two blocks ahead; a block's wait and the load of its first columns come before the last
+            // sums of the block before it, which cover their latency.
+            const int b_last = a.kb - 1, b_next = min(1, b_last);
+            float x0 = __ldg(xs), lo0 = __ldg(ws + o_lo), hi0 = SWIGLU ? __ldg(ws + o_hi) : 0.f;
+            float x1 = load_early(xs + b_next), lo1 = load_early(ws + o_lo + b_next), hi1 = 0.f;
+            if (SWIGLU) hi1 = load_early(ws + o_hi + b_next);
+            uint32_t v0[32], v1[32];
+            if (!(ok = warp_wait_all(bar_full, aph, abort_flag, a.status, a.wait_limit_ns))) break;
+            tc_fence_after();
+            tmem_ld32(t, v0);
+#pragma unroll 1
             for (int b = 0; b < a.kb; ++b) {
-                const float s_lo = x_next * lo_next, s_hi = SWIGLU ? x_next * hi_next : s_lo;
-                const uint64_t lo2 = pack2(s_lo, s_lo), hi2 = pack2(s_hi, s_hi);
-                const int bn = min(b + 1, a.kb - 1);
-                x_next = __ldg(xs + bn);
-                lo_next = __ldg(ws_lo + bn);
-                if (SWIGLU) hi_next = __ldg(ws_hi + bn);
-                if (!(ok = warp_wait_all(acc_full(q), aph, abort_flag, a.status, limit))) break;
-                tc_fence_after();
-                uint32_t v0[32], v1[32];
-                const uint32_t t = base + q * N;
-                tmem_ld32(t + c_lo, v0);
+                const float f_lo = x0 * lo0, f_hi = SWIGLU ? x0 * hi0 : f_lo;
+                x0 = x1; lo0 = lo1; hi0 = hi1;
+                const int bn = min(b + 2, b_last);
+                x1 = load_early(xs + bn);
+                lo1 = load_early(ws + o_lo + bn);
+                if (SWIGLU) hi1 = load_early(ws + o_hi + bn);
                 tmem_wait_ld(v0);
-                tmem_ld32(t + c_lo + 32, v1);
-                add_scaled(acc, v0, lo2);
+                tmem_ld32(t + 32, v1);
+                add_scaled(acc, v0, f_lo);
                 tmem_wait_ld(v1);
-                tmem_ld32(t + c_hi, v0);
-                add_scaled(acc + 16, v1, lo2);
+                tmem_ld32(t + 64, v0);
+                add_scaled(acc + 32, v1, f_lo);
                 tmem_wait_ld(v0);
-                tmem_ld32(t + c_hi + 32, v1);
-                add_scaled(acc + 32, v0, hi2);
+                tmem_ld32(t + 96, v1);
+                add_scaled(acc + 64, v0, f_hi);
                 tmem_wait_ld(v1);
                 tc_fence_before();
-                mbar_arrive(acc_empty(q));
-                add_scaled(acc + 48, v1, hi2);
-                if (++q == A) { q = 0; aph ^= 1u; }
+                __syncwarp();
+                if (one) mbar_arrive(bar_free);
+                aph ^= (bar_full >> 3) & 1u;   // after the second slot (the first one's barrier has bit 3 clear)
+                bar_full ^= 8u;
+                bar_free ^= 8u;
+                t ^= 128u;
+                if (b < b_last) {
+                    if (!(ok = warp_wait_all(bar_full, aph, abort_flag, a.status, a.wait_limit_ns))) break;
+                    tc_fence_after();
+                    tmem_ld32(t, v0);
+                }
+                add_scaled(acc + 96, v1, f_hi);
             }
             if (!ok) break;
             if (p < it.rows) {
-                const int c0 = kTileCols * it.tile + (SWIGLU ? 64 : 128) * half;
 #pragma unroll
                 for (int g = 0; g < (SWIGLU ? 4 : 8); ++g) {
                     float f[16];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 v = unpack2(acc[8 * g + j]);
-                        f[2 * j] = v.x;
-                        f[2 * j + 1] = v.y;
-                        if (SWIGLU) {
-                            const float2 u = unpack2(acc[32 + ((8 * g + j) & 31)]);
-                            f[2 * j] = silu_f(v.x) * u.x;
-                            f[2 * j + 1] = silu_f(v.y) * u.y;
-                        }
+                    for (int j = 0; j < 16; ++j) {
+                        const int n = 16 * g + j;
+                        f[j] = SWIGLU ? silu_f(acc[n]) * acc[(64 + n) & 127] : acc[n];
                     }
-                    store16(a, it.row0 + p, c0 + 16 * g, f, wide);
+                    store16(a, it.row0 + p, c0 + 16 * g, f, aligned);
                 }
             }
         }
@@ -737,23 +842,24 @@ bool row_map(CUtensorMap* map, const uint8_t* x, int rows, int k, int box) {
     return encode(map, x, 2, dims, strides, b);
 }
 
-// Weights [E][n][k] in boxes of 128 bytes x 128 rows; of a gate/up weight
-// [E][2][n/2][k] in boxes of 16 gate rows and their 16 up rows.
-bool weight_map(CUtensorMap* map, const uint8_t* w, int E, int n, int k, bool swiglu) {
-    if (!swiglu) {
-        const uint64_t dims[3] = {(uint64_t)k, (uint64_t)n, (uint64_t)E}, strides[2] = {(uint64_t)k, (uint64_t)n * k};
-        const uint32_t b[3] = {kBlock, 128, 1};
-        return encode(map, w, 3, dims, strides, b);
-    }
+// Weights [E][n][k] in boxes of 128 bytes x 128 rows.
+bool weight_map(CUtensorMap* map, const uint8_t* w, int E, int n, int k) {
+    const uint64_t dims[3] = {(uint64_t)k, (uint64_t)n, (uint64_t)E}, strides[2] = {(uint64_t)k, (uint64_t)n * k};
+    const uint32_t b[3] = {kBlock, 128, 1};
+    return encode(map, w, 3, dims, strides, b);
+}
+
+// A gate/up weight [E][2][n/2][k] in boxes of `box` gate rows and their up rows.
+bool gate_up_map(CUtensorMap* map, const uint8_t* w, int E, int n, int k, int box) {
     const uint64_t h = n / 2;
     const uint64_t dims[4] = {(uint64_t)k, h, 2, (uint64_t)E}, strides[3] = {(uint64_t)k, h * k, (uint64_t)n * k};
-    const uint32_t b[4] = {kBlock, 16, 2, 1};
+    const uint32_t b[4] = {kBlock, (uint32_t)box, 2, 1};
     return encode(map, w, 4, dims, strides, b);
 }
 
 constexpr int kSms = 152;
 
-template <int NT, bool SWIGLU>
+template <bool SWIGLU>
 cudaError_t launch_lanes(const CUtensorMap& map_w, const CUtensorMap& map_x, const Args& a, int64_t items, int split,
                          cudaStream_t st) {
     // per device: the attribute is a property of the function on the current device
@@ -761,15 +867,15 @@ cudaError_t launch_lanes(const CUtensorMap& map_w, const CUtensorMap& map_x, con
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(mm_lanes_kernel<NT, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   LaneSmem<NT>::kBytes);
+        const cudaError_t e = cudaFuncSetAttribute(mm_lanes_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   LaneSmem::kBytes);
         if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(split > 1 ? items * split : std::min<int64_t>(items, kSms)));
     cfg.blockDim = dim3(kLaneThreads);
-    cfg.dynamicSmemBytes = LaneSmem<NT>::kBytes;
+    cfg.dynamicSmemBytes = LaneSmem::kBytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -779,7 +885,7 @@ cudaError_t launch_lanes(const CUtensorMap& map_w, const CUtensorMap& map_x, con
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, mm_lanes_kernel<NT, SWIGLU>, map_w, map_x, a, split);
+    return cudaLaunchKernelEx(&cfg, mm_lanes_kernel<SWIGLU>, map_w, map_x, a, split);
 }
 
 template <bool SWIGLU>
@@ -825,32 +931,40 @@ bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32
     // most row chunks and items there can be, for the grid and (as an int) inside the kernel
     auto chunks_of = [&](int most) { return (int64_t)(rows + most - 1) / most + (offsets ? experts : 0); };
     auto tiles_of = [&](int width) { return (int64_t)(cols + width - 1) / width; };
-    const bool wide = rows / experts >= 96 && chunks_of(128) * tiles_of(swiglu ? 128 : 256) >= 100;
-    const int nt = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    const int64_t chunks = chunks_of(wide ? 128 : nt);
-    const int64_t items = chunks * (wide ? tiles_of(swiglu ? 128 : 256) : tiles_of(swiglu ? 64 : 128));
+    // Which kernel.  Weights on the lanes: while its items fit one wave (n = k = 4096: 128 rows 11.3 us against 15.0;
+    // 192 rows, two waves, 19.4 against 14.7), and for experts of up to 16 rows on average, where both read every
+    // weight once and it reads less beside them (128 experts, gate/up 1536 x 2048: 8 rows 69.1 us against 72.2, 16 rows
+    // 71.0 against 73.1, 32 rows 85.2 against 74.9).  There the wide tile is the faster one when K is so short that the
+    // narrower tile's more items count (down 2048 x 768: 0.3 rows 12.8 against 13.3, 4 rows 38.2 against 35.6).
+    const int kb = (k + kBlock - 1) / kBlock;
+    const int64_t lane_items = chunks_of(kLaneRows) * tiles_of(swiglu ? 64 : 128);
+    const bool few_rows = offsets && rows <= 16 * (int64_t)experts && !(kb <= 8 && lane_items > 8 * kSms);
+    const bool wide = lane_items > kSms && !few_rows;
+    const int64_t chunks = chunks_of(wide ? 128 : kLaneRows);
+    const int64_t items = wide ? chunks * tiles_of(swiglu ? 128 : 256) : lane_items;
     if (items > INT32_MAX / 2) return bq::fail(BQ_ERR_SHAPE, "%s: %d rows x %d columns are too many", name, rows, cols);
     bq_status s = bq::check_arch();
     if (s != BQ_OK) return s;
     const bq::WaitProbe probe = bq::wait_probe();
-    const Args a{xscales, rows, offsets, E, wscales, n, k, (k + kBlock - 1) / kBlock, (n + kBlock - 1) / kBlock, cols,
+    const Args a{xscales, rows, offsets, E, wscales, n, k, kb, (n + kBlock - 1) / kBlock, cols,
                  y, ydtype, ldy, bq::device_status_ptr(), probe.limit_ns, probe.skip_weight_copies, (int)chunks};
     CUtensorMap map_w, map_x;
-    if (!weight_map(&map_w, w, E, n, k, swiglu && !wide) || !row_map(&map_x, x, rows, k, !wide && nt == 32 ? 16 : 32))
+    const bool mapped = swiglu ? gate_up_map(&map_w, w, E, n, k, wide ? 64 : 16) : weight_map(&map_w, w, E, n, k);
+    if (!mapped || !row_map(&map_x, x, rows, k, wide ? 128 : LaneSmem::BOX))
         return bq::fail(BQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", name);
     cudaError_t e;
     if (wide) {
         e = swiglu ? launch_wide<true>(map_w, map_x, a, items, st) : launch_wide<false>(map_w, map_x, a, items, st);
     } else {
+        // K split over a cluster while all clusters are resident at once (this GPU holds 76, 36 and 15 clusters of 2, 4
+        // and 8 CTAs of this size) and a CTA keeps two blocks.  n = k = 4096, one row: 10.6 / 7.2 / 5.6 us for 1, 2 and
+        // 4, and 12.6 for 8, which takes two waves.
         int split = 1;
-        while (split < kMaxCluster && items * split * 2 <= kSms && a.kb >= 4 * split) split *= 2;
-        auto go = [&](auto width) {
-            constexpr int NT = decltype(width)::value;
-            return swiglu ? launch_lanes<NT, true>(map_w, map_x, a, items, split, st)
-                          : launch_lanes<NT, false>(map_w, map_x, a, items, split, st);
-        };
-        e = nt == 32 ? go(std::integral_constant<int, 32>()) : nt == 64 ? go(std::integral_constant<int, 64>())
-                                                                          : go(std::integral_constant<int, 128>());
+        if (items <= 15 && kb >= 16) split = 8;
+        else if (items <= 36 && kb >= 8) split = 4;
+        else if (items <= 76 && kb >= 4) split = 2;
+        e = swiglu ? launch_lanes<true>(map_w, map_x, a, items, split, st)
+                   : launch_lanes<false>(map_w, map_x, a, items, split, st);
     }
     if (e != cudaSuccess) return bq::fail(BQ_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
     bq::note_launch();

@@ -67,7 +67,8 @@ def check(got, want, err, what=""):
 
 MM = [(1, 128, 128), (1, 4096, 4096), (8, 256, 2048), (32, 256, 2048), (33, 200, 272), (7, 1, 16), (64, 1000, 144),
       (129, 384, 512), (130, 4096, 768), (257, 511, 1040), (300, 130, 128), (1000, 640, 384), (16, 4096, 4096),
-      (5, 129, 8208), (65, 2048, 640), (2, 5000, 2048)]
+      (5, 129, 8208), (65, 2048, 640), (2, 5000, 2048), (700, 2050, 272), (5000, 100, 144),
+      (1153, 1024, 128)]
 
 
 @pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
@@ -85,7 +86,7 @@ def test_dense_product(lib, m, n, k, out):
 
 @pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("m,n,k", [(1, 256, 128), (8, 1536, 2048), (40, 768, 272), (130, 512, 1040), (300, 1280, 512),
-                                   (520, 256, 384), (3, 4096, 4096)])
+                                   (520, 256, 384), (3, 4096, 4096), (1200, 1024, 384), (3333, 256, 16)])
 def test_dense_product_with_swiglu(lib, m, n, k, out):
     import torch
     g = np.random.default_rng(m + n + k)
@@ -125,6 +126,9 @@ GROUPS = [
     ([700], 768, 144),
     ([17] * 40, 256, 128),
     ([0] * 30 + [2] + [0] * 33, 1536, 2048),
+    ([40] * 30, 512, 384),
+    ([200, 0, 1, 300, 77, 0, 129, 128], 1024, 272),
+    ([3, 0, 1, 17] * 40, 2048, 144),
 ]
 
 
@@ -140,9 +144,11 @@ def test_grouped_product(lib, case, swiglu, out):
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_grouped_rows_outside_every_expert_stay(lib, swiglu):
     run_grouped(lib, np.random.default_rng(3), [3, 0, 70, 9], 256, 256, "bf16", swiglu, behind=200, first=5)
+    run_grouped(lib, np.random.default_rng(3), [130, 0, 700, 9], 1024, 256, "bf16", swiglu, behind=200, first=5)
 
 
 def test_grouped_odd_columns(lib):
+    run_grouped(lib, np.random.default_rng(2), [500, 0, 333, 150], 1001, 144, "f16", False)
     for n in (1, 127, 129, 1000):
         run_grouped(lib, np.random.default_rng(n), [4, 0, 33, 150], n, 144, "f32", False)
 
@@ -172,7 +178,7 @@ def test_grouped_bad_offsets_are_reported_and_skipped(lib):
     assert np.abs(got[[0, 1, 4, 5, 6, 7]] - want[[0, 1, 4, 5, 6, 7]]).max() < 1e-4 and (got[8:] == 7).all()
 
 
-@pytest.mark.parametrize("m", [3, 200])
+@pytest.mark.parametrize("m", [3, 200, 2000])
 def test_nan_and_infinite_scales_stay_in_their_rows_and_columns(lib, m):
     import torch
     g = np.random.default_rng(7)
@@ -194,7 +200,7 @@ def test_nan_and_infinite_scales_stay_in_their_rows_and_columns(lib, m):
     assert (np.abs(rest - want[:, keep]) <= err[:, keep]).all()
 
 
-@pytest.mark.parametrize("m", [2, 70, 300])
+@pytest.mark.parametrize("m", [2, 70, 300, 3000])
 def test_strided_output(lib, m):
     import torch
     g = np.random.default_rng(8)
@@ -218,7 +224,7 @@ def test_no_rows(lib):
     assert lib.launch_count() == n
 
 
-@pytest.mark.parametrize("m", [1, 33, 260])
+@pytest.mark.parametrize("m", [1, 33, 260, 1500])
 def test_two_runs_agree_bit_for_bit(lib, m):
     import torch
     g = np.random.default_rng(9)
