@@ -4,6 +4,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "bq_internal.cuh"
 
 namespace bq {
@@ -23,7 +25,22 @@ inline bq_status check_rows(const char* name, const char* what, const void* p, i
     return BQ_OK;
 }
 
-// VALUES of one 16-byte vector of row type DT.
+// Calls f with k as a compile-time constant (1..8).
+template <typename F>
+void with_k(int k, F f) {
+    switch (k) {
+        case 1: f(std::integral_constant<int, 1>()); break;
+        case 2: f(std::integral_constant<int, 2>()); break;
+        case 3: f(std::integral_constant<int, 3>()); break;
+        case 4: f(std::integral_constant<int, 4>()); break;
+        case 5: f(std::integral_constant<int, 5>()); break;
+        case 6: f(std::integral_constant<int, 6>()); break;
+        case 7: f(std::integral_constant<int, 7>()); break;
+        default: f(std::integral_constant<int, 8>()); break;
+    }
+}
+
+// One 16-byte vector of row type DT as N fp32 values.
 template <int DT> struct RowVec;
 
 template <> struct RowVec<BQ_DT_F32> {

@@ -19,9 +19,8 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Sorted row of pair f; -1 if it was dropped or is out of range (recorded).
-__device__ __forceinline__ int sorted_row(const int32_t* inv, int64_t f, int64_t pairs, int32_t* status) {
-    const int r = __ldg(inv + f);
+// Sorted row r of a pair, or -1 if it was dropped or is out of range (recorded).
+__device__ __forceinline__ int checked_row(int r, int pairs, int32_t* status) {
     if (r < -1 || r >= pairs) {
         bq::set_device_error(status, BQ_DEV_BAD_ROW);
         return -1;
@@ -29,43 +28,69 @@ __device__ __forceinline__ int sorted_row(const int32_t* inv, int64_t f, int64_t
     return r;
 }
 
-// One 16-byte vector of a token's row to its k sorted rows.
-__global__ void __launch_bounds__(kThreads)
-dispatch_kernel(const uint8_t* __restrict__ x, int64_t ldx, int T, int vecs, const int32_t* __restrict__ inv, int k,
-                uint8_t* __restrict__ xs, int64_t ldxs, int32_t* status) {
-    const int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x;
-    if (i >= (int64_t)T * vecs) return;
-    const int64_t t = i / vecs;
-    const int c = (int)(i - t * vecs);
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + t * ldx) + c);
-    for (int j = 0; j < k; ++j) {
-        const int r = sorted_row(inv, t * k + j, (int64_t)T * k, status);
-        if (r >= 0) reinterpret_cast<uint4*>(xs + r * ldxs)[c] = v;
-    }
+// The K sorted rows of token t, loaded together.
+template <int K>
+__device__ __forceinline__ void sorted_rows(const int32_t* inv, int64_t t, int pairs, int32_t* status, int (&r)[K]) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) r[j] = __ldg(inv + t * K + j);
+#pragma unroll
+    for (int j = 0; j < K; ++j) r[j] = checked_row(r[j], pairs, status);
 }
 
-// One 16-byte vector of y[t].  weights NULL: a plain sum.
-template <int DT>
+// Threads of a block: x over the 16-byte vectors of a row, y over tokens.  K is
+// a template argument so that the K rows' loads (or stores) are issued
+// together: with a loop over k that waits for each row they took 1.3 times as
+// long.
+
+// One vector of a token's row to its K sorted rows.
+template <int K>
+__global__ void __launch_bounds__(kThreads)
+dispatch_kernel(const uint8_t* __restrict__ x, int64_t ldx, int T, int vecs, const int32_t* __restrict__ inv,
+                uint8_t* __restrict__ xs, int64_t ldxs, int32_t* status) {
+    bq::grid_dependency_wait();   // launched behind whatever precedes it on the stream
+    bq::allow_dependents();
+    const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
+    const int c = blockIdx.y * blockDim.x + threadIdx.x;
+    if (t >= T || c >= vecs) return;
+    int r[K];
+    sorted_rows(inv, t, T * K, status, r);
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + t * ldx) + c);
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+        if (r[j] >= 0) reinterpret_cast<uint4*>(xs + r[j] * ldxs)[c] = v;
+}
+
+// One vector of y[t].  weights NULL: a plain sum.
+template <int DT, int K>
 __global__ void __launch_bounds__(kThreads)
 combine_rows_kernel(const uint8_t* __restrict__ ys, int64_t ldys, int T, int vecs, const int32_t* __restrict__ inv,
-                    const float* __restrict__ weights, int k, int accumulate, uint8_t* __restrict__ y, int64_t ldy,
+                    const float* __restrict__ weights, int accumulate, uint8_t* __restrict__ y, int64_t ldy,
                     int32_t* status) {
     using V = bq::RowVec<DT>;
-    const int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x;
-    if (i >= (int64_t)T * vecs) return;
-    const int64_t t = i / vecs;
-    const int c = (int)(i - t * vecs);
+    bq::grid_dependency_wait();   // launched behind whatever precedes it on the stream
+    bq::allow_dependents();
+    const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
+    const int c = blockIdx.y * blockDim.x + threadIdx.x;
+    if (t >= T || c >= vecs) return;
+    int r[K];
+    float w[K];
+    uint4 raw[K];
+    sorted_rows(inv, t, T * K, status, r);
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        raw[j] = r[j] >= 0 ? __ldg(reinterpret_cast<const uint4*>(ys + r[j] * ldys) + c) : make_uint4(0, 0, 0, 0);
+        w[j] = weights ? __ldg(weights + t * K + j) : 1.f;
+        if (r[j] < 0) w[j] = 0.f;   // 0 * 0 adds nothing, whatever the pair's weight is
+    }
     float acc[V::N];
 #pragma unroll
     for (int n = 0; n < V::N; ++n) acc[n] = 0.f;
-    for (int j = 0; j < k; ++j) {
-        const int r = sorted_row(inv, t * k + j, (int64_t)T * k, status);
-        if (r < 0) continue;
-        const float w = weights ? __ldg(weights + t * k + j) : 1.f;
-        float f[V::N];
-        V::unpack(__ldg(reinterpret_cast<const uint4*>(ys + r * ldys) + c), f);
 #pragma unroll
-        for (int n = 0; n < V::N; ++n) acc[n] = __fmaf_rn(w, f[n], acc[n]);
+    for (int j = 0; j < K; ++j) {
+        float f[V::N];
+        V::unpack(raw[j], f);
+#pragma unroll
+        for (int n = 0; n < V::N; ++n) acc[n] = __fmaf_rn(w[j], f[n], acc[n]);
     }
     uint4* out = reinterpret_cast<uint4*>(y + t * ldy) + c;
     if (accumulate) {
@@ -77,52 +102,64 @@ combine_rows_kernel(const uint8_t* __restrict__ ys, int64_t ldys, int T, int vec
     *out = V::pack(acc);
 }
 
-// One CTA per token: its k rows of dys and its k weight gradients.
-template <int DT>
+// One CTA per token: its K rows of dys and its K weight gradients.
+template <int DT, int K>
 __global__ void __launch_bounds__(kThreads)
 combine_backward_kernel(const uint8_t* __restrict__ dy, int64_t lddy, const uint8_t* __restrict__ ys, int64_t ldys,
-                        int T, int vecs, const int32_t* __restrict__ inv, const float* __restrict__ weights, int k,
+                        int T, int vecs, const int32_t* __restrict__ inv, const float* __restrict__ weights,
                         uint8_t* __restrict__ dys, int64_t lddys, float* __restrict__ dweights, int32_t* status) {
     using V = bq::RowVec<DT>;
-    __shared__ float part[kThreads / 32][8];
+    __shared__ float part[kThreads / 32][K];
+    bq::grid_dependency_wait();   // launched behind whatever precedes it on the stream
+    bq::allow_dependents();
     const int64_t t = blockIdx.x;
-    float dot[8];
-    for (int j = 0; j < 8; ++j) dot[j] = 0.f;
-    for (int c = threadIdx.x; c < vecs; c += kThreads) {
+    int r[K];
+    float w[K], dot[K];
+    sorted_rows(inv, t, T * K, status, r);
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        w[j] = dys ? __ldg(weights + t * K + j) : 0.f;
+        dot[j] = 0.f;
+    }
+    for (int c = threadIdx.x; c < vecs; c += blockDim.x) {
+        uint4 raw[K];
+        const uint4 raw_g = __ldg(reinterpret_cast<const uint4*>(dy + t * lddy) + c);
+        if (dweights) {
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (r[j] >= 0) raw[j] = __ldg(reinterpret_cast<const uint4*>(ys + r[j] * ldys) + c);
+        }
         float g[V::N];
-        V::unpack(__ldg(reinterpret_cast<const uint4*>(dy + t * lddy) + c), g);
+        V::unpack(raw_g, g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j >= k) break;
-            const int r = sorted_row(inv, t * k + j, (int64_t)T * k, status);
-            if (r < 0) continue;
-            if (dweights) {
-                float f[V::N];
-                V::unpack(__ldg(reinterpret_cast<const uint4*>(ys + r * ldys) + c), f);
-#pragma unroll
-                for (int n = 0; n < V::N; ++n) dot[j] = __fmaf_rn(g[n], f[n], dot[j]);
-            }
+        for (int j = 0; j < K; ++j) {
+            if (r[j] < 0) continue;
             if (dys) {
-                const float w = __ldg(weights + t * k + j);
                 float o[V::N];
 #pragma unroll
-                for (int n = 0; n < V::N; ++n) o[n] = w * g[n];
-                reinterpret_cast<uint4*>(dys + r * lddys)[c] = V::pack(o);
+                for (int n = 0; n < V::N; ++n) o[n] = w[j] * g[n];
+                reinterpret_cast<uint4*>(dys + r[j] * lddys)[c] = V::pack(o);
+            }
+            if (dweights) {
+                float f[V::N];
+                V::unpack(raw[j], f);
+#pragma unroll
+                for (int n = 0; n < V::N; ++n) dot[j] = __fmaf_rn(g[n], f[n], dot[j]);
             }
         }
     }
     if (!dweights) return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < K; ++j) {
 #pragma unroll
         for (int off = 16; off; off >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], off);
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][j] = dot[j];
     }
     __syncthreads();
-    if (threadIdx.x < k) {
+    if (threadIdx.x < K) {
         float s = 0.f;
-        for (int w = 0; w < kThreads / 32; ++w) s += part[w][threadIdx.x];
-        dweights[t * k + threadIdx.x] = s;
+        for (int i = 0; i < (int)blockDim.x / 32; ++i) s += part[i][threadIdx.x];
+        dweights[t * K + threadIdx.x] = s;
     }
 }
 
@@ -141,28 +178,36 @@ bq_status check_list(const char* name, const char* what, const void* p) {
     return BQ_OK;
 }
 
-// CTAs of one thread per 16-byte vector, or an error when there are too many for a grid.
-bq_status vector_grid(const char* name, int T, int vecs, unsigned* grid) {
-    const int64_t n = ((int64_t)T * vecs + kThreads - 1) / kThreads;
-    if (n > INT32_MAX) return bq::fail(BQ_ERR_SHAPE, "%s: T = %d rows of %d vectors are too many", name, T, vecs);
-    *grid = (unsigned)n;
+// Blocks of one thread per 16-byte vector of T rows.
+struct VectorGrid {
+    dim3 grid, block;
+};
+
+bq_status vector_grid(const char* name, int T, int vecs, VectorGrid* g) {
+    const int x = std::min(kThreads, (vecs + 31) / 32 * 32), y = kThreads / x;
+    g->block = dim3(x, y);
+    g->grid = dim3(((unsigned)T + y - 1) / y, (vecs + x - 1) / x);
+    if (g->grid.y > 65535) return bq::fail(BQ_ERR_SHAPE, "%s: rows of %d vectors are too long", name, vecs);
     return BQ_OK;
 }
 
 bq_status run_combine(const char* name, const void* ys, int32_t dtype, int32_t T, int32_t H, int64_t ldys,
                       const int32_t* inv, const float* weights, int32_t k, int accumulate, void* y, int64_t ldy,
                       cudaStream_t st) {
-    const int es = bq::dtype_size(dtype), vecs = H * es / 16;
-    unsigned grid;
+    const int es = bq::dtype_size(dtype), vecs = (int)((int64_t)H * es / 16);
+    VectorGrid g;
     bq_status s;
-    if ((s = vector_grid(name, T, vecs, &grid)) != BQ_OK || (s = bq::check_arch()) != BQ_OK) return s;
-    auto go = [&](auto kernel) {
-        kernel<<<grid, kThreads, 0, st>>>(static_cast<const uint8_t*>(ys), ldys * es, T, vecs, inv, weights, k,
-                                          accumulate, static_cast<uint8_t*>(y), ldy * es, bq::device_status_ptr());
-    };
-    if (dtype == BQ_DT_F32) go(combine_rows_kernel<BQ_DT_F32>);
-    else if (dtype == BQ_DT_F16) go(combine_rows_kernel<BQ_DT_F16>);
-    else go(combine_rows_kernel<BQ_DT_BF16>);
+    if ((s = vector_grid(name, T, vecs, &g)) != BQ_OK || (s = bq::check_arch()) != BQ_OK) return s;
+    bq::with_k(k, [&](auto kk) {
+        constexpr int K = decltype(kk)::value;
+        auto go = [&](auto kernel) {
+            bq::launch_after(kernel, g.grid, g.block, 0, st, static_cast<const uint8_t*>(ys), ldys * es, T, vecs, inv,
+                             weights, accumulate, static_cast<uint8_t*>(y), ldy * es, bq::device_status_ptr());
+        };
+        if (dtype == BQ_DT_F32) go(combine_rows_kernel<BQ_DT_F32, K>);
+        else if (dtype == BQ_DT_F16) go(combine_rows_kernel<BQ_DT_F16, K>);
+        else go(combine_rows_kernel<BQ_DT_BF16, K>);
+    });
     bq::note_launch();
     return bq::check_launch(name);
 }
@@ -175,14 +220,16 @@ extern "C" bq_status bq_moe_dispatch(const void* x, int32_t dtype, int32_t T, in
     bq_status s = check_pairs(name, dtype, T, H, k);
     if (s != BQ_OK || T == 0) return s;
     const int es = bq::dtype_size(dtype), vecs = (int)((int64_t)H * es / 16);
-    unsigned grid;
+    VectorGrid g;
     if ((s = bq::check_rows(name, "x", x, H, ldx, es)) != BQ_OK ||
         (s = bq::check_rows(name, "xs", xs, H, ldxs, es)) != BQ_OK || (s = check_list(name, "inv", inv)) != BQ_OK ||
-        (s = vector_grid(name, T, vecs, &grid)) != BQ_OK || (s = bq::check_arch()) != BQ_OK)
+        (s = vector_grid(name, T, vecs, &g)) != BQ_OK || (s = bq::check_arch()) != BQ_OK)
         return s;
-    dispatch_kernel<<<grid, kThreads, 0, (cudaStream_t)stream>>>(static_cast<const uint8_t*>(x), ldx * es, T, vecs, inv,
-                                                                 k, static_cast<uint8_t*>(xs), ldxs * es,
-                                                                 bq::device_status_ptr());
+    bq::with_k(k, [&](auto kk) {
+        bq::launch_after(dispatch_kernel<decltype(kk)::value>, g.grid, g.block, 0, (cudaStream_t)stream,
+                         static_cast<const uint8_t*>(x), ldx * es, T, vecs, inv, static_cast<uint8_t*>(xs), ldxs * es,
+                         bq::device_status_ptr());
+    });
     bq::note_launch();
     return bq::check_launch(name);
 }
@@ -234,14 +281,18 @@ extern "C" bq_status bq_moe_combine_backward(const void* dy, int64_t lddy, const
                      (s = check_list(name, "dweights", dweights)) != BQ_OK))
         return s;
     if ((s = bq::check_arch()) != BQ_OK) return s;
-    auto go = [&](auto kernel) {
-        kernel<<<T, kThreads, 0, (cudaStream_t)stream>>>(
-            static_cast<const uint8_t*>(dy), lddy * es, static_cast<const uint8_t*>(ys), ldys * es, T, H * es / 16, inv,
-            weights, k, static_cast<uint8_t*>(dys), lddys * es, dweights, bq::device_status_ptr());
-    };
-    if (dtype == BQ_DT_F32) go(combine_backward_kernel<BQ_DT_F32>);
-    else if (dtype == BQ_DT_F16) go(combine_backward_kernel<BQ_DT_F16>);
-    else go(combine_backward_kernel<BQ_DT_BF16>);
+    const int vecs = (int)((int64_t)H * es / 16), threads = std::min(kThreads, (vecs + 31) / 32 * 32);
+    bq::with_k(k, [&](auto kk) {
+        constexpr int K = decltype(kk)::value;
+        auto go = [&](auto kernel) {
+            bq::launch_after(kernel, dim3(T), dim3(threads), 0, (cudaStream_t)stream, static_cast<const uint8_t*>(dy),
+                             lddy * es, static_cast<const uint8_t*>(ys), ldys * es, T, vecs, inv, weights,
+                             static_cast<uint8_t*>(dys), lddys * es, dweights, bq::device_status_ptr());
+        };
+        if (dtype == BQ_DT_F32) go(combine_backward_kernel<BQ_DT_F32, K>);
+        else if (dtype == BQ_DT_F16) go(combine_backward_kernel<BQ_DT_F16, K>);
+        else go(combine_backward_kernel<BQ_DT_BF16, K>);
+    });
     bq::note_launch();
     return bq::check_launch(name);
 }
