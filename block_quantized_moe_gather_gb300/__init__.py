@@ -118,20 +118,12 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-_raw_stream = None   # handle of the current stream of a device
-
-
 def _stream(stream):
-    """Handle of `stream`, or of the current stream of the current device."""
-    global _raw_stream
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
-    if _raw_stream is None:
-        # the handle alone; a torch.cuda.Stream object costs 3 us to make
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda device: torch.cuda.current_stream(device).cuda_stream)
-    return _raw_stream(torch.cuda.current_device())
+    if stream is None:
+        if _DT is None:
+            _load_torch()
+        return _get_stream(_get_device())
+    return stream.cuda_stream
 
 
 def status_string(s: int) -> str:
@@ -374,32 +366,38 @@ def moe_gather_qmm_hidden(layer: MoELayer, router: QWeight, hidden, gamma, eps: 
 _DT = None          # torch dtype -> bq_dtype
 _KINDS = None       # _dense's kinds -> the torch dtypes they take
 _get_device = None  # ordinal of the current CUDA device
+_get_stream = None  # handle of a device's current stream
 
 
 def _load_torch():
-    global _DT, _KINDS, _get_device
+    global _DT, _KINDS, _get_device, _get_stream
     import torch
     _DT = {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}
     _KINDS = {"f32": (torch.float32,), "i32": (torch.int32,), "fp8": (torch.float8_e4m3fn, torch.uint8)}
-    _get_device = torch.cuda.current_device
+    # the private calls return plain numbers; a torch.cuda.Stream object alone costs 3 us to make
+    _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _refuse(status: int, where: str, msg: str):
     raise BQError(status, where, msg)
 
 
-def _same_device(where: str, *tensors):
-    """Every tensor on the current CUDA device (the one the stream belongs to)."""
+def _on_stream(where: str, stream, *tensors):
+    """Handle of `stream` (None: the current one), after checking that every tensor
+    is on the current CUDA device, the one the stream belongs to."""
     if _DT is None:
         _load_torch()
-    first = tensors[0].get_device()
+    device = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.get_device() != first or first < 0):
-            if not t.is_cuda:
-                _refuse(2, where, f"a tensor is on {t.device}, not on a CUDA device")
-            _refuse(2, where, f"tensors are on cuda:{first} and {t.device}")
-    if first != _get_device():
-        _refuse(2, where, f"the tensors are on cuda:{first}, the current device is cuda:{_get_device()}")
+        if t is not None and t.get_device() != device:
+            _refuse(2, where, f"tensors are on {tensors[0].device} and {t.device}")
+    if device < 0:
+        _refuse(2, where, f"a tensor is on {tensors[0].device}, not on a CUDA device")
+    if device != _get_device():
+        _refuse(2, where, f"the tensors are on cuda:{device}, the current device is cuda:{_get_device()}")
+    return _get_stream(device) if stream is None else stream.cuda_stream
 
 
 def _rows_of(where: str, what: str, t, rows=None, cols=None, dtype=None):
@@ -452,26 +450,26 @@ def moe_dispatch(x, inv, xs, stream=None):
     type (fp32, fp16, bf16), rows 16-byte aligned; inv int32 [T, k] or [T*k] from
     moe_permute (-1: a dropped pair)."""
     where = "bq_moe_dispatch"
-    _same_device(where, x, inv, xs)
+    st = _on_stream(where, stream, x, inv, xs)
     px, dt, t, h, ldx = _rows_of(where, "x", x)
     if t == 0:
         return xs
     pi, k = _pairs(where, inv, t)
     po, _, _, _, ldo = _rows_of(where, "xs", xs, t * k, h, dt)
-    _check(_lib.bq_moe_dispatch(px, dt, t, h, ldx, pi, k, po, ldo, _stream(stream)), where)
+    _check(_lib.bq_moe_dispatch(px, dt, t, h, ldx, pi, k, po, ldo, st), where)
     return xs
 
 
 def moe_dispatch_backward(dxs, inv, dx, stream=None):
     """Gradient of moe_dispatch: dx[t] = sum_j dxs[inv[t][j]] (fp32 sum, slot order)."""
     where = "bq_moe_dispatch_backward"
-    _same_device(where, dxs, inv, dx)
+    st = _on_stream(where, stream, dxs, inv, dx)
     po, dt, t, h, ldo = _rows_of(where, "dx", dx)
     if t == 0:
         return dx
     pi, k = _pairs(where, inv, t)
     px, _, _, _, ldx = _rows_of(where, "dxs", dxs, t * k, h, dt)
-    _check(_lib.bq_moe_dispatch_backward(px, dt, t, h, ldx, pi, k, po, ldo, _stream(stream)), where)
+    _check(_lib.bq_moe_dispatch_backward(px, dt, t, h, ldx, pi, k, po, ldo, st), where)
     return dx
 
 
@@ -479,14 +477,14 @@ def moe_combine(ys, inv, weights, y, accumulate: bool = False, stream=None):
     """Rows back in token order: y[t] = sum_j weights[t][j] * ys[inv[t][j]], with
     accumulate y[t] += that.  ys [T*k, H], y [T, H] of one type; weights fp32 [T, k]."""
     where = "bq_moe_combine"
-    _same_device(where, ys, inv, weights, y)
+    st = _on_stream(where, stream, ys, inv, weights, y)
     po, dt, t, h, ldo = _rows_of(where, "y", y)
     if t == 0:
         return y
     pi, k = _pairs(where, inv, t)
     px, _, _, _, ldx = _rows_of(where, "ys", ys, t * k, h, dt)
     pw = _dense(where, "weights", weights, (t, k), "f32")
-    _check(_lib.bq_moe_combine(px, dt, t, h, ldx, pi, pw, k, int(bool(accumulate)), po, ldo, _stream(stream)), where)
+    _check(_lib.bq_moe_combine(px, dt, t, h, ldx, pi, pw, k, int(bool(accumulate)), po, ldo, st), where)
     return y
 
 
@@ -495,7 +493,7 @@ def moe_combine_backward(dy, ys, inv, weights, dys, dweights, stream=None):
     dweights[t][j] = <dy[t], ys[inv[t][j]]>.  dys or dweights may be None (not
     computed; then weights, or ys, may be None too)."""
     where = "bq_moe_combine_backward"
-    _same_device(where, dy, ys, inv, weights, dys, dweights)
+    st = _on_stream(where, stream, dy, ys, inv, weights, dys, dweights)
     pg, dt, t, h, ldg = _rows_of(where, "dy", dy)
     if t == 0:
         return dys, dweights
@@ -508,7 +506,7 @@ def moe_combine_backward(dy, ys, inv, weights, dys, dweights, stream=None):
         po, _, _, _, ldo = _rows_of(where, "dys", dys, t * k, h, dt)
     pw = None if weights is None else _dense(where, "weights", weights, (t, k), "f32")
     pd = None if dweights is None else _dense(where, "dweights", dweights, (t, k), "f32")
-    _check(_lib.bq_moe_combine_backward(pg, ldg, px, ldx, dt, t, h, pi, pw, k, po, ldo, pd, _stream(stream)), where)
+    _check(_lib.bq_moe_combine_backward(pg, ldg, px, ldx, dt, t, h, pi, pw, k, po, ldo, pd, st), where)
     return dys, dweights
 
 
@@ -518,12 +516,12 @@ def quant_fp8_b128(x, q, scales, n_rows=None, stream=None):
     [rows, ceil(k/128)].  n_rows: optional int32 device tensor of one element, the
     number of rows to quantise (the others are left as they are)."""
     where = "bq_quant_fp8_b128"
-    _same_device(where, x, q, scales, n_rows)
+    st = _on_stream(where, stream, x, q, scales, n_rows)
     px, dt, r, k, ldx = _rows_of(where, "x", x)
     pq = _dense(where, "q", q, (r, k), "fp8")
     ps = _dense(where, "scales", scales, (r, -(-k // 128)), "f32")
     pn = None if n_rows is None else _dense(where, "n_rows", n_rows.view(-1), (1,), "i32")
-    _check(_lib.bq_quant_fp8_b128(px, dt, r, k, ldx, pn, pq, ps, _stream(stream)), where)
+    _check(_lib.bq_quant_fp8_b128(px, dt, r, k, ldx, pn, pq, ps, st), where)
     return q, scales
 
 
@@ -531,14 +529,14 @@ def moe_dispatch_fp8_b128(x, inv, q, scales, stream=None):
     """moe_dispatch and quant_fp8_b128 in one pass: q [T*k, H] and scales
     [T*k, ceil(H/128)] in expert order."""
     where = "bq_moe_dispatch_fp8_b128"
-    _same_device(where, x, inv, q, scales)
+    st = _on_stream(where, stream, x, inv, q, scales)
     px, dt, t, h, ldx = _rows_of(where, "x", x)
     if t == 0:
         return q, scales
     pi, k = _pairs(where, inv, t)
     pq = _dense(where, "q", q, (t * k, h), "fp8")
     ps = _dense(where, "scales", scales, (t * k, -(-h // 128)), "f32")
-    _check(_lib.bq_moe_dispatch_fp8_b128(px, dt, t, h, ldx, pi, k, pq, ps, _stream(stream)), where)
+    _check(_lib.bq_moe_dispatch_fp8_b128(px, dt, t, h, ldx, pi, k, pq, ps, st), where)
     return q, scales
 
 
@@ -564,9 +562,9 @@ def mm_fp8_b128(x, x_scales, w, w_scales, y, swiglu: bool = False, stream=None):
     one scale per 128 x 128 block; y [m, n] fp32, fp16 or bf16.  swiglu: w holds n/2
     gate rows and n/2 up rows, y [m, n/2] = silu(gate) * up."""
     where = "bq_mm_fp8_b128"
-    _same_device(where, x, x_scales, w, w_scales, y)
+    st = _on_stream(where, stream, x, x_scales, w, w_scales, y)
     px, pxs, m, pw, pws, n, k, sw, py, dt, ldy = _product(where, x, x_scales, w, w_scales, y, swiglu, False)
-    _check(_lib.bq_mm_fp8_b128(px, pxs, m, pw, pws, n, k, sw, py, dt, ldy, _stream(stream)), where)
+    _check(_lib.bq_mm_fp8_b128(px, pxs, m, pw, pws, n, k, sw, py, dt, ldy, st), where)
     return y
 
 
@@ -575,9 +573,9 @@ def moe_mm_fp8_b128(x, x_scales, offsets, w, w_scales, y, swiglu: bool = False, 
     take w[e].  w [E, n, k], w_scales [E, ceil(n/128), ceil(k/128)], offsets int32
     [E + 1] from moe_permute.  Rows of y behind offsets[E] are left as they are."""
     where = "bq_moe_mm_fp8_b128"
-    _same_device(where, x, x_scales, offsets, w, w_scales, y)
+    st = _on_stream(where, stream, x, x_scales, offsets, w, w_scales, y)
     px, pxs, m, pw, pws, n, k, sw, py, dt, ldy = _product(where, x, x_scales, w, w_scales, y, swiglu, True)
     e = w.shape[0]
     po = _dense(where, "offsets", offsets, (e + 1,), "i32")
-    _check(_lib.bq_moe_mm_fp8_b128(px, pxs, m, po, e, pw, pws, n, k, sw, py, dt, ldy, _stream(stream)), where)
+    _check(_lib.bq_moe_mm_fp8_b128(px, pxs, m, po, e, pw, pws, n, k, sw, py, dt, ldy, st), where)
     return y
