@@ -549,9 +549,10 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
 // multiply-adds (packed ones cost moves that pair the loaded registers) 37.7 ->
 // 37.3; a block's wait and first load before the last sums of the block before
 // it, scales loaded two blocks ahead 37.3 -> 30.7 (2.2 PFLOP/s; 8192 rows 2.7).
-// A pair of CTAs sharing the weight rows (cta_group::2) fills a third less
-// shared memory per block and took the same time (30.4; 8192 rows 103.6
-// against 101.4), so there is none.
+// A pair of CTAs sharing the weight rows (cta_group::2), which fills a third
+// less shared memory per block, took the same time (30.4; 8192 rows 103.6
+// against 101.4), and so did one MMA of 256 columns in place of the two halves
+// (31.9; K = 8192 30.1 against 31.2): neither is kept.
 constexpr int kWideThreads = 384;
 constexpr int kWideRegs = 224, kControlRegs = 56;   // 256 * 224 + 128 * 56 = 384 * 168, what the launch holds
 static_assert(256 * kWideRegs + 128 * kControlRegs <= kWideThreads * 168, "registers");
@@ -966,7 +967,10 @@ bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32
         e = swiglu ? launch_lanes<true>(map_w, map_x, a, items, split, st)
                    : launch_lanes<false>(map_w, map_x, a, items, split, st);
     }
-    if (e != cudaSuccess) return bq::fail(BQ_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
+    if (e != cudaSuccess) {
+        cudaGetLastError();   // reported here
+        return bq::fail(BQ_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
+    }
     bq::note_launch();
     return bq::check_launch(name);
 }

@@ -7,7 +7,10 @@
 //   combine            y[t] (+)= sum_j w[t][j] ys[inv[t][j]]
 //   combine backward   dys[inv[t][j]] = w[t][j] dy[t],  dw[t][j] = <dy[t], ys[inv[t][j]]>
 //
-// Every kernel is bound by memory.  Going by token rather than by sorted row
+// Every kernel is bound by memory (GB300: dispatch backward 19.8 us, 5.9 TB/s,
+// at 2048 tokens x 6 rows of 4096 bf16; combine 23.6 us, 6.4 TB/s, at 2047 x 8
+// rows of 2048 fp32; its backward pass 23.4 us, 6.1 TB/s, at 2048 x 8 rows of
+// 2048 bf16; a decode step's call 1.5 to 2 us).  Going by token rather than by sorted row
 // reads or writes the token's row once instead of k times, and the k sorted
 // rows exactly once; no thread shares an output, so there are no atomics and
 // every sum has a fixed order.
@@ -60,7 +63,8 @@ dispatch_kernel(const uint8_t* __restrict__ x, int64_t ldx, int T, int vecs, con
         if (r[j] >= 0) reinterpret_cast<uint4*>(xs + r[j] * ldxs)[c] = v;
 }
 
-// One vector of y[t].  weights NULL: a plain sum.
+// One vector of y[t].  weights NULL: a plain sum.  Streaming loads and stores: what is read once and written once does
+// not push the rest out of the L2 (2047 x 8 rows of 2048 fp32: 27.3 -> 23.6 us).
 template <int DT, int K>
 __global__ void __launch_bounds__(kThreads)
 combine_rows_kernel(const uint8_t* __restrict__ ys, int64_t ldys, int T, int vecs, const int32_t* __restrict__ inv,
@@ -78,7 +82,7 @@ combine_rows_kernel(const uint8_t* __restrict__ ys, int64_t ldys, int T, int vec
     sorted_rows(inv, t, T * K, status, r);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-        raw[j] = r[j] >= 0 ? __ldg(reinterpret_cast<const uint4*>(ys + r[j] * ldys) + c) : make_uint4(0, 0, 0, 0);
+        raw[j] = r[j] >= 0 ? __ldcs(reinterpret_cast<const uint4*>(ys + r[j] * ldys) + c) : make_uint4(0, 0, 0, 0);
         w[j] = weights ? __ldg(weights + t * K + j) : 1.f;
         if (r[j] < 0) w[j] = 0.f;   // 0 * 0 adds nothing, whatever the pair's weight is
     }
@@ -99,7 +103,7 @@ combine_rows_kernel(const uint8_t* __restrict__ ys, int64_t ldys, int T, int vec
 #pragma unroll
         for (int n = 0; n < V::N; ++n) acc[n] += f[n];
     }
-    *out = V::pack(acc);
+    __stcs(out, V::pack(acc));
 }
 
 // One CTA per token: its K rows of dys and its K weight gradients.
