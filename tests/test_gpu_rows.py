@@ -309,3 +309,46 @@ def test_the_binding_refuses_what_does_not_fit_on_the_gpu(lib):
         with pytest.raises(lib.BQError):
             call()
     assert lib.launch_count() == n
+
+
+def test_gradients_against_differences(lib):
+    """The forward calls are linear in rows and weights, so a difference over a whole step equals the gradient up to
+    rounding: (k + 2) u of the sums' size on either side of the step, and H u for the weights' gradient."""
+    import torch
+    g = np.random.default_rng(12)
+    t, k, h = 9, 4, 128
+    inv = routing(g, t, k, 0.2)
+    d_inv = dev(inv)
+    (ys, ys64), (dy, dy64), (x, _), (dxs, dxs64) = (rows(g, s, "f32") for s in ((t * k, h), (t, h), (t, h), (t * k, h)))
+    w = dev(g.uniform(0.1, 1, (t, k)).astype(np.float32))
+    dys, dw = torch.zeros_like(ys), torch.empty_like(w)
+    lib.moe_combine_backward(dy, ys, d_inv, w, dys, dw)
+
+    def loss(ys_, w_):
+        y = torch.empty_like(dy)
+        lib.moe_combine(ys_, d_inv, w_, y)
+        return (y.double() * dy.double()).sum().item()
+
+    size = (O.combine_rows(np.abs(ys64), inv, np.full((t, k), 2.0)) * np.abs(dy64)).sum()
+    base = loss(ys, w)
+    for a, j in ((0, 0), (4, 2), (8, 3)):
+        w2 = w.clone()
+        w2[a, j] += 1
+        step = (w2 - w)[a, j].item()
+        assert abs((loss(ys, w2) - base) - step * dw[a, j].item()) <= 4 * (h + k + 2) * U * size
+    for r, c in ((0, 0), (17, 5), (35, 127)):
+        y2 = ys.clone()
+        y2[r, c] += 1
+        step = (y2.double() - ys.double())[r, c].item()
+        assert abs((loss(y2, w) - base) - step * dys[r, c].item()) <= 4 * (k + 2) * U * (size + 2 * np.abs(dy64).max())
+    # dispatch: <dispatch(x + e), dxs> - <dispatch(x), dxs> = <e, dx>
+    dx = torch.empty_like(x)
+    lib.moe_dispatch_backward(dxs, d_inv, dx)
+    xs, xs2 = torch.zeros_like(ys), torch.zeros_like(ys)
+    e = torch.randn_like(x)
+    lib.moe_dispatch(x, d_inv, xs)
+    lib.moe_dispatch(x + e, d_inv, xs2)
+    step = (x + e).double() - x.double()
+    got = ((xs2.double() - xs.double()) * dxs.double()).sum().item()
+    bound = k * U * (np.abs(step.cpu().numpy()) * O.combine_rows(np.abs(dxs64), inv, None)).sum()
+    assert abs(got - (step * dx.double()).sum().item()) <= 2 * bound
