@@ -541,18 +541,20 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
 //               y.  They take the registers that the first warpgroup gives up:
 //               with fewer the sums spill, which made a block 2.4 times as
 //               long.
-// The MMAs of a block take 512 cycles; what bounds it is the instructions
-// around them, at two epilogue warps per scheduler (256 cycles of multiply-adds
-// a block).  Measured at 2048 x 4096 x 4096, each step on the one before: sums
-// not spilling 59.8 -> 37.7 us; loops that a whole warp runs with one lane
-// issuing, both barriers of a block tested together, plain instead of packed
-// multiply-adds (packed ones cost moves that pair the loaded registers) 37.7 ->
-// 37.3; a block's wait and first load before the last sums of the block before
-// it, scales loaded two blocks ahead 37.3 -> 30.7 (2.2 PFLOP/s; 8192 rows 2.7).
-// A pair of CTAs sharing the weight rows (cta_group::2), which fills a third
-// less shared memory per block, took the same time (30.4; 8192 rows 103.6
-// against 101.4), and so did one MMA of 256 columns in place of the two halves
-// (31.9; K = 8192 30.1 against 31.2): neither is kept.
+// In the long run a block of 128 x 256 x 128 takes 0.36 us of an SM, 0.91 of
+// twice the measured bf16 rate, and the MMAs bound it: without the multiply-
+// adds it takes as long, with a quarter of the MMAs 0.32 us.  On top come the
+// rounds of tiles (2048 x 4096 x 4096: 256 on 152 SMs) and about 6 us of
+// launch, first loads and last stores.  Measured at 2048 x 4096 x 4096, each
+// step on the one before: sums not spilling 59.8 -> 37.7 us; loops that a whole
+// warp runs with one lane issuing, both barriers of a block tested together,
+// plain instead of packed multiply-adds (packed ones cost moves that pair the
+// loaded registers) 37.7 -> 37.3; a block's wait and first load before the last
+// sums of the block before it, scales loaded two blocks ahead 37.3 -> 30.9 (2.2
+// PFLOP/s; 8192 rows 2.7).  No faster, and not kept: a pair of CTAs sharing the
+// weight rows (cta_group::2, 30.4 to 33), one MMA of 256 columns in place of
+// the two halves (31.8), one warp issuing both halves (40.3), tiles of 224
+// columns, which fill the second round (31.7).
 constexpr int kWideThreads = 384;
 constexpr int kWideRegs = 224, kControlRegs = 56;   // 256 * 224 + 128 * 56 = 384 * 168, what the launch holds
 static_assert(256 * kWideRegs + 128 * kControlRegs <= kWideThreads * 168, "registers");
