@@ -384,17 +384,17 @@ def _refuse(status: int, where: str, msg: str):
     raise BQError(status, where, msg)
 
 
-def _on_stream(where: str, stream, *tensors):
+def _on_stream(where: str, stream, first, *tensors):
     """Handle of `stream` (None: the current one), after checking that every tensor
     is on the current CUDA device, the one the stream belongs to."""
     if _DT is None:
         _load_torch()
-    device = tensors[0].get_device()
+    device = first.get_device()
     for t in tensors:
         if t is not None and t.get_device() != device:
-            _refuse(2, where, f"tensors are on {tensors[0].device} and {t.device}")
+            _refuse(2, where, f"tensors are on {first.device} and {t.device}")
     if device < 0:
-        _refuse(2, where, f"a tensor is on {tensors[0].device}, not on a CUDA device")
+        _refuse(2, where, f"a tensor is on {first.device}, not on a CUDA device")
     if device != _get_device():
         _refuse(2, where, f"the tensors are on cuda:{device}, the current device is cuda:{_get_device()}")
     return _get_stream(device) if stream is None else stream.cuda_stream
@@ -405,19 +405,25 @@ def _rows_of(where: str, what: str, t, rows=None, cols=None, dtype=None):
     if _DT is None:
         _load_torch()
     shape = t.shape
-    if len(shape) != 2 or (rows is not None and shape != (rows, cols or shape[1])):
-        want = f"[{'rows' if rows is None else rows}, {'columns' if cols is None else cols}]"
-        _refuse(2, where, f"{what} has shape {list(shape)}, expected {want}")
+    if rows is None:
+        if len(shape) != 2:
+            _refuse(2, where, f"{what} has shape {list(shape)}, expected [rows, columns]")
+    elif shape != (rows, cols):
+        _refuse(2, where, f"{what} has shape {list(shape)}, expected [{rows}, {cols}]")
     dt = _DT.get(t.dtype)
     if dt is None or (dtype is not None and dt != dtype):
         _refuse(4, where, f"{what} has type {t.dtype}")
     r, c = shape
-    ld, step = t.stride()
-    if step != 1 and c > 1:
-        _refuse(3, where, f"the rows of {what} are not contiguous (strides {(ld, step)})")
+    ld = c
+    if not t.is_contiguous():
+        ld, step = t.stride()
+        if step != 1 and c > 1:
+            _refuse(3, where, f"the rows of {what} are not contiguous (strides {(ld, step)})")
+        if r <= 1:
+            ld = c
     if r > 0x7fffffff or c > 0x7fffffff:
         _refuse(2, where, f"{what} has shape {list(shape)}")
-    return t.data_ptr(), dt, r, c, ld if r > 1 else c
+    return t.data_ptr(), dt, r, c, ld
 
 
 def _dense(where: str, what: str, t, shape, kind: str):
@@ -439,7 +445,10 @@ def _pairs(where: str, inv, t: int):
     if inv.dtype not in _KINDS["i32"]:
         _refuse(4, where, f"inv has type {inv.dtype}")
     shape = inv.shape
-    k, rest = (shape[1], shape[0] - t) if len(shape) == 2 else divmod(shape[0], t) if len(shape) == 1 else (0, 1)
+    if len(shape) == 2:
+        k, rest = shape[1], shape[0] - t
+    else:
+        k, rest = divmod(shape[0], t) if len(shape) == 1 else (0, 1)
     if rest or not inv.is_contiguous():
         _refuse(2, where, f"inv has shape {list(shape)} and strides {tuple(inv.stride())} for {t} tokens")
     return inv.data_ptr(), k
