@@ -376,3 +376,57 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(lib, m, n, 
     lib.mm_fp8_b128(*a)
     assert lib.device_status() == lib.DEV_OK
     check(a[-1], *expected(x, xs, w[0], ws[0], "f32"))
+
+
+@pytest.mark.parametrize("experts", [0, 1000])
+def test_rows_and_outputs_beyond_32_bit_offsets(lib, experts):
+    """x of more than 2^32 bytes and y of more than 2^31 bytes, of one weight and of 1000: rows from the start, the middle
+    and the end."""
+    import torch
+    m, n, k = 4_300_000, 256, 1008
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB of free device memory")
+    g = np.random.default_rng(40)
+    kb = 8
+    base, x, xs = fp8_rows(g, 1000, k)
+    codes, scales = dev(base).repeat(m // 1000, 1), dev(xs).repeat(m // 1000, 1)
+    e = max(experts, 1)
+    w, ws = fp8_weight(g, e, n, k)
+    y = torch.empty(m, n, dtype=torch.float16, device="cuda")
+    if experts:
+        off = torch.arange(0, m + 1, m // e, device="cuda", dtype=torch.int32)      # 4300 rows each
+        lib.moe_mm_fp8_b128(codes, scales, off, dev(w), dev(ws), y)
+    else:
+        lib.mm_fp8_b128(codes, scales, dev(w[0]), dev(ws[0]), y)
+    assert scales.shape[1] == kb
+    for r in (0, 2_150_000, m - 1000):
+        for a in range(r, r + 1000, 100):      # pieces of 100 rows lie within one expert
+            i = a // (m // e) if experts else 0
+            check(y[a:a + 100], *expected(x[a - r:a - r + 100], xs[a - r:a - r + 100], w[i], ws[i], "f16"), f"row {a}")
+    assert lib.device_status() == lib.DEV_OK
+
+
+@pytest.mark.parametrize("each", [1, 45])
+def test_weights_beyond_32_bit_offsets(lib, each):
+    """300 experts of 4096 x 4096: 5 GB; the first, the last and one behind 2^32 bytes hold values, the others zeros.
+    A row each takes the tile with the weights on the lanes, 45 the wide one."""
+    import torch
+    e, n, k = 300, 4096, 4096
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB of free device memory")
+    g = np.random.default_rng(41)
+    some, (codes, scales) = [0, 270, 299], fp8_weight(g, 3, n, k)
+    w = torch.zeros(e, n, k, dtype=torch.uint8, device="cuda")
+    ws = torch.ones(e, 32, 32, device="cuda")
+    for j, i in enumerate(some):
+        w[i], ws[i] = dev(codes[j]), dev(scales[j])
+    xc, x, xs = fp8_rows(g, e * each, k)
+    off = torch.arange(0, e * each + 1, each, dtype=torch.int32, device="cuda")
+    y = torch.full((e * each, n), 7.0, device="cuda")
+    lib.moe_mm_fp8_b128(dev(xc), dev(xs), off, w, ws, y)
+    zero = torch.ones(e * each, dtype=torch.bool, device="cuda")
+    for j, i in enumerate(some):
+        a, b = i * each, (i + 1) * each
+        zero[a:b] = False
+        check(y[a:b], *expected(x[a:b], xs[a:b], codes[j], scales[j], "f32"), f"expert {i}")
+    assert (y[zero] == 0).all()

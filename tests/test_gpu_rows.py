@@ -352,3 +352,40 @@ def test_gradients_against_differences(lib):
     got = ((xs2.double() - xs.double()) * dxs.double()).sum().item()
     bound = k * U * (np.abs(step.cpu().numpy()) * O.combine_rows(np.abs(dxs64), inv, None)).sum()
     assert abs(got - (step * dx.double()).sum().item()) <= 2 * bound
+
+
+def test_rows_beyond_32_bit_offsets(lib):
+    """Sorted matrices of more than 2^31 elements: every row against the token's row it came from."""
+    import torch
+    t, k, h = 270_000, 4, 2048                     # 2.2 G elements, 4.4 GB
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB of free device memory")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(t, h, generator=gen, device="cuda", dtype=torch.bfloat16)
+    inv = torch.randperm(t * k, generator=gen, device="cuda").int().view(t, k)
+    xs = torch.empty(t * k, h, device="cuda", dtype=torch.bfloat16)
+    lib.moe_dispatch(x, inv, xs)
+    for j in range(k):
+        for a in range(0, t, 90_000):
+            assert torch.equal(xs[inv[a:a + 90_000, j].long()], x[a:a + 90_000])
+    w = torch.rand(t, k, generator=gen, device="cuda")
+    y = torch.empty_like(x)
+    lib.moe_combine(xs, inv, w, y)                 # every term is x[t]: y = (sum of weights) x, fp32, rounded once
+    some = torch.tensor([0, 1, t // 2, t - 2, t - 1], device="cuda")
+    want = (w[some].double().sum(1, keepdim=True) * x[some].double())
+    assert ((y[some].double() - want).abs() <= (HALF["bf16"] + 2 * k * U) * want.abs() * 1.001 + SUB["bf16"]).all()
+    dys, dw = xs, torch.empty_like(w)              # the last rows of dys and dw
+    ys = torch.empty_like(xs)
+    lib.moe_dispatch(x, inv, ys)
+    lib.moe_combine_backward(x, ys, inv, w, dys, dw)
+    want = (w[some].double()[..., None] * x[some].double()[:, None])
+    assert ((dys[inv[some].long()].double() - want).abs() <= (HALF["bf16"] + U) * want.abs() * 1.001 + SUB["bf16"]).all()
+    sq = x[some].double().square().sum(1, keepdim=True).expand(-1, k)
+    assert ((dw[some].double() - sq).abs() <= h * U * sq).all()
+    del dys, xs
+    q, s = torch.empty(t * k, h, dtype=torch.uint8, device="cuda"), torch.empty(t * k, h // 128, device="cuda")
+    lib.quant_fp8_b128(ys, q, s)
+    for r in (0, t * k // 2, t * k - 3):
+        want_q, want_s = O.quant_fp8_rows(ys[r:r + 3].double().cpu().numpy())
+        np.testing.assert_array_equal(s[r:r + 3].cpu().numpy(), want_s)
+        np.testing.assert_array_equal(O.e4m3_value(q[r:r + 3].cpu().numpy()), want_q)
