@@ -133,7 +133,7 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ float peer_load(uint32_t addr, uint32_t rank) {
     float v;
     asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
-                 : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+                 : "=f"(v) : "r"(addr), "r"(rank));
     return v;
 }
 
@@ -490,20 +490,33 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
             const int quarter = warp & 3, p = 32 * quarter + lane;
             const Item it = Items(first, step, items, w_tiles).get(chunks, a.E);
             const int c = SWIGLU ? 64 * it.tile + 16 * quarter + (lane & 15) : 128 * it.tile + p;
-            for (int t = rank; t < it.rows; t += split) {
-                float part[kMaxCluster];
+            constexpr int kAtOnce = 4;   // rows whose loads are in flight together
+            for (int t0 = rank; t0 < it.rows; t0 += kAtOnce * split) {
+                float part[kAtOnce][kMaxCluster] = {};
 #pragma unroll
-                for (int r = 0; r < kMaxCluster; ++r)
-                    part[r] = r < split ? peer_load(smem_u32(smem) + 4 * (t * 128 + p), r) : 0.f;
-                float v = part[0];
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const uint32_t at = ring + 4 * ((t0 + j * split) * 128 + p);
+                    if (t0 + j * split >= it.rows) break;
 #pragma unroll
-                for (int r = 1; r < kMaxCluster; ++r) v += part[r];
-                if (SWIGLU) {
-                    const float u = __shfl_xor_sync(0xffffffffu, v, 16);
-                    v = silu_f(v) * u;
+                    for (int r = 0; r < kMaxCluster; ++r) {
+                        if (r >= split) break;
+                        part[j][r] = peer_load(at, r);
+                    }
                 }
-                if (c < a.cols && (!SWIGLU || lane < 16))
-                    bq::store_value(a.y, (int64_t)(it.row0 + t) * a.ldy + c, a.ydtype, v);
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j) {
+                    const int t = t0 + j * split;
+                    if (t >= it.rows) break;
+                    float v = part[j][0];
+#pragma unroll
+                    for (int r = 1; r < kMaxCluster; ++r) v += part[j][r];
+                    if (SWIGLU) {
+                        const float u = __shfl_xor_sync(0xffffffffu, v, 16);
+                        v = silu_f(v) * u;
+                    }
+                    if (c < a.cols && (!SWIGLU || lane < 16))
+                        bq::store_value(a.y, (int64_t)(it.row0 + t) * a.ldy + c, a.ydtype, v);
+                }
             }
         }
         __syncwarp();
