@@ -1021,12 +1021,17 @@ bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32
         e = swiglu ? launch_wide<true>(map_w, map_x, a, items, st) : launch_wide<false>(map_w, map_x, a, items, st);
     } else {
         // K split over a cluster while all clusters are resident at once (this GPU holds 76, 36 and 15 clusters of 2, 4
-        // and 8 CTAs of this size) and a CTA keeps two blocks.  n = k = 4096, one row: 10.6 / 7.2 / 5.6 us for 1, 2 and
-        // 4, and 12.6 for 8, which takes two waves.
+        // and 8 CTAs of this size) and the blocks saved pay for the cluster's sum, whose cost goes with the rows.
+        // n = k = 4096, one row: 10.4 / 7.2 / 5.6 us for 1, 2 and 4, and 12.6 for 8, which takes two waves.  Eight blocks:
+        // 32 x 1024 x 1024 4.6 us for 8 and 5.2 for 4, 32 x 4096 x 1024 5.5 for 4 and for 1.  Six, n = 1024: 4.2 for 4
+        // and 4.4 for 1 with 8 rows, 5.1 and 4.8 with 32.  A cluster of 2 gains little from many rows: 32 x 8192 6.5 us
+        // against 5.6 unsplit at k = 1024, 7.4 against 7.3 at 2048 and 9.4 against 11.0 at 4096; 4 rows 4.8 against 5.1
+        // already at 1024.
+        const bool few = rows <= 8;
         int split = 1;
-        if (items <= 15 && kb >= 16) split = 8;
-        else if (items <= 36 && kb >= 8) split = 4;
-        else if (items <= 76 && kb >= 4) split = 2;
+        if (items <= 15 && kb >= 8) split = 8;
+        else if (items <= 36 && kb >= (few ? 6 : 8)) split = 4;
+        else if (items <= 76 && kb >= (few ? 8 : 16)) split = 2;
         e = swiglu ? launch_lanes<true>(map_w, map_x, a, items, split, st)
                    : launch_lanes<false>(map_w, map_x, a, items, split, st);
     }

@@ -97,6 +97,28 @@ def test_dense_product_with_swiglu(lib, m, n, k, out):
     check(y, *expected(x, xs, w[0], ws[0], out, True), f"swiglu {m}x{n}x{k}")
 
 
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("m", [1, 8, 31])
+@pytest.mark.parametrize("n", [14 * 128, 15 * 128, 16 * 128, 36 * 128, 38 * 128, 76 * 128, 78 * 128])
+@pytest.mark.parametrize("k", [640, 656, 912, 1936])
+def test_borders_of_the_split_over_k(lib, m, n, k, swiglu):
+    """Parts of one block, of unequal sizes and with a short last block; a part's adds and those over the cluster are
+    together at most kb, the bound's count."""
+    import torch
+    g = np.random.default_rng(m + n + k)
+    codes, x, xs = fp8_rows(g, m, k)
+    w, ws = fp8_weight(g, 1, n, k)
+    y = torch.full((m, n // 2 if swiglu else n), float("nan"), dtype=torch.float32, device="cuda")
+    if swiglu and n % 256:   # gate and up halves would not start on a block of scales
+        with pytest.raises(lib.BQError, match="BQ_ERR_SHAPE"):
+            lib.mm_fp8_b128(dev(codes), dev(xs), dev(w[0]), dev(ws[0]), y, swiglu=True)
+        assert torch.isnan(y).all()
+        return
+    lib.mm_fp8_b128(dev(codes), dev(xs), dev(w[0]), dev(ws[0]), y, swiglu=swiglu)
+    check(y, *expected(x, xs, w[0], ws[0], "f32", swiglu), f"{m}x{n}x{k}")
+    assert lib.device_status() == lib.DEV_OK
+
+
 def run_grouped(lib, g, counts, n, k, out, swiglu, behind=0, first=0):
     """The grouped product over experts of `counts` rows, rows 0..first and the last `behind` outside every expert."""
     import torch
