@@ -23,6 +23,7 @@ using namespace bq::tc;
 constexpr int kBlock = 128;        // K per scale, per TMA box (one 128-byte swizzle row) and per TMEM stage
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxSize = INT32_MAX - 255;   // of rows, n and k: the row or column behind the last tile is still an int
 
 struct Args {
     const float* xs;
@@ -977,6 +978,8 @@ bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32
     if (rows < 0 || n < 1 || k < 16 || k % 16)
         return bq::fail(BQ_ERR_SHAPE, "%s: %d rows, n = %d, k = %d (k must be a positive multiple of 16)", name, rows,
                         n, k);
+    if (rows > kMaxSize || n > kMaxSize || k > kMaxSize)
+        return bq::fail(BQ_ERR_SHAPE, "%s: %d rows, n = %d, k = %d: more than %d", name, rows, n, k, kMaxSize);
     if (swiglu && n % 256)
         return bq::fail(BQ_ERR_SHAPE, "%s: a gate/up weight needs n = %d to be a multiple of 256", name, n);
     if (E < 1 || E > kMaxExperts || (int64_t)E * n > (int64_t)INT32_MAX)

@@ -510,8 +510,8 @@ bq_status bq_moe_dispatch_fp8_b128(const void* x, int32_t dtype, int32_t T, int3
  * w: device uint8 [E][n][k]; wscales: device fp32 [E][ceil(n/128)]
  * [ceil(k/128)]; y: device rows of n (swiglu: n/2) elements of `ydtype`,
  * ldy elements apart.  k a multiple of 16 (a short last block is fine),
- * n >= 1 of any value (without swiglu), E * n <= 2^31 - 1, E <= 1024.  x, w
- * 16-byte aligned; scales and offsets 4-byte aligned; y aligned to its
+ * n >= 1 of any value (without swiglu), rows, n and k at most 2^31 - 256,
+ * E * n <= 2^31 - 1, E <= 1024.  x, w 16-byte aligned; scales and offsets 4-byte aligned; y aligned to its
  * element.
  * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_FORMAT, BQ_ERR_ALIGN,
  * BQ_ERR_CUDA.  No rows: a no-op.
