@@ -13,6 +13,7 @@
 #include <atomic>
 
 #include "gemm_internal.cuh"
+#include "row_chunks.cuh"
 #include "row_types.cuh"
 #include "tc_ptx.cuh"
 
@@ -149,7 +150,7 @@ __device__ __forceinline__ int chunks_of(const Args& a, int e, int most) {
         bq::set_device_error(a.status, BQ_DEV_BAD_ROW);
         return 0;
     }
-    return (hi - lo + most - 1) / most;
+    return bq::row_chunks(hi - lo, most);
 }
 
 // What the CTA keeps of it in shared memory.
@@ -165,7 +166,7 @@ __device__ __forceinline__ void count_chunks(const Args& a, int most, Chunks* ch
     if (!a.offsets) {
         if (threadIdx.x == 0) {
             ch->before[0] = ch->first[0] = 0;
-            ch->before[1] = (a.rows + most - 1) / most;
+            ch->before[1] = bq::row_chunks(a.rows, most);
             ch->first[1] = a.rows;
         }
     } else if (threadIdx.x < 32) {
@@ -239,11 +240,11 @@ struct Items {
         it.tile = rest;
         const int before = ch->before[e], chunks = ch->before[e + 1] - before;
         if (chunks > 1) {   // chunks of near-equal size, fastest
-            const int local = (chunk - before) * w_tiles + rest, size = (it.rows + chunks - 1) / chunks;
+            const int local = (chunk - before) * w_tiles + rest;
             it.tile = local / chunks;
-            const int skip = (local - it.tile * chunks) * size;
-            it.row0 += skip;
-            it.rows = min(size, it.rows - skip);
+            const bq::RowChunk part = bq::row_chunk(it.rows, chunks, local - it.tile * chunks);
+            it.row0 += part.first;
+            it.rows = part.rows;
         }
         return it;
     }
@@ -996,7 +997,7 @@ bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32
                         name);
     const int experts = offsets ? std::min(E, rows) : 1;   // that can have rows
     // most row chunks and items there can be, for the grid and (as an int) inside the kernel
-    auto chunks_of = [&](int most) { return (int64_t)(rows + most - 1) / most + (offsets ? experts : 0); };
+    auto chunks_of = [&](int most) { return (int64_t)bq::row_chunks(rows, most) + (offsets ? experts : 0); };
     auto tiles_of = [&](int width) { return (int64_t)(cols + width - 1) / width; };
     // Which kernel.  Weights on the lanes: while its items fit one wave (n = k = 4096: 128 rows 11.3 us against 15.0;
     // 192 rows, two waves, 19.4 against 14.7), and for experts of up to 16 rows on average, where both read every

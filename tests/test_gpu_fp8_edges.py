@@ -1,0 +1,49 @@
+"""GPU: the ends of the FP8 products' and the row kernels' ranges (the largest
+sizes, malformed offsets, scales whose product leaves fp32, waits that run out
+in a part of a cluster, neighbours of every code's border)."""
+import numpy as np
+import pytest
+
+import oracle as O
+
+pytestmark = pytest.mark.gpu
+
+ONE = 0x38      # the e4m3 code of 1
+
+
+def needs(gb):
+    import torch
+    if torch.cuda.mem_get_info()[0] < gb << 30:
+        pytest.skip(f"needs {gb} GB of free device memory")
+
+
+def e4m3_table():
+    import torch
+    return torch.from_numpy(O.e4m3_value(np.arange(256, dtype=np.uint8))).float().cuda()
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_as_many_rows_as_the_products_take(lib, grouped):
+    """2^31 - 256 rows of 16: y is the first value of each row (times scales of 1), exact."""
+    import torch
+    needs(72)
+    rows, k = 2 ** 31 - 256, 16
+    x = torch.zeros(rows, k, dtype=torch.uint8, device="cuda")
+    piece = 1 << 26
+    codes = (torch.arange(piece, device="cuda") % 113).to(torch.uint8)      # e4m3 codes of 0 .. 2^7
+    for a in range(0, rows, piece):
+        x[a:a + piece, 0] = codes[:min(piece, rows - a)]
+    xs = torch.ones(rows, 1, device="cuda")
+    w = torch.zeros(2, 1, k, dtype=torch.uint8, device="cuda")
+    w[:, 0, 0] = ONE
+    ws = torch.ones(2, 1, 1, device="cuda")
+    y = torch.full((rows, 1), float("nan"), dtype=torch.float16, device="cuda")
+    if grouped:
+        off = torch.tensor([0, 200, rows], dtype=torch.int32, device="cuda")
+        lib.moe_mm_fp8_b128(x, xs, off, w, ws, y)
+    else:
+        lib.mm_fp8_b128(x, xs, w[0], ws[0], y)
+    assert lib.device_status() == lib.DEV_OK
+    want = e4m3_table()[codes.long()].half()
+    for a in range(0, rows, piece):
+        assert torch.equal(y[a:a + piece, 0], want[:min(piece, rows - a)]), f"rows from {a}"
