@@ -40,7 +40,7 @@ struct Args {
     int32_t* status;
     unsigned long long wait_limit_ns;
     int skip_copies;          // test only: the producer issues no copies (waits run out)
-    int max_chunks;           // row chunks that offsets in order can make (more: overlapping, so descending, ones)
+    int max_chunks;           // row chunks that offsets in order can make
 };
 
 // ---------------------------------------------------------------- PTX used here only
@@ -155,13 +155,16 @@ __device__ __forceinline__ int chunks_of(const Args& a, int e, int most) {
 
 // What the CTA keeps of it in shared memory.
 struct Chunks {
-    int32_t before[kMaxExperts + 1];   // [e]: chunks of the experts before e, [E]: of all
+    int32_t before[kMaxExperts + 1];   // [e]: chunks of the experts before e, [E]: of all that are computed
     int32_t first[kMaxExperts + 1];    // [e]: first row of expert e, [E]: end of the last
     int32_t pad[2];                    // to a multiple of 16 bytes
 };
 static_assert(sizeof(Chunks) % 16 == 0, "what lies behind it is 16-byte aligned");
 
-// Fills it (all threads of the CTA; ends with a barrier).
+// Fills it (all threads of the CTA; ends with a barrier).  Ranges that overlap
+// (so descending offsets) can hold more chunks than max_chunks, up to 2^36:
+// the sums stop one above max_chunks, and the first expert that passes it and
+// all behind it are left out ([E] counts the experts before them).
 __device__ __forceinline__ void count_chunks(const Args& a, int most, Chunks* ch) {
     if (!a.offsets) {
         if (threadIdx.x == 0) {
@@ -171,7 +174,7 @@ __device__ __forceinline__ void count_chunks(const Args& a, int most, Chunks* ch
         }
     } else if (threadIdx.x < 32) {
         // one warp: 32 experts at a time, all loads of a group of four issued together
-        int total = 0;
+        int total = 0, used = 0;
         for (int e0 = 0; e0 < a.E; e0 += 128) {
             int c[4];
 #pragma unroll
@@ -187,14 +190,18 @@ __device__ __forceinline__ void count_chunks(const Args& a, int most, Chunks* ch
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
                     const int v = __shfl_up_sync(0xffffffffu, incl, off);
-                    if ((int)threadIdx.x >= off) incl += v;
+                    if ((int)threadIdx.x >= off) incl = bq::add_chunks(incl, v, a.max_chunks);
                 }
-                if (e < a.E) ch->before[e] = total + incl - c[i];
-                total += __shfl_sync(0xffffffffu, incl, 31);
+                incl = bq::add_chunks(total, incl, a.max_chunks);
+                const int excl = __shfl_up_sync(0xffffffffu, incl, 1);
+                if (e < a.E) ch->before[e] = threadIdx.x ? excl : total;
+                const uint32_t fit = __ballot_sync(0xffffffffu, incl <= a.max_chunks);   // the sums ascend
+                if (fit) used = __shfl_sync(0xffffffffu, incl, __popc(fit) - 1);
+                total = __shfl_sync(0xffffffffu, incl, 31);
             }
         }
         if (threadIdx.x == 0) {
-            ch->before[a.E] = total;
+            ch->before[a.E] = used;
             ch->first[a.E] = __ldg(a.offsets + a.E);
         }
     }
@@ -336,7 +343,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
 
     constexpr int kTileCols = SWIGLU ? 64 : 128;
     const int w_tiles = (a.cols + kTileCols - 1) / kTileCols;
-    const int items = min(chunks->before[a.E], a.max_chunks) * w_tiles;   // the host made sure that it is an int
+    const int items = chunks->before[a.E] * w_tiles;   // the host made sure that it is an int
     const int rank = split > 1 ? (int)cluster_rank() : 0;
     const int first = blockIdx.x / split, step = gridDim.x / split;
     const int b0 = a.kb * rank / split, b1 = a.kb * (rank + 1) / split;
@@ -694,7 +701,7 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int w_tiles = (a.cols + kTileCols - 1) / kTileCols;
-    const int items = min(chunks->before[a.E], a.max_chunks) * w_tiles;   // the host made sure that it is an int
+    const int items = chunks->before[a.E] * w_tiles;   // the host made sure that it is an int
     const int first = blockIdx.x, step = gridDim.x;
 
     if (warp < 4) {

@@ -29,4 +29,12 @@ BQ_HOST_DEVICE RowChunk row_chunk(int rows, int chunks, int i) {
     return {first, size < rows - first ? size : rows - first};
 }
 
+// a + b, or limit + 1 where the sum is more than `limit` (0 <= a, b <= limit + 1,
+// limit < 2^30).  Sums of chunks that pass the limit stay there instead of
+// wrapping, in whatever order they are added.
+BQ_HOST_DEVICE int add_chunks(int a, int b, int limit) {
+    const uint32_t sum = (uint32_t)a + (uint32_t)b;
+    return sum > (uint32_t)limit ? limit + 1 : (int)sum;
+}
+
 }  // namespace bq

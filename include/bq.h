@@ -504,7 +504,8 @@ bq_status bq_moe_dispatch_fp8_b128(const void* x, int32_t dtype, int32_t T, int3
  * offsets[e + 1]) of x take matrix e of w [E][n][k] (offsets: device int32
  * [E + 1], as bq_moe_permute writes it).  Rows outside [offsets[0],
  * offsets[E]) are not written.  Offsets that descend or leave [0, rows] set
- * BQ_DEV_BAD_ROW; the experts concerned are skipped.
+ * BQ_DEV_BAD_ROW; the experts concerned are skipped (where ranges overlap,
+ * experts behind them may be skipped too).
  *
  * x: device uint8 [rows][k]; xscales: device fp32 [rows][ceil(k/128)];
  * w: device uint8 [E][n][k]; wscales: device fp32 [E][ceil(n/128)]

@@ -17,6 +17,11 @@ def needs(gb):
         pytest.skip(f"needs {gb} GB of free device memory")
 
 
+def dev(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
 def e4m3_table():
     import torch
     return torch.from_numpy(O.e4m3_value(np.arange(256, dtype=np.uint8))).float().cuda()
@@ -47,3 +52,37 @@ def test_as_many_rows_as_the_products_take(lib, grouped):
     want = e4m3_table()[codes.long()].half()
     for a in range(0, rows, piece):
         assert torch.equal(y[a:a + piece, 0], want[:min(piece, rows - a)]), f"rows from {a}"
+
+
+def test_ranges_that_overlap_leave_whole_experts_out(lib):
+    """Offsets 0, 1024, 0, 1024: expert 1 descends, and expert 2's chunks are more than ascending offsets can make."""
+    import torch
+    g = np.random.default_rng(50)
+    rows, n, k = 1024, 1024, 256
+    x = dev(g.integers(0, 0x7F, (rows, k), dtype=np.uint8))
+    xs, ws = torch.ones(rows, 2, device="cuda"), torch.ones(3, 8, 2, device="cuda")
+    w = dev(g.integers(0, 0x7F, (3, n, k), dtype=np.uint8))
+    y, want = torch.full((rows, n), 7.0, device="cuda"), torch.empty(rows, n, device="cuda")
+    off = torch.tensor([0, rows, 0, rows], dtype=torch.int32, device="cuda")
+    lib.moe_mm_fp8_b128(x, xs, off, w, ws, y)
+    assert lib.device_status() == lib.DEV_BAD_ROW
+    lib.mm_fp8_b128(x, xs, w[0], ws[0], want)      # the same tile, so the same sums
+    assert torch.equal(y, want)
+
+
+def test_ranges_that_overlap_more_often_than_an_int_counts(lib):
+    """512 experts of all of 1.1e9 rows (of one weight, so that it does not matter which one a row gets): 4.4e9 chunks."""
+    import torch
+    needs(40)
+    rows, k, e = 1_100_000_000, 16, 1024
+    x = torch.zeros(rows, k, dtype=torch.uint8, device="cuda")
+    x[::1000, 0] = ONE
+    xs = torch.ones(rows, 1, device="cuda")
+    w = torch.zeros(e, 1, k, dtype=torch.uint8, device="cuda")
+    w[:, 0, 0] = ONE
+    y = torch.full((rows, 1), float("nan"), dtype=torch.float16, device="cuda")
+    off = torch.zeros(e + 1, dtype=torch.int32, device="cuda")
+    off[1::2] = rows
+    lib.moe_mm_fp8_b128(x, xs, off, w, torch.ones(e, 1, 1, device="cuda"), y)
+    assert lib.device_status() == lib.DEV_BAD_ROW
+    assert (y[::1000] == 1).all() and int((y == 0).sum()) == rows - rows // 1000

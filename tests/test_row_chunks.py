@@ -23,7 +23,8 @@ def chunks(tmp_path_factory):
         'extern "C" void row_chunk(int rows, int chunks, int i, int* out) {\n'
         '    const bq::RowChunk c = bq::row_chunk(rows, chunks, i);\n'
         '    out[0] = c.first; out[1] = c.rows;\n'
-        '}\n')
+        '}\n'
+        'extern "C" int add_chunks(int a, int b, int limit) { return bq::add_chunks(a, b, limit); }\n')
     subprocess.run([gxx, "-std=c++17", "-O1", "-fwrapv", "-shared", "-fPIC", "-I", CSRC, str(d / "c.cpp"), "-o",
                     str(d / "c.so")], check=True)
     return ctypes.CDLL(str(d / "c.so"))
@@ -49,3 +50,30 @@ def test_chunks_cover_the_rows(chunks, rows, most):
     for i in some:
         first, count = part(chunks, rows, n, i)
         assert first == i * size and count == min(size, rows - first) and 1 <= count <= most
+
+
+@pytest.mark.parametrize("rows", [1000, 2 ** 30, 1_100_000_000, 2 ** 31 - 256])
+@pytest.mark.parametrize("experts", [3, 300, 600, 1024])
+def test_sums_of_overlapping_ranges_stop_at_the_limit(chunks, rows, experts):
+    """Offsets 0, rows, 0, rows, ...: every other expert has all rows.  The sums ascend, are exact up to the limit and
+    stay one above it, added one after the other or as a scan does."""
+    most = 128
+    each = [chunks.row_chunks(rows, most) if e % 2 == 0 else 0 for e in range(experts)]
+    limit = chunks.row_chunks(rows, most) + min(experts, rows)     # what ascending offsets can make
+    serial, exact = [0], [0]
+    for c in each:
+        serial.append(chunks.add_chunks(serial[-1], c, limit))
+        exact.append(exact[-1] + c)
+    assert serial == [min(v, limit + 1) for v in exact]
+    scan = each[:]
+    off = 1
+    while off < experts:
+        scan = [chunks.add_chunks(scan[i], scan[i - off], limit) if i >= off else scan[i] for i in range(experts)]
+        off *= 2
+    assert scan == serial[1:]
+
+
+def test_sums_at_the_largest_limit(chunks):
+    limit = 2 ** 30 - 1
+    assert chunks.add_chunks(limit + 1, limit + 1, limit) == limit + 1
+    assert chunks.add_chunks(limit, 1, limit) == limit + 1 and chunks.add_chunks(limit, 0, limit) == limit
