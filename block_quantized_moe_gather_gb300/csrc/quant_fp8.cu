@@ -172,7 +172,7 @@ bq_status run_quant(const char* name, const void* x, int32_t dtype, int32_t rows
     if (!q || !scales) return bq::fail(BQ_ERR_NULL, "%s: q or scales is NULL", name);
     if (!bq::aligned(q, 16) || !bq::aligned(scales, 4) || !bq::aligned(n_rows, 4) || !bq::aligned(inv, 4))
         return bq::fail(BQ_ERR_ALIGN, "%s: q must be 16-byte aligned, scales, n_rows and inv 4-byte", name);
-    const int kb = (k + kGroup - 1) / kGroup;
+    const int kb = (int)(((int64_t)k + kGroup - 1) / kGroup);   // k may be within a group of 2^31
     if ((int64_t)rows * kb > (int64_t)INT32_MAX)
         return bq::fail(BQ_ERR_SHAPE, "%s: %d rows of %d groups are too many", name, rows, kb);
     const unsigned grid = (unsigned)(((int64_t)rows * kb * kLanes + kThreads - 1) / kThreads);

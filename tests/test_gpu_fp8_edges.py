@@ -86,3 +86,29 @@ def test_ranges_that_overlap_more_often_than_an_int_counts(lib):
     lib.moe_mm_fp8_b128(x, xs, off, w, torch.ones(e, 1, 1, device="cuda"), y)
     assert lib.device_status() == lib.DEV_BAD_ROW
     assert (y[::1000] == 1).all() and int((y == 0).sum()) == rows - rows // 1000
+
+
+@pytest.mark.parametrize("op", ["quant", "dispatch"])
+def test_the_longest_row_the_quantiser_takes(lib, op):
+    """One row of 2^31 - 16 values: the last group has 112."""
+    import torch
+    needs(24)
+    k = 2 ** 31 - 16
+    x = torch.ones(1, k, dtype=torch.float16, device="cuda")
+    x[0, 1] = 7.0                  # group 0: 1 -> code of 64, scale 7 / 448
+    x[0, k - 3] = 28.0             # the last group: 1 -> code of 16
+    q = torch.zeros(1, k, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(1, 2 ** 24, device="cuda")
+    if op == "quant":
+        lib.quant_fp8_b128(x, q, s)
+    else:
+        lib.moe_dispatch_fp8_b128(x, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), q, s)
+    assert lib.device_status() == lib.DEV_OK
+    want_s = torch.full_like(s, np.float32(1 / 448))
+    want_s[0, 0], want_s[0, -1] = float(np.float32(7 / 448)), float(np.float32(28 / 448))
+    assert torch.equal(s, want_s)
+    top = 0x7E                     # the code of 448
+    assert q[0, 1] == top and q[0, k - 3] == top and (q[0, 128:-112] == top).all()
+    assert (e4m3_table()[q[0, 2:128].long()] == 64).all()
+    last = e4m3_table()[q[0, -112:].long()]
+    assert int((last == 16).sum()) == 111 and last[-3] == 448
