@@ -142,10 +142,9 @@ __device__ __forceinline__ float peer_load(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.f + expf(-g)); }
 
 // ---------------------------------------------------------------- work items
-// The row chunks of every expert: a chunk is at most `most` rows, an expert's
-// rows are cut into chunks of near-equal size.
-__device__ __forceinline__ int chunks_of(const Args& a, int e, int most) {
-    const int lo = __ldg(a.offsets + e), hi = __ldg(a.offsets + e + 1);
+// The row chunks of an expert of rows [lo, hi): a chunk is at most `most`
+// rows, an expert's rows are cut into chunks of near-equal size.
+__device__ __forceinline__ int chunks_of(const Args& a, int lo, int hi, int most) {
     if (!(0 <= lo && lo <= hi && hi <= a.rows)) {
         bq::set_device_error(a.status, BQ_DEV_BAD_ROW);
         return 0;
@@ -173,33 +172,36 @@ __device__ __forceinline__ void count_chunks(const Args& a, int most, Chunks* ch
             ch->first[1] = a.rows;
         }
     } else if (threadIdx.x < 32) {
-        // one warp: 32 experts at a time, all loads of a group of four issued together
+        // one warp, four experts a lane
         int total = 0, used = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 128) {
-            int c[4];
+        for (int e0 = 4 * (int)threadIdx.x; e0 - 4 * (int)threadIdx.x < a.E; e0 += 128) {
+            int offset[5], c[4], incl = 0;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) offset[i] = __ldg(a.offsets + min(e0 + i, a.E));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int e = e0 + 32 * i + (int)threadIdx.x;
-                c[i] = e < a.E ? chunks_of(a, e, most) : 0;
-                if (e <= a.E) ch->first[e] = __ldg(a.offsets + e);
+                c[i] = e0 + i < a.E ? chunks_of(a, offset[i], offset[i + 1], most) : 0;
+                incl = bq::add_chunks(incl, c[i], a.max_chunks);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int e = e0 + 32 * i + (int)threadIdx.x;
-                int incl = c[i];
+            for (int off = 1; off < 32; off <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, off);
+                if ((int)threadIdx.x >= off) incl = bq::add_chunks(incl, v, a.max_chunks);
+            }
+            const int behind = __shfl_up_sync(0xffffffffu, incl, 1);
+            int before = threadIdx.x ? bq::add_chunks(total, behind, a.max_chunks) : total;
 #pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, incl, off);
-                    if ((int)threadIdx.x >= off) incl = bq::add_chunks(incl, v, a.max_chunks);
+            for (int i = 0; i < 4; ++i) {
+                if (e0 + i < a.E) {
+                    ch->first[e0 + i] = offset[i];
+                    ch->before[e0 + i] = before;
                 }
-                incl = bq::add_chunks(total, incl, a.max_chunks);
-                const int excl = __shfl_up_sync(0xffffffffu, incl, 1);
-                if (e < a.E) ch->before[e] = threadIdx.x ? excl : total;
-                const uint32_t fit = __ballot_sync(0xffffffffu, incl <= a.max_chunks);   // the sums ascend
-                if (fit) used = __shfl_sync(0xffffffffu, incl, __popc(fit) - 1);
-                total = __shfl_sync(0xffffffffu, incl, 31);
+                before = bq::add_chunks(before, c[i], a.max_chunks);
+                if (before <= a.max_chunks) used = before;   // the sums ascend
             }
+            total = bq::add_chunks(total, __shfl_sync(0xffffffffu, incl, 31), a.max_chunks);
         }
+        used = __reduce_max_sync(0xffffffffu, used);
         if (threadIdx.x == 0) {
             ch->before[a.E] = used;
             ch->first[a.E] = __ldg(a.offsets + a.E);
