@@ -276,12 +276,13 @@ def launch_count() -> int:
     return int(_lib.bq_launch_count())
 
 
-def test_set_wait_probe(skip_weight_copies: bool, wait_limit_ns: int = 0):
+def test_set_wait_probe(skip_weight_copies: bool, wait_limit_ns: int = 0, odd_parts_only: bool = False):
     """Test hook: GEMM launches that follow take `wait_limit_ns` as the bound of
     their barrier waits and, with `skip_weight_copies`, issue no weight copies
-    (so those waits run out); (False, 0) restores the defaults."""
-    _check(_lib.bq_test_set_wait_probe(int(bool(skip_weight_copies)), int(wait_limit_ns)),
-           "bq_test_set_wait_probe")
+    (so those waits run out), with `odd_parts_only` only in the odd parts of an
+    FP8 product's K split; (False, 0) restores the defaults."""
+    skip = int(bool(skip_weight_copies)) | (2 if odd_parts_only else 0)
+    _check(_lib.bq_test_set_wait_probe(skip, int(wait_limit_ns)), "bq_test_set_wait_probe")
 
 
 def moe_permute_noalloc(ids, n_experts: int, counts, offsets, perm_token, perm_slot, inv, stream=None):

@@ -859,8 +859,8 @@ bq_status launch_gemm_shared(const bq_qweight* gu, const bq_qweight* dn, int T, 
 }  // namespace bq
 
 extern "C" bq_status bq_test_set_wait_probe(int32_t skip_weight_copies, uint64_t wait_limit_ns) {
-    if (skip_weight_copies < 0 || skip_weight_copies > 1)
-        return bq::fail(BQ_ERR_SHAPE, "bq_test_set_wait_probe: skip_weight_copies must be 0 or 1");
+    if (skip_weight_copies != 0 && skip_weight_copies != 1 && skip_weight_copies != 3)
+        return bq::fail(BQ_ERR_SHAPE, "bq_test_set_wait_probe: skip_weight_copies must be 0, 1 or 3");
     if (wait_limit_ns == 0) wait_limit_ns = kWaitLimitNs;
     if (wait_limit_ns < 1000000ull || wait_limit_ns > kWaitLimitNs)
         return bq::fail(BQ_ERR_SHAPE, "bq_test_set_wait_probe: wait limit %llu ns outside [1 ms, 2 s]",

@@ -39,7 +39,7 @@ struct Args {
     int64_t ldy;
     int32_t* status;
     unsigned long long wait_limit_ns;
-    int skip_copies;          // test only: the producer issues no copies (waits run out)
+    int skip_copies;          // test only: the producer issues no copies (waits run out); 3: only in a part of a cluster
     int max_chunks;           // row chunks that offsets in order can make
 };
 
@@ -136,6 +136,13 @@ __device__ __forceinline__ float peer_load(uint32_t addr, uint32_t rank) {
     float v;
     asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
                  : "=f"(v) : "r"(addr), "r"(rank));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t peer_load_u32(uint32_t addr, uint32_t rank) {
+    uint32_t v;
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.u32 %0, [a];\n}\n"
+                 : "=r"(v) : "r"(addr), "r"(rank));
     return v;
 }
 
@@ -352,7 +359,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     const unsigned long long limit = a.wait_limit_ns;
 
     const bool one = elect_one();
-    bool ok = !a.skip_copies;
+    bool ok = !(a.skip_copies == 3 && split > 1 ? rank & 1 : a.skip_copies);
     if (warp == 0) {
         int s = 0, issued = 0;
         uint32_t ph = 1;   // a fresh barrier passes for the phase before its first
@@ -497,7 +504,10 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     if (split > 1) {
         __syncwarp();
         cluster_sync();
-        if (warp >= 3 && first < items && !*abort_flag) {
+        if (warp >= 3 && first < items) {
+            // a CTA whose waits ran out left no sums: then y is not written, as without a split (asked for beside the
+            // first sums, which take as long to come)
+            const uint32_t aborted = lane < split ? peer_load_u32(smem_u32(tmem_slot + 1), lane) : 0u;
             const int quarter = warp & 3, p = 32 * quarter + lane;
             const Item it = Items(first, step, items, w_tiles).get(chunks, a.E);
             const int c = SWIGLU ? 64 * it.tile + 16 * quarter + (lane & 15) : 128 * it.tile + p;
@@ -514,6 +524,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                         part[j][r] = peer_load(at, r);
                     }
                 }
+                if (__any_sync(0xffffffffu, aborted != 0)) break;
 #pragma unroll
                 for (int j = 0; j < kAtOnce; ++j) {
                     const int t = t0 + j * split;

@@ -560,8 +560,9 @@ uint64_t bq_launch_count(void);
  * `wait_limit_ns` as that limit (1 ms .. 2 s; 0 restores the 2 s default)
  * and, if `skip_weight_copies` is 1, their weight producer issues no copies,
  * so the waits for weights run out: the call then returns BQ_OK, its output
- * is undefined and bq_device_status reports BQ_DEV_WAIT_TIMEOUT.  Process
- * wide, for tests only; call bq_test_set_wait_probe(0, 0) to restore.
+ * is undefined and bq_device_status reports BQ_DEV_WAIT_TIMEOUT.  3: the same,
+ * but of an FP8 product whose K is split over a cluster only the odd parts
+ * issue none; no part of a split then writes y.  Process wide, for tests only; call bq_test_set_wait_probe(0, 0) to restore.
  * Errors: BQ_ERR_SHAPE (argument outside the ranges above).
  */
 bq_status bq_test_set_wait_probe(int32_t skip_weight_copies, uint64_t wait_limit_ns);

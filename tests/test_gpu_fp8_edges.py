@@ -112,3 +112,25 @@ def test_the_longest_row_the_quantiser_takes(lib, op):
     assert (e4m3_table()[q[0, 2:128].long()] == 64).all()
     last = e4m3_table()[q[0, -112:].long()]
     assert int((last == 16).sum()) == 111 and last[-3] == 448
+
+
+@pytest.mark.parametrize("m,n,k,swiglu", [(1, 4096, 4096, False), (3, 256, 1024, False), (32, 512, 1024, True),
+                                          (8, 8192, 2048, False)])
+def test_a_wait_that_runs_out_in_one_part_of_a_split_leaves_y(lib, m, n, k, swiglu):
+    """K split over 4, 8, 8 and 2 parts, the odd ones without copies: the others have their sums, y is not written."""
+    import torch
+    g = np.random.default_rng(51)
+    x, w = dev(g.integers(0, 0x7F, (m, k), dtype=np.uint8)), dev(g.integers(0, 0x7F, (n, k), dtype=np.uint8))
+    xs, ws = torch.ones(m, k // 128, device="cuda"), torch.ones(n // 128, k // 128, device="cuda")
+    y, want = (torch.full((m, n // 2 if swiglu else n), 7.0, device="cuda") for _ in range(2))
+    lib.test_set_wait_probe(True, 2_000_000, odd_parts_only=True)
+    try:
+        lib.mm_fp8_b128(x, xs, w, ws, y, swiglu=swiglu)
+        assert lib.device_status() == lib.DEV_WAIT_TIMEOUT
+    finally:
+        lib.test_set_wait_probe(False)
+    assert (y == 7).all()
+    lib.mm_fp8_b128(x, xs, w, ws, y, swiglu=swiglu)
+    lib.mm_fp8_b128(x, xs, w, ws, want, swiglu=swiglu)
+    assert lib.device_status() == lib.DEV_OK
+    assert torch.equal(y, want) and (y != 7).all()
