@@ -327,6 +327,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     const uint32_t drain = bar0 + 8u * (2 * S + 3 * A);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + M::kNumBars);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    volatile uint32_t* filled = tmem_slot + 2;   // stages that the producer has filled
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -386,11 +387,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                 if (++s == S) { s = 0; ph ^= 1u; }
             }
         }
-        if (!ok) {   // copies in flight land before the CTA leaves (bounded)
-            volatile uint32_t no_abort = 0;
-            for (int u = max(0, issued - S); u < issued; ++u)
-                mbar_wait(full(u % S), (u / S) & 1, &no_abort, a.status, limit);
-        }
+        if (one) *filled = issued;
     } else if (warp == 1) {
         const uint64_t wd0 = smem_desc_sw128(ring), xd0 = smem_desc_sw128(ring + M::kWBytes);
         int s = 0, q = 0;
@@ -414,11 +411,6 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                 if (++s == S) { s = 0; ph ^= 1u; }
                 if (++q == A) { q = 0; aph ^= 1u; }
             }
-        }
-        if (!ok && one) {   // our MMAs end before the TMEM is freed (bounded)
-            volatile uint32_t no_abort = 0;
-            mma_commit(drain);
-            mbar_wait(drain, 0, &no_abort, a.status, limit);
         }
     } else if (warp == 2) {
         int q = 0;
@@ -546,6 +538,18 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     }
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag) {   // a warp gave up: what the others started ends before the memory it uses is freed (bounded)
+        volatile uint32_t no_abort = 0;
+        if (warp == 0) {
+            const int issued = *filled;
+            for (int u = max(0, issued - S); u < issued; ++u)
+                mbar_wait(full(u % S), (u / S) & 1, &no_abort, a.status, limit);
+        } else if (warp == 1 && elect_one()) {
+            mma_commit(drain);
+            mbar_wait(drain, 0, &no_abort, a.status, limit);
+        }
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
@@ -604,7 +608,7 @@ struct WideSmem {
     static constexpr int kTiles = S * kStage;
     static constexpr int kOut = kTiles + (int)sizeof(Chunks);       // the epilogue warps' pieces of y
     static constexpr int kBars = kOut + 8 * 16 * kOutRow;           // 16-byte aligned: the slots' barriers differ in bit 3
-    static constexpr int kNumBars = 2 * S + 4 * A + 1;
+    static constexpr int kNumBars = 2 * S + 4 * A + 2;
     static constexpr int kBytes = 1024 + kBars + 8 * kNumBars + 16;
 };
 static_assert(WideSmem::kBytes <= 232448 && WideSmem::kBars % 16 == 0 && WideSmem::S % 2 == 0, "smem");
@@ -688,15 +692,17 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     auto empty = [&](int s) { return bar0 + 8u * (S + s); };
     auto acc_full = [&](int half, int q) { return bar0 + 8u * (2 * S + A * half + q); };
     auto acc_empty = [&](int half, int q) { return bar0 + 8u * (2 * S + A * (2 + half) + q); };
-    const uint32_t drain = bar0 + 8u * (2 * S + 4 * A);
+    auto drain = [&](int half) { return bar0 + 8u * (2 * S + 4 * A + half); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + M::kNumBars);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    volatile uint32_t* filled = tmem_slot + 2;   // stages that the producer has filled
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) { mbar_init(full(i), 1); mbar_init(empty(i), 2); }
         for (int i = 0; i < 2 * A; ++i) { mbar_init(acc_full(0, i), 1); mbar_init(acc_empty(0, i), 4); }
-        mbar_init(drain, 2);
+        mbar_init(drain(0), 1);
+        mbar_init(drain(1), 1);
         *abort_flag = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -746,11 +752,7 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
             }
-            if (!ok) {   // copies in flight land before the CTA leaves (bounded)
-                volatile uint32_t no_abort = 0;
-                for (int u = max(0, issued - S); u < issued; ++u)
-                    mbar_wait(full(u % S), (u / S) & 1, &no_abort, a.status, a.wait_limit_ns);
-            }
+            if (one) *filled = issued;
         } else if (warp < 3) {
             // Lean: what one warp does per block, in order, bounds the MMA rate.
             const int half = warp - 1;
@@ -789,11 +791,6 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                     stage_full = full(0);
                     stage_empty = empty(0);
                 }
-            }
-            if (!ok && one) {   // our MMAs end before the TMEM is freed (bounded)
-                volatile uint32_t no_abort = 0;
-                mma_commit(drain);
-                mbar_wait(drain, 0, &no_abort, a.status, a.wait_limit_ns);
             }
         }
     } else {
@@ -904,6 +901,18 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     }
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag) {   // a warp gave up: what the others started ends before the memory it uses is freed (bounded)
+        volatile uint32_t no_abort = 0;
+        if (warp == 0) {
+            const int issued = *filled;
+            for (int u = max(0, issued - S); u < issued; ++u)
+                mbar_wait(full(u % S), (u / S) & 1, &no_abort, a.status, a.wait_limit_ns);
+        } else if (warp < 3 && elect_one()) {
+            mma_commit(drain(warp - 1));
+            mbar_wait(drain(warp - 1), 0, &no_abort, a.status, a.wait_limit_ns);
+        }
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");

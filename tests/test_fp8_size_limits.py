@@ -29,3 +29,10 @@ def test_products_refuse_sizes_they_cannot_count(bq, m, n, k, status):
     assert bq._lib.bq_mm_fp8_b128(None, None, m, None, None, n, k, 0, None, F16, n, None) == status
     # offsets: any address, nothing reads it
     assert bq._lib.bq_moe_mm_fp8_b128(None, None, m, 4096, 1, None, None, n, k, 0, None, F16, n, None) == status
+
+
+def test_the_wait_probe_for_parts_of_a_split(bq):
+    assert bq._lib.bq_test_set_wait_probe(3, 0) == 0
+    for bad in (-1, 2, 4, 5):
+        assert bq._lib.bq_test_set_wait_probe(bad, 0) == SHAPE
+    assert bq._lib.bq_test_set_wait_probe(0, 0) == 0

@@ -134,3 +134,25 @@ def test_a_wait_that_runs_out_in_one_part_of_a_split_leaves_y(lib, m, n, k, swig
     lib.mm_fp8_b128(x, xs, w, ws, want, swiglu=swiglu)
     assert lib.device_status() == lib.DEV_OK
     assert torch.equal(y, want) and (y != 7).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (100, 256, 1024), (2048, 2048, 512)])
+def test_calls_queued_behind_one_whose_waits_run_out(lib, m, n, k):
+    """No synchronisation in between: the next calls take the shared memory and TMEM that the failed one left."""
+    import torch
+    g = np.random.default_rng(52)
+    x, w = dev(g.integers(0, 0x7F, (m, k), dtype=np.uint8)), dev(g.integers(0, 0x7F, (n, k), dtype=np.uint8))
+    xs, ws = torch.ones(m, k // 128, device="cuda"), torch.ones(n // 128, k // 128, device="cuda")
+    y, z, want = (torch.full((m, n), 7.0, device="cuda") for _ in range(3))
+    lib.mm_fp8_b128(x, xs, w, ws, want)
+    for odd in (False, True) * 3:
+        lib.test_set_wait_probe(True, 1_000_000, odd_parts_only=odd)
+        try:
+            lib.mm_fp8_b128(x, xs, w, ws, z)
+        finally:
+            lib.test_set_wait_probe(False)
+        y.fill_(7.0)
+        for _ in range(4):
+            lib.mm_fp8_b128(x, xs, w, ws, y)
+        assert lib.device_status() == lib.DEV_WAIT_TIMEOUT
+        assert torch.equal(y, want) and (z == 7).all()
