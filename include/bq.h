@@ -493,9 +493,14 @@ bq_status bq_moe_dispatch_fp8_b128(const void* x, int32_t dtype, int32_t T, int3
  * repack):
  *   y[r][c] = sum_b xscales[r][b] * wscales[c/128][b]
  *                   * sum_{i in block b of 128} e4m3(x[r][i]) * e4m3(w[c][i])
- * Products and sums in fp32, the scales applied in fp32 to each block's sum;
- * the result is rounded once to `ydtype` (bq_dtype).  NaN codes, NaN and
- * infinite scales propagate.
+ * Products and sums in fp32; the result is rounded once to `ydtype`
+ * (bq_dtype).  A block's two scales are multiplied first, in fp32, and their
+ * product then meets the block's sum.  The scales may be of any size, but
+ * their product should be zero or a normal number: where it is below 2^-126
+ * the block's term is off by up to 2^-125 (rows of the smallest scale that
+ * bq_quant_fp8_b128 gives, 2^-126, hold values below 2^-117; zeros stay
+ * zeros); from 2^128 on the term is infinite, or NaN where the block's sum
+ * is 0.  NaN codes, NaN and infinite scales propagate.
  * swiglu = 1: w holds n/2 gate rows, then n/2 up rows (n a multiple of 256);
  * y has n/2 columns, silu(gate) * up with silu(g) = g / (1 + exp(-g)).
  *

@@ -156,3 +156,98 @@ def test_calls_queued_behind_one_whose_waits_run_out(lib, m, n, k):
             lib.mm_fp8_b128(x, xs, w, ws, y)
         assert lib.device_status() == lib.DEV_WAIT_TIMEOUT
         assert torch.equal(y, want) and (z == 7).all()
+
+
+def products(lib, x, xs, w, ws, swiglu, grouped):
+    """y (fp32) of the codes' product, dense or with every row in the second of three experts."""
+    import torch
+    m, n = x.shape[0], w.shape[0]
+    y = torch.full((m, n // 2 if swiglu else n), 7.0, device="cuda")
+    if grouped:
+        off = torch.tensor([0, 0, m, m], dtype=torch.int32, device="cuda")
+        lib.moe_mm_fp8_b128(dev(x), dev(xs), off, dev(np.stack([w] * 3)), dev(np.stack([ws] * 3)), y, swiglu=swiglu)
+    else:
+        lib.mm_fp8_b128(dev(x), dev(xs), dev(w), dev(ws), y, swiglu=swiglu)
+    assert lib.device_status() == lib.DEV_OK
+    return y
+
+
+def bound(x, xs, w, ws):
+    """(exact product, bound of the error of fp32 sums): (259 + kb) u S as for scales of ordinary size, and half a
+    subnormal step for each block where a sum comes out below the normal numbers."""
+    kb = xs.shape[1]
+    size = O.mm_fp8_block(np.abs(O.e4m3_value(x)), np.abs(xs), w & 0x7F, np.abs(ws))
+    exact = O.mm_fp8_block(O.e4m3_value(x), xs, w, ws)
+    return exact, (260 + kb) * 2.0 ** -24 * size + (kb + 1) * 2.0 ** -150
+
+
+# rows that take the split lanes, the lanes, and the wide tile
+RANGE = [(1, 256, 1024), (7, 512, 272), (32, 4096, 256), (45, 384, 512), (700, 1280, 400)]
+
+
+def scaled_case(m, n, k, ex, ew):
+    """Random codes of both signs; row scales of about 2^ex, weight scales of about 2^ew, of both signs."""
+    g = np.random.default_rng(10000 + ex * 31 + ew + m)
+    kb, nb = -(-k // 128), -(-n // 128)
+    x, w = (g.integers(0, 0x7F, s, dtype=np.uint8) | (g.integers(0, 2, s, dtype=np.uint8) << 7) for s in ((m, k), (n, k)))
+    xs, ws = (np.float32(g.choice([-1.0, 1.0], s) * np.exp2(e + g.uniform(-1, 1, s))) for e, s in
+              ((ex, (m, kb)), (ew, (nb, kb))))
+    assert (xs != 0).all() and (ws != 0).all() and np.isfinite(xs).all() and np.isfinite(ws).all()
+    return x, xs, w, ws
+
+
+def assert_within(got, want, err):
+    got = got.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    worst = (np.abs(got - want) / err).max()
+    assert worst <= 1.0, f"{worst:.2f} times the bound"
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("m,n,k", RANGE)
+@pytest.mark.parametrize("ex,ew", [(-126, 4), (-126, 126), (126, -126), (-140, 30), (30, -140), (-62, -60), (50, 48)])
+def test_scales_of_any_size_whose_product_is_normal(lib, m, n, k, ex, ew, grouped):
+    x, xs, w, ws = scaled_case(m, n, k, ex, ew)
+    exact, err = bound(x, xs, w, ws)
+    assert_within(products(lib, x, xs, w, ws, False, grouped), exact, err)
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("m,n,k", RANGE)
+@pytest.mark.parametrize("ex,ew", [(-126, -1), (-126, -14), (-126, -24), (-100, -40), (-8, -130), (-120, -100)])
+def test_scales_whose_product_is_below_the_normal_numbers(lib, m, n, k, ex, ew, grouped):
+    """The product of the scales is off by half a subnormal step, 2^-150, and a block's sum is below 2^25."""
+    x, xs, w, ws = scaled_case(m, n, k, ex, ew)
+    exact, err = bound(x, xs, w, ws)
+    assert_within(products(lib, x, xs, w, ws, False, grouped), exact, err + xs.shape[1] * 2.0 ** -125)
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("m,n,k", [(8, 512, 1024), (45, 512, 512), (700, 1280, 400)])
+def test_zero_rows_are_zero_and_change_no_other(lib, m, n, k, swiglu):
+    """A padded batch: rows of zeros get the smallest scale, whose product with the weight's is subnormal."""
+    import torch
+    g = np.random.default_rng(61)
+    rows = torch.randn(m, k, device="cuda")
+    padded = rows.clone()
+    padded[2::3] = 0.0
+    w, ws = g.integers(0, 0x7F, (n, k), dtype=np.uint8), np.float32(g.uniform(1e-5, 1e-4, (-(-n // 128), -(-k // 128))))
+    y = []
+    for r in (rows, padded):
+        q, s = torch.empty(m, k, dtype=torch.uint8, device="cuda"), torch.empty(m, -(-k // 128), device="cuda")
+        lib.quant_fp8_b128(r, q, s)
+        y.append(products(lib, q.cpu().numpy(), s.cpu().numpy(), w, ws, swiglu, False))
+    assert (y[1][2::3] == 0).all()
+    keep = torch.arange(m, device="cuda") % 3 != 2
+    assert torch.equal(y[0][keep], y[1][keep])
+
+
+@pytest.mark.parametrize("m,n,k", RANGE)
+def test_scales_whose_product_is_beyond_fp32_show_in_their_rows_only(lib, m, n, k):
+    x, xs, w, ws = scaled_case(m, n, k, -5, 10)
+    x[0], xs[0, 0] = 0, 2.0 ** 127          # zeros: NaN, as the header says
+    got = products(lib, x, xs, w, ws, False, False)
+    assert not got[0].isfinite().any()
+    if m > 1:
+        exact, err = bound(x[1:], xs[1:], w, ws)
+        assert_within(got[1:], exact, err)
