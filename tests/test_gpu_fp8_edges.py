@@ -251,3 +251,79 @@ def test_scales_whose_product_is_beyond_fp32_show_in_their_rows_only(lib, m, n, 
     if m > 1:
         exact, err = bound(x[1:], xs[1:], w, ws)
         assert_within(got[1:], exact, err)
+
+
+HALF_STEP = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+
+
+def torch_type(name):
+    import torch
+    return {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[name]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("amax", [448.0, 1.0, 21.0, 7.0, 1.25, 0.0302734375, 1.5 * 2 ** -9, 60000.0, 3.0 * 2.0 ** -14])
+def test_quotients_one_step_beside_every_border(lib, dtype, amax):
+    """For each border of two codes the value of the type nearest to it, and the values one step above and below that."""
+    import torch
+    dt = torch_type(dtype)
+    bits = {"f32": torch.int32}.get(dtype, torch.int16)
+    amax = torch.tensor(amax).to(dt)
+    table = O.e4m3_value(np.arange(127, dtype=np.uint8))
+    at = torch.from_numpy((table[1:] + table[:-1]) / 2 * amax.double().item() / 448.0).to(dt)
+    at = at[at > 0]                                   # fp16 has no value beside the smallest borders of a small amax
+    assert at.numel() >= 100
+    up, down = ((at.view(bits) + d).to(bits).view(dt) for d in (1, -1))    # neighbours of a positive value
+    assert (up > at).all() and (down < at).all() and (down >= 0).all()
+    rows = []
+    for v in (at, up, down):
+        row = torch.zeros(128, dtype=dt)
+        row[:at.numel()] = v.clamp(max=amax.item())
+        row[127] = amax
+        rows += [row, -row]
+    x = torch.stack(rows)
+    q, s = torch.empty(6, 128, dtype=torch.uint8, device="cuda"), torch.empty(6, 1, device="cuda")
+    lib.quant_fp8_b128(x.cuda(), q, s)
+    want_q, want_s = O.quant_fp8_rows(x.double().numpy())
+    np.testing.assert_array_equal(s.cpu().numpy(), want_s)
+    np.testing.assert_array_equal(O.e4m3_value(q.cpu().numpy()), want_q)
+
+
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m,n,ld", [(5000, 101, 104), (5000, 101, 112), (2500, 357, 360), (2500, 260, 264), (4, 101, 104)])
+def test_rows_of_y_on_16_byte_boundaries_that_end_inside_a_vector(lib, m, n, ld, out):
+    import torch
+    k = 144
+    x, xs, w, ws = scaled_case(m, n, k, -9, -9)
+    big = torch.full((m, ld), 7.0, dtype=torch_type(out), device="cuda")
+    y = big[:, :n]
+    lib.mm_fp8_b128(dev(x), dev(xs), dev(w), dev(ws), y)
+    exact, err = bound(x, xs, w, ws)
+    assert_within(y, exact, err + HALF_STEP[out] * np.abs(exact) + 2.0 ** -25)     # fp16's half subnormal step
+    assert (big[:, n:] == 7).all() and lib.device_status() == lib.DEV_OK
+
+
+def test_backward_and_fp8_rows_beyond_32_bit_offsets(lib):
+    """Sorted matrices of more than 2^31 elements: the sort's gradient, and the sort into FP8 rows."""
+    import torch
+    needs(24)
+    t, k, h = 270_000, 4, 2048
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    dxs = torch.randn(t * k, h, generator=gen, device="cuda", dtype=torch.bfloat16)
+    inv = torch.randperm(t * k, generator=gen, device="cuda").int().view(t, k)
+    dx = torch.full((t, h), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lib.moe_dispatch_backward(dxs, inv, dx)
+    for a in range(0, t, 30_000):
+        terms = dxs[inv[a:a + 30_000].long()].double()
+        err = k * 2.0 ** -24 * terms.abs().sum(1) + 2.0 ** -8 * terms.sum(1).abs() * 1.001 + 2.0 ** -134
+        assert ((dx[a:a + 30_000].double() - terms.sum(1)).abs() <= err).all()
+    q = torch.empty(t * k, h, dtype=torch.uint8, device="cuda")
+    s = torch.empty(t * k, h // 128, device="cuda")
+    lib.moe_dispatch_fp8_b128(dx, inv, q, s)
+    one_q, one_s = torch.empty(t, h, dtype=torch.uint8, device="cuda"), torch.empty(t, h // 128, device="cuda")
+    lib.quant_fp8_b128(dx, one_q, one_s)
+    for j in range(k):
+        for a in range(0, t, 90_000):
+            at = inv[a:a + 90_000, j].long()
+            assert torch.equal(q[at], one_q[a:a + 90_000]) and torch.equal(s[at], one_s[a:a + 90_000])
+    assert lib.device_status() == lib.DEV_OK
