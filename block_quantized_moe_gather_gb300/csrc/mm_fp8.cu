@@ -228,8 +228,7 @@ struct Item {
 // their weight tiles, then the chunks of rows that share such a tile (so that
 // a tile's second reader finds it in the L2).  A whole warp steps through them;
 // i is kept as chunk * w_tiles + rest, and the expert is found in two ballots
-// (a serial search and its loads held every role up for 1000 cycles an item,
-// which small K did not hide).
+// (small K does not hide a search that reads one expert after the other).
 struct Items {
     int i, count, step, w_tiles, chunk, rest, d_chunk, d_rest;
 
@@ -285,10 +284,12 @@ struct Items {
 // With few items K is split over a cluster: the CTAs leave their sums in
 // shared memory and each finishes a share of the rows, in rank order.
 //
-// Measured: up to 48 of 256 experts with a row or two each, 4096 x 2048: 63.5
-// us, 5.9 TB/s (loops run by one lane 79.1; a serial search for each item's
-// expert 66.4); one row x 4096 x 4096 5.5 us (6.5), of which the weights take
-// 2.5: launch, first loads and the cluster's two barriers are the rest.
+// Measured: up to 48 of 256 experts with a row or two each, 4096 x 2048: 62.2
+// us, 6.0 TB/s.  One row x 4096 x 4096: 5.7 us, of which reading the weights
+// would take 2.5.  An epilogue warp takes its blocks one after the other (wait,
+// TMEM load, scales, sums, release), 0.22 us each, eight of them with K split
+// over four CTAs; launch, first loads and the cluster's two barriers are the
+// rest.  128 rows, unsplit, 32 blocks: 11.4 us.
 constexpr int kLaneRows = 32;      // rows of x in a tile (the columns of a TMEM slot)
 constexpr int kLaneThreads = 224;
 
@@ -583,17 +584,12 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
 // In the long run a block of 128 x 256 x 128 takes 0.36 us of an SM, 0.91 of
 // twice the measured bf16 rate, and the MMAs bound it: without the multiply-
 // adds it takes as long, with a quarter of the MMAs 0.32 us.  On top come the
-// rounds of tiles (2048 x 4096 x 4096: 256 on 152 SMs) and about 6 us of
-// launch, first loads and last stores.  Measured at 2048 x 4096 x 4096, each
-// step on the one before: sums not spilling 59.8 -> 37.7 us; loops that a whole
-// warp runs with one lane issuing, both barriers of a block tested together,
-// plain instead of packed multiply-adds (packed ones cost moves that pair the
-// loaded registers) 37.7 -> 37.3; a block's wait and first load before the last
-// sums of the block before it, scales loaded two blocks ahead 37.3 -> 30.9 (2.2
-// PFLOP/s; 8192 rows 2.7).  No faster, and not kept: a pair of CTAs sharing the
-// weight rows (cta_group::2, 30.4 to 33), one MMA of 256 columns in place of
-// the two halves (31.8), one warp issuing both halves (40.3), tiles of 224
-// columns, which fill the second round (31.7).
+// rounds of tiles (2048 x 4096 x 4096: 256 on 152 SMs), about 6 us of launch,
+// first loads and last stores for the first round, and about 2 us for each
+// further one, while a tile is stored and the next one's scales are fetched and
+// the MMAs run only two blocks ahead.  2048 x 4096 x 4096: 31.5 us (2.2
+// PFLOP/s; 8192 rows 2.6).  A tile is 256 columns wide whatever the rows, so
+// 256 to 1024 rows take 15.3 to 17.6 us.
 constexpr int kWideThreads = 384;
 constexpr int kWideRegs = 224, kControlRegs = 56;   // 256 * 224 + 128 * 56 = 384 * 168, what the launch holds
 static_assert(256 * kWideRegs + 128 * kControlRegs <= kWideThreads * 168, "registers");
@@ -636,10 +632,10 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
 //   time (whole sectors);
 //   other rows, and fp32: by way of shared memory, below, so that eight lanes
 //   store 128 contiguous bytes.
-// 2048 x 4096 x 4096: fp32 34.3 us by way of shared memory, 37.1 direct; 4095
-// columns, on no boundary, 60.4 against 104; bf16 31.3 against 31.6, and the
-// gate/up product of 128 experts, whose epilogue has less time, 90.3 against
-// 87.0.
+// Both ways in one run each, 2048 x 4096 x 4096: fp32 34.3 us by way of shared
+// memory and 37.1 direct; 4095 columns of 16 bits, on no boundary, 60.4 and 104;
+// bf16 31.3 and 31.6, and the gate/up product of 128 experts, whose epilogue has
+// less time, 90.3 and 87.0.
 //
 // 128 bytes of each row (w) to rows row0.. of y from column c on, those below `rows`, 16 rows at a time.
 __device__ __forceinline__ void store_rows(const Args& a, uint8_t* buf, const uint4 (&w)[8], int64_t row0, int rows, int c,
@@ -1032,7 +1028,9 @@ bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32
     // 192 rows, two waves, 19.4 against 14.7), and for experts of up to 16 rows on average, where both read every
     // weight once and it reads less beside them (128 experts, gate/up 1536 x 2048: 8 rows 69.1 us against 72.2, 16 rows
     // 71.0 against 73.1, 32 rows 85.2 against 74.9).  There the wide tile is the faster one when K is so short that the
-    // narrower tile's more items count (down 2048 x 768: 0.3 rows 12.8 against 13.3, 4 rows 38.2 against 35.6).
+    // narrower tile's more items count (down 2048 x 768: 0.3 rows 12.8 against 13.3, 4 rows 38.2 against 35.6).  The
+    // average is all the host knows: with 2048 gate/up rows over 128 experts in Zipf(1.1) shares it takes 77.4 us
+    // against 69.9, with all of them at one expert, the worst case, 37.2 against 12.5.
     const int kb = (k + kBlock - 1) / kBlock;
     const int64_t lane_items = chunks_of(kLaneRows) * tiles_of(swiglu ? 64 : 128);
     const bool few_rows = offsets && rows <= 16 * (int64_t)experts && !(kb <= 8 && lane_items > 8 * kSms);

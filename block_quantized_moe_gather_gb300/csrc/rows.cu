@@ -7,10 +7,12 @@
 //   combine            y[t] (+)= sum_j w[t][j] ys[inv[t][j]]
 //   combine backward   dys[inv[t][j]] = w[t][j] dy[t],  dw[t][j] = <dy[t], ys[inv[t][j]]>
 //
-// Every kernel is bound by memory (GB300: dispatch backward 19.8 us, 5.9 TB/s,
-// at 2048 tokens x 6 rows of 4096 bf16; combine 23.6 us, 6.4 TB/s, at 2047 x 8
-// rows of 2048 fp32; its backward pass 23.4 us, 6.1 TB/s, at 2048 x 8 rows of
-// 2048 bf16; a decode step's call 1.5 to 2 us).  Going by token rather than by sorted row
+// Every kernel is bound by memory (GB300: dispatch 19.3 us, 6.1 TB/s, at 2048
+// tokens x 6 rows of 4096 fp16, 13.8 us, 5.5 TB/s, at 2048 x 8 of 2048 bf16; its
+// backward pass 19.8 us, 5.9 TB/s, at 2048 x 6 of 4096 bf16; combine 23.7 to
+// 26.4 us, 6.4 to 5.7 TB/s, at 2047 x 8 rows of 2048 fp32; its backward pass
+// 23.4 us, 6.1 TB/s, at 2048 x 8 rows of 2048 bf16; a decode step's call 1.5 to
+// 2 us).  Going by token rather than by sorted row
 // reads or writes the token's row once instead of k times, and the k sorted
 // rows exactly once; no thread shares an output, so there are no atomics and
 // every sum has a fixed order.
