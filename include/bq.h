@@ -517,8 +517,8 @@ bq_status bq_moe_dispatch_fp8_b128(const void* x, int32_t dtype, int32_t T, int3
  * [ceil(k/128)]; y: device rows of n (swiglu: n/2) elements of `ydtype`,
  * ldy elements apart.  k a multiple of 16 (a short last block is fine),
  * n >= 1 of any value (without swiglu), rows, n and k at most 2^31 - 256,
- * E * n <= 2^31 - 1, E <= 1024.  x, w 16-byte aligned; scales and offsets 4-byte aligned; y aligned to its
- * element.
+ * E * n <= 2^31 - 1, E <= 1024.  x, w 16-byte aligned; scales and offsets
+ * 4-byte aligned; y aligned to its element.
  * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_FORMAT, BQ_ERR_ALIGN,
  * BQ_ERR_CUDA.  No rows: a no-op.
  */
@@ -567,7 +567,8 @@ uint64_t bq_launch_count(void);
  * so the waits for weights run out: the call then returns BQ_OK, its output
  * is undefined and bq_device_status reports BQ_DEV_WAIT_TIMEOUT.  3: the same,
  * but of an FP8 product whose K is split over a cluster only the odd parts
- * issue none; no part of a split then writes y.  Process wide, for tests only; call bq_test_set_wait_probe(0, 0) to restore.
+ * issue none; no part of a split then writes y.  Process wide, for tests
+ * only; call bq_test_set_wait_probe(0, 0) to restore.
  * Errors: BQ_ERR_SHAPE (argument outside the ranges above).
  */
 bq_status bq_test_set_wait_probe(int32_t skip_weight_copies, uint64_t wait_limit_ns);
