@@ -43,6 +43,17 @@ class MoEDescC(ctypes.Structure):
                 ("route_scale", c_float), ("reserved", c_int32)]
 
 
+class EpilogueC(ctypes.Structure):
+    _fields_ = [("act", c_int32), ("scale", c_float), ("bias", c_void_p), ("residual", c_void_p), ("ldr", c_int64)]
+
+
+class ResidualNormDescC(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in ("T", "H", "y_dtype", "h_dtype", "x_dtype", "gain_dtype", "gate_dtype", "gate_kind",
+                                       "gate_sigmoid")] + [
+        ("scale", c_float), ("residual_scale", c_float), ("eps", c_float), ("gain", c_void_p), ("post_gain", c_void_p),
+        ("gate", c_void_p), ("ldgate", c_int64)]
+
+
 _SIGS = {
     "bq_status_string": (c_char_p, [c_int32]),
     "bq_last_error": (c_char_p, []),
@@ -94,6 +105,24 @@ _SIGS = {
                                  c_int32, c_int64, c_void_p]),
     "bq_moe_mm_fp8_b128": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_int32,
                                      c_int32, c_int32, c_void_p, c_int32, c_int64, c_void_p]),
+    "bq_mm_fp8_b128_epilogue": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32,
+                                          POINTER(EpilogueC), c_void_p, c_int32, c_int64, c_void_p]),
+    "bq_moe_mm_fp8_b128_epilogue": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
+                                              c_int32, c_int32, POINTER(EpilogueC), c_void_p, c_int32, c_int64,
+                                              c_void_p]),
+    "bq_residual_norm": (c_int32, [POINTER(ResidualNormDescC), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                   c_void_p, c_int64, c_void_p]),
+    "bq_residual_norm_backward_workspace_bytes": (c_size_t, [c_int32, c_int32]),
+    "bq_residual_norm_backward": (c_int32, [POINTER(ResidualNormDescC), c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                            c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                            c_void_p, c_void_p, c_int64, c_void_p, c_size_t, c_void_p]),
+    "bq_moe_balance_workspace_bytes": (c_size_t, [c_int32, c_int32, c_int32]),
+    "bq_moe_balance_loss": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_int32, c_int32, c_void_p,
+                                      c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "bq_moe_route_backward_workspace_bytes": (c_size_t, [c_int32, c_int32]),
+    "bq_moe_route_backward": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_int32, c_int32, c_float,
+                                        c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_void_p,
+                                        c_void_p, c_size_t, c_void_p]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -567,25 +596,234 @@ def _product(where, x, x_scales, w, w_scales, y, swiglu, grouped):
     return px, pxs, m, pw, pws, n, k, 1 if swiglu else 0, py, dt, ldy
 
 
-def mm_fp8_b128(x, x_scales, w, w_scales, y, swiglu: bool = False, stream=None):
+# bq_activation
+ACT_NONE, ACT_SWIGLU, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU, ACT_RELU2 = range(7)
+ACT_BY_NAME = {"none": ACT_NONE, "swiglu": ACT_SWIGLU, "silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH,
+               "relu": ACT_RELU, "relu2": ACT_RELU2}
+
+
+def _epilogue(where, swiglu, act, bias, bias_shape, residual, scale, dt, rows, cols):
+    """The C struct of a product's end, or None where it changes nothing."""
+    if act is not None and act not in ACT_BY_NAME:
+        _refuse(2, where, f"unknown activation {act!r}")
+    code = ACT_SWIGLU if swiglu else ACT_NONE if act is None else ACT_BY_NAME[act]
+    if bias is None and residual is None and scale == 1.0 and code <= ACT_SWIGLU:
+        return None
+    pb = None if bias is None else _dense(where, "bias", bias, bias_shape, "f32")
+    pr, ldr = None, 0
+    if residual is not None:
+        pr, _, _, _, ldr = _rows_of(where, "residual", residual, rows, cols, dt)
+    return EpilogueC(code, scale, pb, pr, ldr)
+
+
+def _gated(where, swiglu, act):
+    if swiglu and act not in (None, "swiglu"):
+        _refuse(2, where, f"swiglu and act={act!r} exclude each other")
+    return swiglu or act == "swiglu"
+
+
+def mm_fp8_b128(x, x_scales, w, w_scales, y, swiglu: bool = False, stream=None, *, act: str | None = None, bias=None,
+                residual=None, scale: float = 1.0):
     """y = x w^T of FP8 rows x [m, k] (quant_fp8_b128) and an FP8 weight w [n, k] with
-    one scale per 128 x 128 block; y [m, n] fp32, fp16 or bf16.  swiglu: w holds n/2
-    gate rows and n/2 up rows, y [m, n/2] = silu(gate) * up."""
+    one scale per 128 x 128 block; y [m, n] fp32, fp16 or bf16.  swiglu (or act="swiglu"):
+    w holds n/2 gate rows and n/2 up rows, y [m, n/2] = silu(gate) * up.  With any of act
+    (silu, gelu, gelu_tanh, relu, relu2), bias (fp32 [n]), scale and residual (rows like
+    y's; it may be y): y = scale * act(x w^T + bias) + residual."""
     where = "bq_mm_fp8_b128"
-    st = _on_stream(where, stream, x, x_scales, w, w_scales, y)
+    st = _on_stream(where, stream, x, x_scales, w, w_scales, y, bias, residual)
+    swiglu = _gated(where, swiglu, act)
     px, pxs, m, pw, pws, n, k, sw, py, dt, ldy = _product(where, x, x_scales, w, w_scales, y, swiglu, False)
-    _check(_lib.bq_mm_fp8_b128(px, pxs, m, pw, pws, n, k, sw, py, dt, ldy, st), where)
+    epi = _epilogue(where, swiglu, act, bias, (n,), residual, scale, dt, m, y.shape[1])
+    if epi is None:
+        _check(_lib.bq_mm_fp8_b128(px, pxs, m, pw, pws, n, k, sw, py, dt, ldy, st), where)
+    else:
+        _check(_lib.bq_mm_fp8_b128_epilogue(px, pxs, m, pw, pws, n, k, ctypes.byref(epi), py, dt, ldy, st), where)
     return y
 
 
-def moe_mm_fp8_b128(x, x_scales, offsets, w, w_scales, y, swiglu: bool = False, stream=None):
+def moe_mm_fp8_b128(x, x_scales, offsets, w, w_scales, y, swiglu: bool = False, stream=None, *, act: str | None = None,
+                    bias=None, residual=None, scale: float = 1.0):
     """mm_fp8_b128 over rows sorted by expert: rows offsets[e] .. offsets[e + 1] of x
-    take w[e].  w [E, n, k], w_scales [E, ceil(n/128), ceil(k/128)], offsets int32
-    [E + 1] from moe_permute.  Rows of y behind offsets[E] are left as they are."""
+    take w[e] (and bias[e]).  w [E, n, k], w_scales [E, ceil(n/128), ceil(k/128)], bias
+    fp32 [E, n], offsets int32 [E + 1] from moe_permute.  Rows of y behind offsets[E]
+    are left as they are."""
     where = "bq_moe_mm_fp8_b128"
-    st = _on_stream(where, stream, x, x_scales, offsets, w, w_scales, y)
+    st = _on_stream(where, stream, x, x_scales, offsets, w, w_scales, y, bias, residual)
+    swiglu = _gated(where, swiglu, act)
     px, pxs, m, pw, pws, n, k, sw, py, dt, ldy = _product(where, x, x_scales, w, w_scales, y, swiglu, True)
     e = w.shape[0]
     po = _dense(where, "offsets", offsets, (e + 1,), "i32")
-    _check(_lib.bq_moe_mm_fp8_b128(px, pxs, m, po, e, pw, pws, n, k, sw, py, dt, ldy, st), where)
+    epi = _epilogue(where, swiglu, act, bias, (e, n), residual, scale, dt, m, y.shape[1])
+    if epi is None:
+        _check(_lib.bq_moe_mm_fp8_b128(px, pxs, m, po, e, pw, pws, n, k, sw, py, dt, ldy, st), where)
+    else:
+        _check(_lib.bq_moe_mm_fp8_b128_epilogue(px, pxs, m, po, e, pw, pws, n, k, ctypes.byref(epi), py, dt, ldy, st),
+               where)
     return y
+
+
+# ---------------------------------------------------------------- block to block
+GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_FULL = 0, 1, 2, 3
+
+
+def _vector(where: str, what: str, t, n: int):
+    """(pointer, bq_dtype) of a contiguous vector of n elements of a row type."""
+    if _DT is None:
+        _load_torch()
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        _refuse(4, where, f"{what} has type {t.dtype}")
+    if t.shape != (n,) or not t.is_contiguous():
+        _refuse(2, where, f"{what} has shape {list(t.shape)} and strides {tuple(t.stride())}, expected contiguous [{n}]")
+    return t.data_ptr(), dt
+
+
+def _gate(where: str, gate, t: int, h: int):
+    """(kind, pointer, bq_dtype, row stride) of a gate [T, 1], [H] or [T, H]."""
+    if gate is None:
+        return GATE_NONE, None, DT_F32, 0
+    shape = gate.shape
+    if len(shape) == 1:
+        return (GATE_CHANNEL, *_vector(where, "gate", gate, h), 0)
+    if shape == (t, 1):
+        return (GATE_TOKEN, *_vector(where, "gate", gate.view(-1) if gate.is_contiguous() else gate, t), 0)
+    p, dt, _, _, ld = _rows_of(where, "gate", gate, t, h)
+    return GATE_FULL, p, dt, ld
+
+
+def _norm_desc(where, t, h, dy, dh, dx, gain, post_gain, gate, gate_sigmoid, scale, residual_scale, eps):
+    pg, gdt = (None, None) if gain is None else _vector(where, "gain", gain, h)
+    pp, pdt = (None, gdt) if post_gain is None else _vector(where, "post_gain", post_gain, h)
+    if gdt is not None and pdt != gdt:
+        _refuse(4, where, f"gain has type {gain.dtype}, post_gain {post_gain.dtype}")
+    kind, pgate, gate_dt, ldgate = _gate(where, gate, t, h)
+    return ResidualNormDescC(t, h, dy, dh, dx, DT_F32 if pdt is None else pdt, gate_dt, kind, int(bool(gate_sigmoid)),
+                             scale, residual_scale, eps, pg, pp, pgate, ldgate)
+
+
+def residual_norm(y, h, h_out, x=None, gain=None, post_gain=None, gate=None, gate_sigmoid: bool = False,
+                  scale: float = 1.0, residual_scale: float = 1.0, eps: float = 1e-6, stream=None):
+    """A block's output y into the residual stream, and the stream normalised for the
+    next block: h_out = residual_scale * h + scale * g * (post_gain * n(y), or y),
+    x = gain * n(h_out), n(v) = v / sqrt(mean(v^2) + eps) per row.  g: gate [T, 1],
+    [H] or [T, H], or its sigmoid.  y, h, x [T, H] of any row type each (h_out of h's;
+    it may be h); gains [H] of one type.  x None: only h_out."""
+    where = "bq_residual_norm"
+    st = _on_stream(where, stream, y, h, h_out, x, gain, post_gain, gate)
+    py, dy, t, n, ldy = _rows_of(where, "y", y)
+    ph, dh, _, _, ldh = _rows_of(where, "h", h, t, n)
+    po, _, _, _, ldo = _rows_of(where, "h_out", h_out, t, n, dh)
+    px, dx, ldx = None, dh, 0
+    if x is not None:
+        px, dx, _, _, ldx = _rows_of(where, "x", x, t, n)
+    desc = _norm_desc(where, t, n, dy, dh, dx, gain, post_gain, gate, gate_sigmoid, scale, residual_scale, eps)
+    _check(_lib.bq_residual_norm(ctypes.byref(desc), py, ldy, ph, ldh, po, ldo, px, ldx, st), where)
+    return h_out, x
+
+
+def residual_norm_backward_workspace_bytes(t: int, h: int) -> int:
+    return int(_lib.bq_residual_norm_backward_workspace_bytes(t, h))
+
+
+def residual_norm_backward(y, h_out, dh_out, dx, dy, dh, gain=None, post_gain=None, gate=None,
+                           gate_sigmoid: bool = False, scale: float = 1.0, residual_scale: float = 1.0,
+                           eps: float = 1e-6, dgain=None, dpost_gain=None, dgate=None, workspace=None, stream=None):
+    """Gradients of residual_norm from those of h_out and x (dh_out or dx may be None):
+    dy, dh (may be dh_out), and where given dgain, dpost_gain (fp32 [H]) and dgate (the
+    gate's shape; fp32, or the gate's type for a gate [T, H]).  The sums over rows need
+    a workspace of residual_norm_backward_workspace_bytes(T, H) bytes (uint8)."""
+    where = "bq_residual_norm_backward"
+    st = _on_stream(where, stream, y, h_out, dh_out, dx, dy, dh, gain, post_gain, gate, dgain, dpost_gain, dgate,
+                    workspace)
+    py, ty, t, n, ldy = _rows_of(where, "y", y)
+    pd, _, _, _, ldd = _rows_of(where, "dy", dy, t, n, ty)
+    pg, th, _, _, ldg = _rows_of(where, "dh", dh, t, n)
+    ph, ldh, po, ldo, px, ldx, tx = None, 0, None, 0, None, 0, th
+    if h_out is not None:
+        ph, _, _, _, ldh = _rows_of(where, "h_out", h_out, t, n, th)
+    if dh_out is not None:
+        po, _, _, _, ldo = _rows_of(where, "dh_out", dh_out, t, n, th)
+    if dx is not None:
+        px, tx, _, _, ldx = _rows_of(where, "dx", dx, t, n)
+    desc = _norm_desc(where, t, n, ty, th, tx, gain, post_gain, gate, gate_sigmoid, scale, residual_scale, eps)
+    sums = [None if s is None else _dense(where, what, s, (n,), "f32")
+            for what, s in (("dgain", dgain), ("dpost_gain", dpost_gain))]
+    pgate, ldgate = None, 0
+    if dgate is not None:
+        if gate is None or dgate.shape != gate.shape:
+            _refuse(2, where, f"dgate has shape {list(dgate.shape)}, the gate "
+                              f"{None if gate is None else list(gate.shape)}")
+        if desc.gate_kind == GATE_FULL:
+            pgate, _, _, _, ldgate = _rows_of(where, "dgate", dgate, t, n, desc.gate_dtype)
+        else:
+            pgate = _dense(where, "dgate", dgate, gate.shape, "f32")
+    pw, nw = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _check(_lib.bq_residual_norm_backward(ctypes.byref(desc), py, ldy, ph, ldh, po, ldo, px, ldx, pd, ldd, pg, ldg,
+                                          *sums, pgate, ldgate, pw, nw, st), where)
+    return dy, dh
+
+
+# ---------------------------------------------------------------- router training
+def _router(where, logits, ids, seq_offsets):
+    if len(logits.shape) != 2:
+        _refuse(2, where, f"logits has shape {list(logits.shape)}, expected [T, E]")
+    t, e = logits.shape
+    if len(ids.shape) != 2 or t > 0x7fffffff:
+        _refuse(2, where, f"ids has shape {list(ids.shape)}, logits {list(logits.shape)}")
+    k = ids.shape[1]
+    pl = _dense(where, "logits", logits, (t, e), "f32")
+    pi = _dense(where, "ids", ids, (t, k), "i32")
+    ps, s = None, 1
+    if seq_offsets is not None:
+        s = seq_offsets.numel() - 1
+        ps = _dense(where, "seq_offsets", seq_offsets, (s + 1,), "i32")
+    return pl, pi, t, e, k, ps, s
+
+
+def moe_balance_workspace_bytes(t: int, e: int, sequences: int = 1) -> int:
+    return int(_lib.bq_moe_balance_workspace_bytes(t, e, sequences))
+
+
+def moe_balance_loss(logits, ids, counts, probs, losses, workspace, bias=None, scoring: int = SCORE_SOFTMAX,
+                     seq_offsets=None, stream=None):
+    """Balance statistics of a router's logits (fp32 [T, E]) and its ids (int32 [T, k]), over
+    all rows or per sequence (seq_offsets int32 [S + 1]): counts int32 and probs fp32 [S, E]
+    (S = 1 without offsets), losses fp32 [2]: the balance loss (1 for an even load) and the
+    z-loss.  bias: of the softmax rule.  workspace: moe_balance_workspace_bytes(T, E, S)."""
+    where = "bq_moe_balance_loss"
+    st = _on_stream(where, stream, logits, ids, counts, probs, losses, workspace, bias, seq_offsets)
+    pl, pi, t, e, k, ps, s = _router(where, logits, ids, seq_offsets)
+    pb = None if bias is None else _dense(where, "bias", bias, (e,), "f32")
+    pc = _dense(where, "counts", counts, (s, e), "i32")
+    pp = _dense(where, "probs", probs, (s, e), "f32")
+    po = _dense(where, "losses", losses, (2,), "f32")
+    _check(_lib.bq_moe_balance_loss(pl, pb, t, e, pi, k, scoring, ps, s, pc, pp, po, workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), st), where)
+    return counts, probs, losses
+
+
+def moe_route_backward_workspace_bytes(t: int, e: int) -> int:
+    return int(_lib.bq_moe_route_backward_workspace_bytes(t, e))
+
+
+def moe_route_backward(logits, ids, dweights, dlogits, bias=None, scoring: int = SCORE_SOFTMAX, scale: float = 1.0,
+                       counts=None, dlosses=None, seq_offsets=None, dbias=None, workspace=None, stream=None):
+    """Gradient of the router's weights (dweights fp32 [T, k], or None) and of the two losses of
+    moe_balance_loss (dlosses fp32 [2] with its counts, or None) with respect to the logits:
+    dlogits [T, E] of any row type; rows in no sequence stay as they were.  dbias fp32 [E] (softmax
+    rule) needs a workspace of moe_route_backward_workspace_bytes(T, E) bytes."""
+    where = "bq_moe_route_backward"
+    st = _on_stream(where, stream, logits, ids, dweights, dlogits, bias, counts, dlosses, seq_offsets, dbias, workspace)
+    pl, pi, t, e, k, ps, s = _router(where, logits, ids, seq_offsets)
+    if not dlogits.is_contiguous():
+        _refuse(2, where, f"dlogits has strides {tuple(dlogits.stride())}")
+    po, dt, _, _, _ = _rows_of(where, "dlogits", dlogits, t, e)
+    vectors = [None if v is None else _dense(where, what, v, shape, kind)
+               for what, v, shape, kind in (("bias", bias, (e,), "f32"), ("dweights", dweights, (t, k), "f32"),
+                                            ("counts", counts, (s, e), "i32"), ("dlosses", dlosses, (2,), "f32"),
+                                            ("dbias", dbias, (e,), "f32"))]
+    pb, pw, pc, pd, pdb = vectors
+    ws, nw = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _check(_lib.bq_moe_route_backward(pl, pb, t, e, pi, k, scoring, scale, pw, pc, pd, ps, s, po, dt, pdb, ws, nw, st),
+           where)
+    return dlogits

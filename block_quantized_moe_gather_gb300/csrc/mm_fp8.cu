@@ -41,6 +41,12 @@ struct Args {
     unsigned long long wait_limit_ns;
     int skip_copies;          // test only: the producer issues no copies (waits run out); 3: only in a part of a cluster
     int max_chunks;           // row chunks that offsets in order can make
+    // kernels with an end of their own only: y = scale * act(product + bias) + residual
+    const float* bias;        // [E][n], or NULL
+    int act;                  // bq_activation
+    float scale;
+    const void* residual;     // rows like y's, or NULL
+    int64_t ldr;
 };
 
 // ---------------------------------------------------------------- PTX used here only
@@ -147,6 +153,56 @@ __device__ __forceinline__ uint32_t peer_load_u32(uint32_t addr, uint32_t rank) 
 }
 
 __device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.f + expf(-g)); }
+
+// ---------------------------------------------------------------- ends
+// Activations other than SwiGLU, in place; the branch is the same for every thread.
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
+    switch (act) {
+        case BQ_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = silu_f(v[i]);
+            break;
+        case BQ_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = v[i] * normcdff(v[i]);
+            break;
+        case BQ_ACT_GELU_TANH:   // (1 + tanh(u)) / 2 is sigmoid(2 u)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float u = 1.5957691216057308f * __fmaf_rn(0.044715f * v[i] * v[i], v[i], v[i]);
+                v[i] = __fdividef(v[i], 1.f + expf(-u));
+            }
+            break;
+        case BQ_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
+            break;
+        case BQ_ACT_RELU2:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i] * v[i];
+            break;
+        default: break;
+    }
+}
+
+// Element i of a matrix of y's type.
+__device__ __forceinline__ float load_value(const void* p, int64_t i, int dtype) {
+    if (dtype == BQ_DT_F32) return static_cast<const float*>(p)[i];
+    if (dtype == BQ_DT_F16) return __half2float(static_cast<const __half*>(p)[i]);
+    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+__device__ __forceinline__ float residual_at(const Args& a, int64_t row, int c) {
+    return a.residual ? load_value(a.residual, row * a.ldr + c, a.ydtype) : 0.f;
+}
+
+// One value's end, its residual loaded before (y may be the residual).
+__device__ __forceinline__ float end_of(const Args& a, float v, float residual) {
+    float f[1] = {v};
+    activate(f, a.act);
+    return __fmaf_rn(a.scale, f[0], residual);
+}
 
 // ---------------------------------------------------------------- work items
 // The row chunks of an expert of rows [lo, hi): a chunk is at most `most`
@@ -306,7 +362,16 @@ struct LaneSmem {
 };
 static_assert(LaneSmem::kBytes <= 232448 && LaneSmem::kTiles % 16 == 0, "smem");
 
+// Bias of the weight row that a lane holds: column c of y, with SwiGLU its gate value (lanes 0-15) or its up value.
 template <bool SWIGLU>
+__device__ __forceinline__ float lane_bias(const Args& a, int e, int c) {
+    if (!a.bias || c >= a.cols) return 0.f;
+    const int up = SWIGLU && (threadIdx.x & 16) ? a.cols : 0;
+    return __ldg(a.bias + (int64_t)e * a.n + up + c);
+}
+
+// EPI: with an end (bias, activation, scale, residual).
+template <bool SWIGLU, bool EPI>
 __global__ void __launch_bounds__(kLaneThreads, 1)
 mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a,
                 int split) {
@@ -475,6 +540,18 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                 break;         // one item per cluster
             }
             const int c = SWIGLU ? 64 * it.tile + 16 * quarter + (lane & 15) : 128 * it.tile + p;
+            float res[NT];
+            if (EPI) {
+                const float b = lane_bias<SWIGLU>(a, it.e, c);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[t] += b;
+                // the values that this thread stores: with SwiGLU those of every other row
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const int r = SWIGLU ? t + (lane >> 4) : t;
+                    res[t] = (!SWIGLU || t % 2 == 0) && r < it.rows && c < a.cols ? residual_at(a, it.row0 + r, c) : 0.f;
+                }
+            }
             if (SWIGLU) {
                 // lanes 0-15 hold gate rows, 16-31 their up rows; each half finishes every other row of x
 #pragma unroll
@@ -483,13 +560,18 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                         const float recv = __shfl_xor_sync(0xffffffffu, lane < 16 ? acc[t + 1] : acc[t], 16);
                         const float g = lane < 16 ? acc[t] : recv, u = lane < 16 ? recv : acc[t + 1];
                         const int r = t + (lane >> 4);
-                        if (r < it.rows) bq::store_value(a.y, (int64_t)(it.row0 + r) * a.ldy + c, a.ydtype, silu_f(g) * u);
+                        const float v = silu_f(g) * u;
+                        if (r < it.rows)
+                            bq::store_value(a.y, (int64_t)(it.row0 + r) * a.ldy + c, a.ydtype,
+                                            EPI ? end_of(a, v, res[t]) : v);
                     }
                 }
             } else if (c < a.cols) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    if (t < it.rows) bq::store_value(a.y, (int64_t)(it.row0 + t) * a.ldy + c, a.ydtype, acc[t]);
+                    if (t < it.rows)
+                        bq::store_value(a.y, (int64_t)(it.row0 + t) * a.ldy + c, a.ydtype,
+                                        EPI ? end_of(a, acc[t], res[t]) : acc[t]);
             }
         }
     }
@@ -505,8 +587,15 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
             const Item it = Items(first, step, items, w_tiles).get(chunks, a.E);
             const int c = SWIGLU ? 64 * it.tile + 16 * quarter + (lane & 15) : 128 * it.tile + p;
             constexpr int kAtOnce = 4;   // rows whose loads are in flight together
+            const float bias = EPI ? lane_bias<SWIGLU>(a, it.e, c) : 0.f;
             for (int t0 = rank; t0 < it.rows; t0 += kAtOnce * split) {
                 float part[kAtOnce][kMaxCluster] = {};
+                float res[kAtOnce];
+                if (EPI) {
+#pragma unroll
+                    for (int j = 0; j < kAtOnce; ++j)
+                        res[j] = t0 + j * split < it.rows && c < a.cols ? residual_at(a, it.row0 + t0 + j * split, c) : 0.f;
+                }
 #pragma unroll
                 for (int j = 0; j < kAtOnce; ++j) {
                     const uint32_t at = ring + 4 * ((t0 + j * split) * 128 + p);
@@ -525,10 +614,12 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                     float v = part[j][0];
 #pragma unroll
                     for (int r = 1; r < kMaxCluster; ++r) v += part[j][r];
+                    if (EPI) v += bias;
                     if (SWIGLU) {
                         const float u = __shfl_xor_sync(0xffffffffu, v, 16);
                         v = silu_f(v) * u;
                     }
+                    if (EPI) v = end_of(a, v, res[j]);
                     if (c < a.cols && (!SWIGLU || lane < 16))
                         bq::store_value(a.y, (int64_t)(it.row0 + t) * a.ldy + c, a.ydtype, v);
                 }
@@ -674,7 +765,33 @@ __device__ __forceinline__ void store_rows(const Args& a, uint8_t* buf, const ui
     }
 }
 
-template <bool SWIGLU>
+// Eight values of a row of the residual from column c on, as fp32; 0 where there is none (rows or columns behind the
+// last).  vectors: the matrix allows 16-byte loads.
+__device__ __forceinline__ void residual8(const Args& a, int64_t row, bool live, int c, bool vectors, float (&r)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = 0.f;
+    if (!a.residual || !live) return;
+    const int64_t at = row * a.ldr + c;
+    if (vectors && c + 8 <= a.cols) {
+        if (a.ydtype == BQ_DT_F32) {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + at);
+            const float4 lo = p[0], hi = p[1];
+            r[0] = lo.x; r[1] = lo.y; r[2] = lo.z; r[3] = lo.w;
+            r[4] = hi.x; r[5] = hi.y; r[6] = hi.z; r[7] = hi.w;
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + at);
+            if (a.ydtype == BQ_DT_F16) bq::RowVec<BQ_DT_F16>::unpack(v, r);
+            else bq::RowVec<BQ_DT_BF16>::unpack(v, r);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < a.cols) r[i] = load_value(a.residual, at + i, a.ydtype);
+}
+
+// EPI: with an end (bias, activation, scale, residual).
+template <bool SWIGLU, bool EPI>
 __global__ void __launch_bounds__(kWideThreads, 1)
 mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a) {
     using M = WideSmem;
@@ -795,6 +912,7 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         const int es = a.ydtype == BQ_DT_F32 ? 4 : 2;
         const uintptr_t y_align = reinterpret_cast<uintptr_t>(a.y) | (uintptr_t)(a.ldy * es);
         const bool aligned = y_align % 16 == 0, sectors = y_align % 32 == 0;
+        const bool vectors = (reinterpret_cast<uintptr_t>(a.residual) | (uintptr_t)(a.ldr * es)) % 16 == 0;
         // The slot in turn: its barriers (the second's 8 bytes behind the first's) and its columns, flipped by a bit.
         uint32_t bar_full = acc_full(half, 0), t = tmem + ((uint32_t)(32 * quarter) << 16) + half * A * 128, aph = 0;
         uint32_t bar_free = acc_empty(half, 0);
@@ -857,7 +975,30 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             if (rows > 0) {
                 uint8_t* buf = smem + M::kOut + (warp - 4) * 16 * kOutRow;
                 const int64_t row0 = it.row0 + 32 * quarter;
-                auto out = [&](int n) { return SWIGLU ? silu_f(acc[n]) * acc[(64 + n) & 127] : acc[n]; };
+                if (EPI) {   // in place, where the plain product's values lie: column c0 + n of y in acc[n]
+                    const float* bias = a.bias ? a.bias + (int64_t)it.e * a.n : nullptr;
+                    constexpr int kCols = SWIGLU ? 64 : 128;
+#pragma unroll
+                    for (int n = 0; n < kCols; n += 8) {
+                        float f[8], r[8];
+                        residual8(a, row0 + lane, lane < rows, c0 + n, vectors, r);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int c = min(c0 + n + i, a.cols - 1);
+                            f[i] = acc[n + i];
+                            if (bias) f[i] += __ldg(bias + c);
+                            if (SWIGLU) {
+                                float u = acc[(64 + n + i) & 127];
+                                if (bias) u += __ldg(bias + a.cols + c);
+                                f[i] = silu_f(f[i]) * u;
+                            }
+                        }
+                        activate(f, a.act);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) acc[n + i] = __fmaf_rn(a.scale, f[i], r[i]);
+                    }
+                }
+                auto out = [&](int n) { return SWIGLU && !EPI ? silu_f(acc[n]) * acc[(64 + n) & 127] : acc[n]; };
                 auto out8 = [&](int n) {
                     const float f[8] = {out(n), out(n + 1), out(n + 2), out(n + 3), out(n + 4), out(n + 5), out(n + 6), out(n + 7)};
                     return a.ydtype == BQ_DT_F16 ? bq::RowVec<BQ_DT_F16>::pack(f) : bq::RowVec<BQ_DT_BF16>::pack(f);
@@ -950,7 +1091,7 @@ bool gate_up_map(CUtensorMap* map, const uint8_t* w, int E, int n, int k, int bo
 
 constexpr int kSms = 152;
 
-template <bool SWIGLU>
+template <bool SWIGLU, bool EPI>
 cudaError_t launch_lanes(const CUtensorMap& map_w, const CUtensorMap& map_x, const Args& a, int64_t items, int split,
                          cudaStream_t st) {
     // per device: the attribute is a property of the function on the current device
@@ -958,7 +1099,7 @@ cudaError_t launch_lanes(const CUtensorMap& map_w, const CUtensorMap& map_x, con
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(mm_lanes_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(mm_lanes_kernel<SWIGLU, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    LaneSmem::kBytes);
         if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
@@ -976,10 +1117,10 @@ cudaError_t launch_lanes(const CUtensorMap& map_w, const CUtensorMap& map_x, con
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, mm_lanes_kernel<SWIGLU>, map_w, map_x, a, split);
+    return cudaLaunchKernelEx(&cfg, mm_lanes_kernel<SWIGLU, EPI>, map_w, map_x, a, split);
 }
 
-template <bool SWIGLU>
+template <bool SWIGLU, bool EPI>
 cudaError_t launch_wide(const CUtensorMap& map_w, const CUtensorMap& map_x, const Args& a, int64_t items,
                         cudaStream_t st) {
     static std::atomic<bool> attr_set[64];
@@ -987,17 +1128,17 @@ cudaError_t launch_wide(const CUtensorMap& map_w, const CUtensorMap& map_x, cons
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev].load(std::memory_order_acquire)) {
         const cudaError_t e =
-            cudaFuncSetAttribute(mm_wide_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideSmem::kBytes);
+            cudaFuncSetAttribute(mm_wide_kernel<SWIGLU, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideSmem::kBytes);
         if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
     }
-    return bq::launch_after(mm_wide_kernel<SWIGLU>, dim3((unsigned)std::min<int64_t>(items, kSms)), dim3(kWideThreads),
+    return bq::launch_after(mm_wide_kernel<SWIGLU, EPI>, dim3((unsigned)std::min<int64_t>(items, kSms)), dim3(kWideThreads),
                             WideSmem::kBytes, st, map_w, map_x, a);
 }
 
 bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32_t rows, const int32_t* offsets,
                  int32_t E, const uint8_t* w, const float* wscales, int32_t n, int32_t k, int32_t swiglu, void* y,
-                 int32_t ydtype, int64_t ldy, cudaStream_t st) {
+                 int32_t ydtype, int64_t ldy, cudaStream_t st, const bq_epilogue* epi = nullptr) {
     const int es = bq::dtype_size(ydtype);
     if (es == 0) return bq::fail(BQ_ERR_FORMAT, "%s: unknown element type %d", name, ydtype);
     if (swiglu != 0 && swiglu != 1) return bq::fail(BQ_ERR_SHAPE, "%s: swiglu must be 0 or 1, not %d", name, swiglu);
@@ -1020,6 +1161,11 @@ bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32
         !bq::aligned(offsets, 4) || !bq::aligned(y, es))
         return bq::fail(BQ_ERR_ALIGN, "%s: x and w must be 16-byte aligned, scales and offsets 4-byte, y to its element",
                         name);
+    if (epi && epi->residual && epi->ldr < cols)
+        return bq::fail(BQ_ERR_SHAPE, "%s: rows of the residual are %lld elements apart, fewer than their %d", name,
+                        (long long)epi->ldr, cols);
+    if (epi && (!bq::aligned(epi->bias, 4) || !bq::aligned(epi->residual, es)))
+        return bq::fail(BQ_ERR_ALIGN, "%s: the bias must be 4-byte aligned, the residual to its element", name);
     const int experts = offsets ? std::min(E, rows) : 1;   // that can have rows
     // most row chunks and items there can be, for the grid and (as an int) inside the kernel
     auto chunks_of = [&](int most) { return (int64_t)bq::row_chunks(rows, most) + (offsets ? experts : 0); };
@@ -1042,14 +1188,21 @@ bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32
     if (s != BQ_OK) return s;
     const bq::WaitProbe probe = bq::wait_probe();
     const Args a{xscales, rows, offsets, E, wscales, n, k, kb, (n + kBlock - 1) / kBlock, cols,
-                 y, ydtype, ldy, bq::device_status_ptr(), probe.limit_ns, probe.skip_weight_copies, (int)chunks};
+                 y, ydtype, ldy, bq::device_status_ptr(), probe.limit_ns, probe.skip_weight_copies, (int)chunks,
+                 epi ? epi->bias : nullptr, epi && !swiglu ? epi->act : BQ_ACT_NONE, epi ? epi->scale : 1.f,
+                 epi ? epi->residual : nullptr, epi ? epi->ldr : 0};
+    // an end that changes nothing is none
+    const bool end = epi && (epi->bias || a.act != BQ_ACT_NONE || epi->scale != 1.f || epi->residual);
     CUtensorMap map_w, map_x;
     const bool mapped = swiglu ? gate_up_map(&map_w, w, E, n, k, wide ? 64 : 16) : weight_map(&map_w, w, E, n, k);
     if (!mapped || !row_map(&map_x, x, rows, k, wide ? 128 : LaneSmem::BOX))
         return bq::fail(BQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", name);
     cudaError_t e;
     if (wide) {
-        e = swiglu ? launch_wide<true>(map_w, map_x, a, items, st) : launch_wide<false>(map_w, map_x, a, items, st);
+        if (end) e = swiglu ? launch_wide<true, true>(map_w, map_x, a, items, st)
+                            : launch_wide<false, true>(map_w, map_x, a, items, st);
+        else e = swiglu ? launch_wide<true, false>(map_w, map_x, a, items, st)
+                        : launch_wide<false, false>(map_w, map_x, a, items, st);
     } else {
         // K split over a cluster while all clusters are resident at once (this GPU holds 76, 36 and 15 clusters of 2, 4
         // and 8 CTAs of this size) and the blocks saved pay for the cluster's sum, whose cost goes with the rows.
@@ -1063,8 +1216,10 @@ bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32
         if (items <= 15 && kb >= 8) split = 8;
         else if (items <= 36 && kb >= (few ? 6 : 8)) split = 4;
         else if (items <= 76 && kb >= (few ? 8 : 16)) split = 2;
-        e = swiglu ? launch_lanes<true>(map_w, map_x, a, items, split, st)
-                   : launch_lanes<false>(map_w, map_x, a, items, split, st);
+        if (end) e = swiglu ? launch_lanes<true, true>(map_w, map_x, a, items, split, st)
+                            : launch_lanes<false, true>(map_w, map_x, a, items, split, st);
+        else e = swiglu ? launch_lanes<true, false>(map_w, map_x, a, items, split, st)
+                        : launch_lanes<false, false>(map_w, map_x, a, items, split, st);
     }
     if (e != cudaSuccess) {
         cudaGetLastError();   // reported here
@@ -1072,6 +1227,13 @@ bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32
     }
     bq::note_launch();
     return bq::check_launch(name);
+}
+
+bq_status check_epilogue(const char* name, const bq_epilogue* epi) {
+    if (!epi) return bq::fail(BQ_ERR_NULL, "%s: the epilogue is NULL", name);
+    if (epi->act < BQ_ACT_NONE || epi->act > BQ_ACT_RELU2)
+        return bq::fail(BQ_ERR_SHAPE, "%s: unknown activation %d", name, epi->act);
+    return BQ_OK;
 }
 
 }  // namespace
@@ -1089,4 +1251,25 @@ extern "C" bq_status bq_moe_mm_fp8_b128(const uint8_t* x, const float* xscales, 
     if (rows > 0 && !offsets) return bq::fail(BQ_ERR_NULL, "bq_moe_mm_fp8_b128: offsets is NULL");
     return run_mm("bq_moe_mm_fp8_b128", x, xscales, rows, offsets, E, w, wscales, n, k, swiglu, y, ydtype, ldy,
                   (cudaStream_t)stream);
+}
+
+extern "C" bq_status bq_mm_fp8_b128_epilogue(const uint8_t* x, const float* xscales, int32_t m, const uint8_t* w,
+                                             const float* wscales, int32_t n, int32_t k, const bq_epilogue* epi, void* y,
+                                             int32_t ydtype, int64_t ldy, bq_stream_t stream) {
+    const bq_status s = check_epilogue("bq_mm_fp8_b128_epilogue", epi);
+    if (s != BQ_OK) return s;
+    return run_mm("bq_mm_fp8_b128_epilogue", x, xscales, m, nullptr, 1, w, wscales, n, k, epi->act == BQ_ACT_SWIGLU, y,
+                  ydtype, ldy, (cudaStream_t)stream, epi);
+}
+
+extern "C" bq_status bq_moe_mm_fp8_b128_epilogue(const uint8_t* x, const float* xscales, int32_t rows,
+                                                 const int32_t* offsets, int32_t E, const uint8_t* w,
+                                                 const float* wscales, int32_t n, int32_t k, const bq_epilogue* epi,
+                                                 void* y, int32_t ydtype, int64_t ldy, bq_stream_t stream) {
+    const char* name = "bq_moe_mm_fp8_b128_epilogue";
+    const bq_status s = check_epilogue(name, epi);
+    if (s != BQ_OK) return s;
+    if (rows > 0 && !offsets) return bq::fail(BQ_ERR_NULL, "%s: offsets is NULL", name);
+    return run_mm(name, x, xscales, rows, offsets, E, w, wscales, n, k, epi->act == BQ_ACT_SWIGLU, y, ydtype, ldy,
+                  (cudaStream_t)stream, epi);
 }

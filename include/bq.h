@@ -530,6 +530,166 @@ bq_status bq_moe_mm_fp8_b128(const uint8_t* x, const float* xscales, int32_t row
                              const float* wscales, int32_t n, int32_t k, int32_t swiglu, void* y,
                              int32_t ydtype, int64_t ldy, bq_stream_t stream);
 
+/*
+ * The same products with an end of their own, in the same pass:
+ *   y[r][c] = scale * act(product[r][c] + bias[c]) + residual[r][c]
+ * act: bq_activation; BQ_ACT_SWIGLU as swiglu = 1 above (its bias has n values,
+ * gate then up).  bias: device fp32 [n], of bq_moe_mm_fp8_b128_epilogue [E][n]
+ * (a row takes its expert's), or NULL.  residual: device rows of y's type and
+ * columns, ldr elements apart, aligned to the element, or NULL; it may be y
+ * itself (then with ldr = ldy) but not overlap it otherwise.  All of it in fp32
+ * before the one rounding to `ydtype`.  epi: host struct, read during the call.
+ * NaN of the product, bias or residual propagates through every activation.
+ * Errors: as above, plus BQ_ERR_SHAPE (unknown activation, ldr below the columns).
+ */
+typedef enum {
+    BQ_ACT_NONE = 0,
+    BQ_ACT_SWIGLU = 1,
+    BQ_ACT_SILU = 2,        /* v / (1 + exp(-v)) */
+    BQ_ACT_GELU = 3,        /* v * Phi(v), the normal distribution's Phi */
+    BQ_ACT_GELU_TANH = 4,   /* v / 2 * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3))) */
+    BQ_ACT_RELU = 5,        /* max(v, 0) */
+    BQ_ACT_RELU2 = 6        /* max(v, 0)^2 */
+} bq_activation;
+
+typedef struct {
+    int32_t act;
+    float scale;
+    const float* bias;
+    const void* residual;
+    int64_t ldr;
+} bq_epilogue;
+
+bq_status bq_mm_fp8_b128_epilogue(const uint8_t* x, const float* xscales, int32_t m,
+                                  const uint8_t* w, const float* wscales, int32_t n, int32_t k,
+                                  const bq_epilogue* epi, void* y, int32_t ydtype, int64_t ldy,
+                                  bq_stream_t stream);
+bq_status bq_moe_mm_fp8_b128_epilogue(const uint8_t* x, const float* xscales, int32_t rows,
+                                      const int32_t* offsets, int32_t E, const uint8_t* w,
+                                      const float* wscales, int32_t n, int32_t k,
+                                      const bq_epilogue* epi, void* y, int32_t ydtype, int64_t ldy,
+                                      bq_stream_t stream);
+
+/* ------------------------------------------------------------------ block to block
+ * The way out of a block and into the next, in one pass over the rows ([butter]:
+ * sigmoidScalarFMAResidual, the gated residual; gatedMixerNormMany).  With
+ * n(v) = v / sqrt(mean(v^2) + eps) and, per row t,
+ *   b     = post_gain * n(y), or y where post_gain is NULL
+ *   g     = the gate, its sigmoid (gate_sigmoid = 1), or 1 (BQ_GATE_NONE)
+ *   h_out = residual_scale * h + scale * g * b
+ *   x     = gain * n(h_out)                      (not computed where x is NULL)
+ * Everything is computed in fp32 and rounded once to the output's type; x comes
+ * from h_out before that rounding.
+ *
+ * bq_residual_norm_backward: with dh_out and dx the gradients of h_out and x
+ * (either may be NULL: none; then what only it needs, gain, may be NULL too),
+ * r = 1 / sqrt(mean(h_out^2) + eps), s the same of y, all sums in fp32:
+ *   G     = dh_out + r * gain * dx - h_out * r^3 * mean(gain * dx * h_out)
+ *   D     = scale * G,      dh = residual_scale * G
+ *   dy    = s * post_gain * D * g - y * s^3 * mean(post_gain * D * g * y), or D * g
+ *   dgate = D * b (times g * (1 - g) under a sigmoid), summed over what the gate is shared by
+ *   dgain = sum_t dx * h_out * r,   dpost_gain = sum_t D * g * y * s
+ * h_out is the forward pass's output (read only where dx is given).  dgain,
+ * dpost_gain: fp32 [H]; dgate: fp32 [T] or [H], for a gate per value rows of the
+ * gate's type.  Each of the three may be NULL (not computed).  Sums over rows
+ * have a fixed order: results do not change from run to run.
+ *
+ * y, h, h_out, x and their gradients: device rows of H elements of y_dtype (y,
+ * dy), h_dtype (h, h_out, dh_out, dh) or x_dtype (x, dx), ld* elements apart.
+ * H a multiple of 8, at most 16384; rows start and end on 16-byte boundaries.
+ * gain, post_gain: gain_dtype [H], 16-byte aligned.  gate: gate_dtype, [T]
+ * (aligned to its element), [H] (16-byte aligned) or rows like y.  Outputs must
+ * not overlap inputs, but h_out may be h, and dh may be dh_out.
+ * workspace of the backward pass: device, at least
+ * bq_residual_norm_backward_workspace_bytes(T, H) bytes, 16-byte aligned; needed
+ * only for dgain, dpost_gain and the dgate of a gate per channel.
+ * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_FORMAT (an unknown type), BQ_ERR_ALIGN,
+ * BQ_ERR_WORKSPACE, BQ_ERR_CUDA.  T == 0: a no-op, but sums over rows become 0.
+ */
+typedef enum {
+    BQ_GATE_NONE = 0,
+    BQ_GATE_TOKEN = 1,     /* [T]: a factor per row, as a shared expert's gate */
+    BQ_GATE_CHANNEL = 2,   /* [H]: a factor per column, as a layer scale */
+    BQ_GATE_FULL = 3       /* [T][H] */
+} bq_gate;
+
+typedef struct {
+    int32_t T, H;
+    int32_t y_dtype, h_dtype, x_dtype, gain_dtype, gate_dtype;   /* bq_dtype */
+    int32_t gate_kind;       /* bq_gate */
+    int32_t gate_sigmoid;    /* 0 or 1 */
+    float scale, residual_scale, eps;
+    const void* gain;        /* device, of the norm that gives x */
+    const void* post_gain;   /* device, of the norm of y; NULL: none */
+    const void* gate;        /* device */
+    int64_t ldgate;          /* BQ_GATE_FULL */
+} bq_residual_norm_desc;
+
+bq_status bq_residual_norm(const bq_residual_norm_desc* desc, const void* y, int64_t ldy,
+                           const void* h, int64_t ldh, void* h_out, int64_t ldho, void* x,
+                           int64_t ldx, bq_stream_t stream);
+size_t bq_residual_norm_backward_workspace_bytes(int32_t T, int32_t H);
+bq_status bq_residual_norm_backward(const bq_residual_norm_desc* desc, const void* y, int64_t ldy,
+                                    const void* h_out, int64_t ldho, const void* dh_out,
+                                    int64_t lddho, const void* dx, int64_t lddx, void* dy,
+                                    int64_t lddy, void* dh, int64_t lddh, float* dgain,
+                                    float* dpost_gain, void* dgate, int64_t lddgate,
+                                    void* workspace, size_t workspace_bytes, bq_stream_t stream);
+
+/* ------------------------------------------------------------------ router training
+ * Per-expert counts, mean probabilities, the balance loss and the z-loss of a
+ * router's logits, over one batch or over the sequences of it.  Rows
+ * [seq_offsets[s], seq_offsets[s + 1]) are sequence s (device int32 [S + 1],
+ * ascending in [0, T]); rows before the first and behind the last are not read.
+ * seq_offsets NULL: S = 1, all T rows.  z = logits + bias under
+ * BQ_SCORE_SOFTMAX; under the other rules the bias only selects, so bias must
+ * be NULL and z = logits.
+ *   p[t]         = softmax(z[t]), under BQ_SCORE_SQRTSOFTPLUS score / sum of scores
+ *   counts[s][e] = pairs (t, j) of the sequence with ids[t][j] = e
+ *   probs[s][e]  = mean of p[t][e] over its n_s rows (0 for an empty sequence)
+ *   losses[0]    = mean over the sequences that have rows of
+ *                  sum_e E * counts[s][e] / (k * n_s) * probs[s][e]
+ *   losses[1]    = mean over all rows of sequences of logsumexp(z[t])^2
+ * A row of -inf only has probabilities 0 and adds 0 to losses[1]; NaN and +inf
+ * propagate.  An id outside [0, E) sets BQ_DEV_BAD_EXPERT_ID and counts nowhere.
+ * Offsets that descend or leave [0, T] set BQ_DEV_BAD_ROW; what such a call
+ * returns is undefined.  Sums are fp32 in a fixed order.
+ *
+ * bq_moe_route_backward: the gradient with respect to the logits of what
+ * bq_moe_route(_scored) returned, given dweights (fp32 [T][k], as
+ * bq_moe_combine_backward writes them; NULL: none), and of the two losses,
+ * given dlosses (device fp32 [2]; NULL: none) and the counts of the forward
+ * call; selection and counts are constants.
+ *   softmax rules:  dlogits[ids[j]] += w_j * (dweights_j - sum_i w_i dweights_i), w over the k selected
+ *   score rule:     dlogits[ids[j]] += scale * dweights_j * score'(z)
+ * ids are read only with dweights; those outside [0, E) set
+ * BQ_DEV_BAD_EXPERT_ID and are left out of the k.  dlogits: device [T][E] of
+ * `dtype`, computed in fp32 and rounded once; rows that belong to no sequence
+ * are left as they were.  dbias: fp32 [E], the sum of the gradient over the
+ * rows written (BQ_SCORE_SOFTMAX only), or NULL; it alone needs the workspace.
+ *
+ * logits: device fp32 [T][E]; ids int32 [T][k]; counts int32 [S][E]; probs fp32
+ * [S][E]; losses fp32 [2]; all 4-byte aligned, dlogits to its element.  E in
+ * 1..1024, k in 1..min(8, E), S in 1..65536.  workspace: device, 256-byte
+ * aligned, at least bq_moe_balance_workspace_bytes(T, E, S) or
+ * bq_moe_route_backward_workspace_bytes(T, E) bytes (0: invalid sizes).
+ * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_FORMAT, BQ_ERR_ALIGN,
+ * BQ_ERR_WORKSPACE, BQ_ERR_CUDA.  T == 0: counts, probs, losses and dbias become 0.
+ */
+size_t bq_moe_balance_workspace_bytes(int32_t T, int32_t E, int32_t S);
+bq_status bq_moe_balance_loss(const float* logits, const float* bias, int32_t T, int32_t E,
+                              const int32_t* ids, int32_t k, int32_t scoring,
+                              const int32_t* seq_offsets, int32_t S, int32_t* counts, float* probs,
+                              float* losses, void* workspace, size_t workspace_bytes,
+                              bq_stream_t stream);
+size_t bq_moe_route_backward_workspace_bytes(int32_t T, int32_t E);
+bq_status bq_moe_route_backward(const float* logits, const float* bias, int32_t T, int32_t E,
+                                const int32_t* ids, int32_t k, int32_t scoring, float scale,
+                                const float* dweights, const int32_t* counts,
+                                const float* dlosses, const int32_t* seq_offsets, int32_t S,
+                                void* dlogits, int32_t dtype, float* dbias, void* workspace,
+                                size_t workspace_bytes, bq_stream_t stream);
+
 /* ------------------------------------------------------------------ observability
  * Stage timing: while set, every bq_moe_gather_qmm call on this host thread
  * records `start` (a cudaEvent_t) on its stream immediately before the

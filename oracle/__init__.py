@@ -10,3 +10,4 @@ written from the pages' formulas.  It shares no code with the CUDA path.
 See ``oracle/bq_oracle.py`` for the functions and the passages each follows.
 """
 from .bq_oracle import *  # noqa: F401,F403
+from .block_oracle import *  # noqa: F401,F403
