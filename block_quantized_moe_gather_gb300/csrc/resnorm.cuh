@@ -1,0 +1,303 @@
+// Shared by the two directions of the residual norm: row types, packed fp32
+// arithmetic, sums over a row, argument checks.
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+
+#include "row_types.cuh"
+
+namespace bq {
+namespace resnorm {
+
+constexpr int kMaxH = 16384;
+constexpr int kSms = 152;
+constexpr int kAny = -1;   // a row type that is read from the arguments
+
+enum { GATE_NONE = BQ_GATE_NONE, GATE_TOKEN = BQ_GATE_TOKEN, GATE_CHANNEL = BQ_GATE_CHANNEL, GATE_FULL = BQ_GATE_FULL };
+
+struct Rows {
+    uint8_t* p;
+    int64_t ld;    // bytes
+    int dtype;
+};
+
+struct Gate {
+    const uint8_t* p;
+    int dtype, kind, sigmoid;
+};
+
+// Two fp32 values in a register pair: the packed instructions do both in one issue slot, and these kernels would be
+// bound by issue without them.
+typedef unsigned long long f32x2;
+
+__device__ __forceinline__ f32x2 two(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 both(float v) { return two(v, v); }
+
+__device__ __forceinline__ float2 parts_of(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float sum2(f32x2 v) {
+    const float2 p = parts_of(v);
+    return p.x + p.y;
+}
+
+// Eight values of a row.
+struct Vec {
+    f32x2 p[4];
+};
+
+__device__ __forceinline__ Vec same8(float v) { return {both(v), both(v), both(v), both(v)}; }
+
+// From their 16 bytes, or the two 16-byte halves of fp32.
+template <int DT>
+__device__ __forceinline__ Vec unpack8(const uint4& lo, const uint4& hi, int dtype) {
+    const int dt = DT == kAny ? dtype : DT;
+    Vec r;
+    if (dt == BQ_DT_F32) {
+        r.p[0] = two(__uint_as_float(lo.x), __uint_as_float(lo.y));
+        r.p[1] = two(__uint_as_float(lo.z), __uint_as_float(lo.w));
+        r.p[2] = two(__uint_as_float(hi.x), __uint_as_float(hi.y));
+        r.p[3] = two(__uint_as_float(hi.z), __uint_as_float(hi.w));
+    } else {
+        float f[8];
+        if (dt == BQ_DT_F16) bq::RowVec<BQ_DT_F16>::unpack(lo, f);
+        else bq::RowVec<BQ_DT_BF16>::unpack(lo, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.p[j] = two(f[2 * j], f[2 * j + 1]);
+    }
+    return r;
+}
+
+// Vector i of a row in global memory.
+template <int DT>
+__device__ __forceinline__ Vec load8(const uint8_t* row, int i, int dtype) {
+    const bool wide = (DT == kAny ? dtype : DT) == BQ_DT_F32;
+    const uint4* p = reinterpret_cast<const uint4*>(row) + (wide ? 2 * i : i);
+    const uint4 lo = p[0];
+    return unpack8<DT>(lo, wide ? p[1] : lo, dtype);
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(uint8_t* row, int i, int dtype, const Vec& v) {
+    const int dt = DT == kAny ? dtype : DT;
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 x = parts_of(v.p[j]);
+        f[2 * j] = x.x;
+        f[2 * j + 1] = x.y;
+    }
+    if (dt == BQ_DT_F32) {
+        reinterpret_cast<float4*>(row)[2 * i] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(row)[2 * i + 1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+        reinterpret_cast<uint4*>(row)[i] =
+            dt == BQ_DT_F16 ? bq::RowVec<BQ_DT_F16>::pack(f) : bq::RowVec<BQ_DT_BF16>::pack(f);
+    }
+}
+
+__device__ __forceinline__ float load1(const uint8_t* p, int64_t i, int dtype) {
+    if (dtype == BQ_DT_F32) return reinterpret_cast<const float*>(p)[i];
+    if (dtype == BQ_DT_F16) return __half2float(reinterpret_cast<const __half*>(p)[i]);
+    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.f, 1.f + expf(-v)); }
+
+__device__ __forceinline__ Vec sigmoid8(const Vec& v) {
+    Vec r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 x = parts_of(v.p[j]);
+        r.p[j] = two(sigmoid_f(x.x), sigmoid_f(x.y));
+    }
+    return r;
+}
+
+struct Columns {
+    const uint8_t *gain, *post;        // NULL: none
+    int gain_dtype;
+    Gate gate;
+    float scale;
+};
+
+// The factor that a row's branch has as a whole: a gate per token, or 1.
+__device__ __forceinline__ float token_factor(const Gate& gate, int64_t t, bool live) {
+    if (!live || gate.kind != GATE_TOKEN) return 1.f;
+    const float f = load1(gate.p, t, gate.dtype);
+    return gate.sigmoid ? sigmoid_f(f) : f;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float peer_load(const float* p, int rank) {
+    float v;
+    asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
+                 : "=f"(v) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return v;
+}
+
+// What the sums over a row go through.  Consecutive sums take different halves, so a half is written again only
+// behind the barrier of the sum between.
+struct SumBuf {
+    float warp[2][16][8];
+    float cta[2][8];
+};
+
+// One sum over the threads of a row, the same in each: lanes and warps (16 at most) by butterflies.
+__device__ __forceinline__ float row_sum(float v, SumBuf& buf, int& turn) {
+#pragma unroll
+    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return v;
+    float (*mine)[8] = buf.warp[turn] + threadIdx.y * warps;
+    if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5][0] = v;
+    __syncthreads();
+    const int w = threadIdx.x & 15;
+    v = w < warps ? mine[w][0] : 0.f;
+#pragma unroll
+    for (int off = 8; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    turn ^= 1;
+    return v;
+}
+
+// Eight sums at once, of a row that a cluster's CTAs may share.  Three steps halve the sums that a lane holds while
+// they double the lanes added (7 exchanges instead of 24), and the warps' sums are added with a sum a lane.
+template <bool CLUSTER>
+__device__ __forceinline__ void row_sums(float (&v)[8], SumBuf& buf, int& turn, int ranks) {
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int half = 4; half; half >>= 1) {
+        const bool upper = lane & (4 * half);
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float send = upper ? v[i] : v[i + half], keep = upper ? v[i + half] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * half);
+        }
+    }
+    // lanes 4 n .. 4 n + 3 hold sum n
+    float t = v[0];
+    t += __shfl_xor_sync(0xffffffffu, t, 2);
+    t += __shfl_xor_sync(0xffffffffu, t, 1);
+    int at = 4;   // lanes that hold different sums
+    if (warps > 1 || CLUSTER) {
+        float (*mine)[8] = buf.warp[turn] + threadIdx.y * warps;
+        if ((lane & 3) == 0) mine[threadIdx.x >> 5][lane >> 2] = t;
+        __syncthreads();
+        t = 0.f;
+        for (int w = lane >> 3; w < warps; w += 4) t += mine[w][lane & 7];
+        t += __shfl_xor_sync(0xffffffffu, t, 16);
+        t += __shfl_xor_sync(0xffffffffu, t, 8);
+        at = 1;
+        if (CLUSTER) {
+            if (threadIdx.x < 8) buf.cta[turn][threadIdx.x] = t;
+            cluster_sync();
+            t = 0.f;
+            for (int r = 0; r < ranks; ++r) t += peer_load(&buf.cta[turn][lane & 7], r);
+        }
+        turn ^= 1;
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n) v[n] = __shfl_sync(0xffffffffu, t, n * at);
+}
+
+// ---------------------------------------------------------------- host side
+inline bq_status check_desc(const char* name, const bq_residual_norm_desc* d, bool x) {
+    if (!d) return bq::fail(BQ_ERR_NULL, "%s: desc is NULL", name);
+    if (d->T < 0 || d->H < 8 || d->H % 8 || d->H > kMaxH)
+        return bq::fail(BQ_ERR_SHAPE, "%s: T = %d, H = %d (H must be a multiple of 8, 8 to %d)", name, d->T, d->H, kMaxH);
+    const int32_t types[4] = {d->y_dtype, d->h_dtype, x ? d->x_dtype : BQ_DT_F32, d->gain_dtype};
+    for (int32_t t : types)
+        if (bq::dtype_size(t) == 0) return bq::fail(BQ_ERR_FORMAT, "%s: unknown element type %d", name, t);
+    if (d->gate_kind < BQ_GATE_NONE || d->gate_kind > BQ_GATE_FULL)
+        return bq::fail(BQ_ERR_SHAPE, "%s: unknown gate kind %d", name, d->gate_kind);
+    if (d->gate_sigmoid != 0 && d->gate_sigmoid != 1)
+        return bq::fail(BQ_ERR_SHAPE, "%s: gate_sigmoid must be 0 or 1, not %d", name, d->gate_sigmoid);
+    const bool gated = d->gate_kind != BQ_GATE_NONE;
+    if (gated && bq::dtype_size(d->gate_dtype) == 0)
+        return bq::fail(BQ_ERR_FORMAT, "%s: unknown element type %d", name, d->gate_dtype);
+    if (!(d->eps >= 0.f) || d->eps > 3.0e38f) return bq::fail(BQ_ERR_SHAPE, "%s: eps must be finite and >= 0", name);
+    if (d->T == 0) return BQ_OK;
+    if (x && !d->gain) return bq::fail(BQ_ERR_NULL, "%s: gain is NULL", name);
+    if (gated && !d->gate) return bq::fail(BQ_ERR_NULL, "%s: gate is NULL", name);
+    if (!bq::aligned(d->gain, 16) || !bq::aligned(d->post_gain, 16))
+        return bq::fail(BQ_ERR_ALIGN, "%s: gains must be 16-byte aligned", name);
+    if (!gated) return BQ_OK;
+    const int es = bq::dtype_size(d->gate_dtype);
+    if (d->gate_kind == BQ_GATE_FULL) return bq::check_rows(name, "gate", d->gate, d->H, d->ldgate, es);
+    if (!bq::aligned(d->gate, d->gate_kind == BQ_GATE_CHANNEL ? 16 : es))
+        return bq::fail(BQ_ERR_ALIGN, "%s: the gate is not aligned", name);
+    return BQ_OK;
+}
+
+inline Rows rows(const void* p, int64_t ld, int32_t dtype) {
+    return {static_cast<uint8_t*>(const_cast<void*>(p)), ld * bq::dtype_size(dtype), dtype};
+}
+
+inline Columns columns_of(const bq_residual_norm_desc* d, bool x) {
+    const Gate gate{static_cast<const uint8_t*>(d->gate), d->gate_dtype, d->gate_kind, d->gate_sigmoid};
+    return {x ? static_cast<const uint8_t*>(d->gain) : nullptr, static_cast<const uint8_t*>(d->post_gain), d->gain_dtype,
+            gate, d->scale};
+}
+
+template <int Y, int H, int X>
+struct Types {
+    static constexpr int y = Y, h = H, x = X;
+};
+
+// Calls f with the row types as constants: one type for all, a 16-bit type with an fp32 block output (as this
+// library's MoE layer leaves it) or with an fp32 stream; other mixes read their types from the arguments.
+template <typename F>
+void with_types(int y, int h, int x, F f) {
+    constexpr int F32 = BQ_DT_F32, F16 = BQ_DT_F16, BF16 = BQ_DT_BF16;
+    if (y == F32 && h == F32 && x == F32) f(Types<F32, F32, F32>());
+    else if (y == F16 && h == F16 && x == F16) f(Types<F16, F16, F16>());
+    else if (y == BF16 && h == BF16 && x == BF16) f(Types<BF16, BF16, BF16>());
+    else if (y == F32 && h == F16 && x == F16) f(Types<F32, F16, F16>());
+    else if (y == F32 && h == BF16 && x == BF16) f(Types<F32, BF16, BF16>());
+    else if (y == F16 && h == F32 && x == F16) f(Types<F16, F32, F16>());
+    else if (y == BF16 && h == F32 && x == BF16) f(Types<BF16, F32, BF16>());
+    else f(Types<kAny, kAny, kAny>());
+}
+
+inline bq_status launched(const char* name, cudaError_t e) {
+    if (e != cudaSuccess) {
+        cudaGetLastError();   // reported here
+        return bq::fail(BQ_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
+    }
+    bq::note_launch();
+    return bq::check_launch(name);
+}
+
+
+}  // namespace resnorm
+}  // namespace bq

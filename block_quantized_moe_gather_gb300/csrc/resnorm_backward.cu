@@ -1,0 +1,523 @@
+// Gradients of the residual norm (resnorm.cu has the formulas).
+//
+// With P = scale * post_gain * (a gate per channel), f the gate per token and w
+// the one per value (or 1 each), yn = s y (y without a post norm):
+//   dy = f (s P w G - y s^3 mean(P w G y)), or f P w G;   Q = sum over rows of f w G yn
+//   dpost_gain = scale gate Q;   dgate per channel = scale gate' post_gain Q
+//   dgate per token = gate' sum of P G yn;   dgate per value = P G yn w'
+// so one column sum serves both gradients of the branch, and the constants are
+// folded in at the end.  The sum of P w G y is linear in G = dh' + r gain dx - h' c:
+// its three parts need neither r nor c, so every sum over a row is formed in one
+// pass and one barrier, and a second pass writes all outputs.
+#include "resnorm.cuh"
+
+namespace {
+
+using namespace bq::resnorm;
+
+constexpr int kVpt = 2;   // vectors of a thread
+
+// Where a thread keeps its vectors of a row in flight: planes of 16 bytes per vector of the block (an fp32 vector takes
+// two), so that a warp's lie in distinct banks, and places that are constants.
+__host__ __device__ constexpr int planes(int dt) { return dt == BQ_DT_F16 || dt == BQ_DT_BF16 ? 1 : 2; }
+
+template <int DY, int DH, int DX, int THREADS>
+struct Stage {
+    static constexpr int kPlane = THREADS * kVpt * 16;
+    static constexpr int kY = 0, kOut = kY + planes(DY) * kPlane, kDx = kOut + planes(DH) * kPlane;
+    static constexpr int kDout = kDx + planes(DX) * kPlane, kGate = kDout + planes(DH) * kPlane;   // two planes more
+    static constexpr int kGain = 0, kBranch = 2 * kPlane, kConstants = 4 * kPlane;   // fp32, in front of the stages
+};
+
+struct BackwardArgs {
+    int T, H, slice;                // slice: vectors of a row in this CTA (a cluster shares a row)
+    int stages, stage_bytes;
+    Rows y, out, dout, dx;          // dout.p or dx.p NULL: no gradient comes that way
+    Rows dy, dh;
+    Columns columns;
+    Rows full, dgate;               // a gate per value; dgate of one per token (fp32) or per value, p NULL: not computed
+    float residual_scale, eps;
+    float* part;                    // [arrays][parts][H] column sums: dgain, Q
+    int sum_gain, sum_branch;       // which array each is, or -1
+};
+
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// A thread's vectors of a row into a stage.
+template <int DT, int PLANE>
+__device__ __forceinline__ void fetch(uint32_t dst, const uint8_t* src, int dtype, const bool (&has)[kVpt]) {
+    const bool wide = (DT == kAny ? dtype : DT) == BQ_DT_F32;
+#pragma unroll
+    for (int v = 0; v < kVpt; ++v) {
+        if (!has[v]) continue;
+        const uint8_t* p = src + v * (int)blockDim.x * (wide ? 32 : 16);
+        copy16_async(dst + v * (PLANE / kVpt), p);
+        if (wide) copy16_async(dst + v * (PLANE / kVpt) + PLANE, p + 16);
+    }
+}
+
+template <int DT, int PLANE>
+__device__ __forceinline__ Vec staged8(const uint8_t* at, int v, int dtype) {
+    const uint8_t* p = at + v * (PLANE / kVpt);
+    const uint4 lo = *reinterpret_cast<const uint4*>(p);
+    if ((DT == kAny ? dtype : DT) != BQ_DT_F32) return unpack8<DT>(lo, lo, dtype);
+    return unpack8<BQ_DT_F32>(lo, *reinterpret_cast<const uint4*>(p + PLANE), dtype);
+}
+
+template <int PLANE>
+__device__ __forceinline__ void keep8(uint8_t* at, int v, const Vec& x) {
+    uint8_t* p = at + v * (PLANE / kVpt);
+    *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(x.p[0], x.p[1]);
+    *reinterpret_cast<ulonglong2*>(p + PLANE) = make_ulonglong2(x.p[2], x.p[3]);
+}
+
+template <int PLANE>
+__device__ __forceinline__ Vec kept8(const uint8_t* at, int v) {
+    const uint8_t* p = at + v * (PLANE / kVpt);
+    const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(p), hi = *reinterpret_cast<const ulonglong2*>(p + PLANE);
+    return {{lo.x, lo.y, hi.x, hi.y}};
+}
+
+// blockDim.x threads take a row (or a cluster's slice of one), a thread the vectors x, x + blockDim.x of it;
+// blockDim.y rows at a time.  Blocks walk over the rows; a thread's columns stay the same, so it adds their column sums
+// in registers.  Each thread fetches the vectors that it will use itself, rows ahead, into shared memory of its own
+// (cp.async): the loads need no registers while they are in flight, and no barrier when they land.  A vector behind the
+// row's last, and a row behind the last, is zeros there: the arithmetic goes over all alike.
+template <int DY, int DH, int DX, int THREADS, bool POST, bool CLUSTER>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS)
+residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
+    using L = Stage<DY, DH, DX, THREADS>;
+    constexpr int PLANE = L::kPlane;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ SumBuf s_buf;
+    bq::grid_dependency_wait();   // launched behind whatever precedes it on the stream
+    bq::allow_dependents();
+    const Gate& gate = a.columns.gate;
+    const bool has_x = a.dx.p != nullptr, full = gate.kind == GATE_FULL;
+    const bool token = gate.kind == GATE_TOKEN && a.dgate.p;   // its gradient is wanted
+    const int vecs = a.H / 8, tid = threadIdx.y * blockDim.x + threadIdx.x;
+    const int ranks = CLUSTER ? (vecs + a.slice - 1) / a.slice : 1, rank = CLUSTER ? (int)cluster_rank() : 0;
+    const int mine = min(a.slice, vecs - rank * a.slice), vec0 = rank * a.slice + threadIdx.x;
+    bool has[kVpt];
+#pragma unroll
+    for (int v = 0; v < kVpt; ++v) has[v] = (int)(threadIdx.x + v * blockDim.x) < mine;
+    const int64_t step = (int64_t)(gridDim.x / ranks) * blockDim.y, block0 = (int64_t)(blockIdx.x / ranks) * blockDim.y;
+    // a thread's first vector in the rows of a block, from the block's first row on (the host made sure that it is an int)
+    auto offset = [&](const Rows& m) { return (int)threadIdx.y * (int)m.ld + vec0 * (m.dtype == BQ_DT_F32 ? 32 : 16); };
+    const int o_y = offset(a.y), o_out = offset(a.out), o_dx = offset(a.dx), o_dout = offset(a.dout);
+    const int o_dy = offset(a.dy), o_dh = offset(a.dh);
+    const int end = L::kConstants + a.stages * a.stage_bytes;
+    for (int i = tid * 16; i < end; i += THREADS * 16) *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
+    uint8_t* own = smem + tid * 16;
+    const uint32_t own_u32 = (uint32_t)__cvta_generic_to_shared(own);
+    auto fetch_row = [&](int stage, int64_t r0) {
+        const uint32_t to = own_u32 + stage;
+        if (r0 + threadIdx.y < a.T) {
+            fetch<DY, PLANE>(to + L::kY, a.y.p + r0 * a.y.ld + o_y, a.y.dtype, has);
+            if (has_x) {
+                fetch<DH, PLANE>(to + L::kOut, a.out.p + r0 * a.out.ld + o_out, a.out.dtype, has);
+                fetch<DX, PLANE>(to + L::kDx, a.dx.p + r0 * a.dx.ld + o_dx, a.dx.dtype, has);
+            }
+            if (a.dout.p) fetch<DH, PLANE>(to + L::kDout, a.dout.p + r0 * a.dout.ld + o_dout, a.dout.dtype, has);
+            if (full) fetch<kAny, PLANE>(to + L::kGate, a.full.p + r0 * a.full.ld + offset(a.full), a.full.dtype, has);
+        } else if (r0 < a.T) {
+            for (int i = 0; i < a.stage_bytes; i += PLANE / kVpt)
+                *reinterpret_cast<uint4*>(own + stage + i) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int ahead = L::kConstants;
+    int64_t next = block0;
+    for (int i = 0; i < a.stages - 1; ++i) {
+        fetch_row(ahead, next);
+        ahead += a.stage_bytes;
+        next += step;
+    }
+#pragma unroll
+    for (int v = 0; v < kVpt; ++v) {   // the constants of the thread's columns, while its first rows are on their way
+        if (!has[v]) continue;
+        const int i = vec0 + v * blockDim.x;
+        if (has_x) keep8<PLANE>(own + L::kGain, v, load8<kAny>(a.columns.gain, i, a.columns.gain_dtype));
+        Vec b = same8(a.columns.scale);
+        if (POST) {
+            const Vec p = load8<kAny>(a.columns.post, i, a.columns.gain_dtype);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b.p[j] = mul2(b.p[j], p.p[j]);
+        }
+        if (gate.kind == GATE_CHANNEL) {
+            Vec f = load8<kAny>(gate.p, i, gate.dtype);
+            if (gate.sigmoid) f = sigmoid8(f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b.p[j] = mul2(b.p[j], f.p[j]);
+        }
+        keep8<PLANE>(own + L::kBranch, v, b);
+    }
+    Vec gain_sum[kVpt], branch[kVpt];
+#pragma unroll
+    for (int v = 0; v < kVpt; ++v) gain_sum[v] = branch[v] = same8(0.f);
+    const float inv_h = 1.f / (float)a.H;
+    int stage = L::kConstants, turn = 0;
+    for (int64_t t0 = block0; t0 < a.T; t0 += step) {
+        const int64_t t = t0 + threadIdx.y;
+        const bool live = t < a.T;
+        if (a.stages == 2) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        else asm volatile("cp.async.wait_group 1;" ::: "memory");
+        fetch_row(ahead, next);
+        next += step;
+        ahead = ahead + a.stage_bytes == end ? L::kConstants : ahead + a.stage_bytes;
+        const uint8_t* st = own + stage;
+        stage = stage + a.stage_bytes == end ? L::kConstants : stage + a.stage_bytes;
+        const float f = token_factor(gate, t, live);
+        // sums over the row: h'^2, gain dx h', y^2, and P w y times dh', gain dx and h'
+        f32x2 hh = both(0.f), dh = both(0.f), yy = both(0.f), in_dout = both(0.f), in_dx = both(0.f), in_h = both(0.f);
+#pragma unroll
+        for (int v = 0; v < kVpt; ++v) {
+            Vec h, q;   // h', gain dx
+            if (has_x) {
+                h = staged8<DH, PLANE>(st + L::kOut, v, a.out.dtype);
+                const Vec d = staged8<DX, PLANE>(st + L::kDx, v, a.dx.dtype);
+                q = kept8<PLANE>(own + L::kGain, v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    q.p[j] = mul2(d.p[j], q.p[j]);
+                    hh = fma2(h.p[j], h.p[j], hh);
+                    dh = fma2(q.p[j], h.p[j], dh);
+                }
+            }
+            if (!POST && !token) continue;
+            const Vec y = staged8<DY, PLANE>(st + L::kY, v, a.y.dtype);
+            Vec p = kept8<PLANE>(own + L::kBranch, v);
+            if (full) {
+                Vec w = staged8<kAny, PLANE>(st + L::kGate, v, a.full.dtype);
+                if (gate.sigmoid) w = sigmoid8(w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) p.p[j] = mul2(p.p[j], w.p[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                yy = fma2(y.p[j], y.p[j], yy);
+                p.p[j] = mul2(p.p[j], y.p[j]);
+            }
+            if (has_x) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    in_dx = fma2(p.p[j], q.p[j], in_dx);
+                    in_h = fma2(p.p[j], h.p[j], in_h);
+                }
+            }
+            if (a.dout.p) {
+                const Vec o = staged8<DH, PLANE>(st + L::kDout, v, a.dout.dtype);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) in_dout = fma2(p.p[j], o.p[j], in_dout);
+            }
+        }
+        float sums[8] = {sum2(hh), sum2(dh), sum2(yy), sum2(in_dout), sum2(in_dx), sum2(in_h), 0.f, 0.f};
+        if (has_x || POST || token) row_sums<CLUSTER>(sums, s_buf, turn, ranks);
+        // a row behind the last has sums of 0, whose roots would be infinite without eps
+        const float r = live ? rsqrtf(__fmaf_rn(sums[0], inv_h, a.eps)) : 0.f, c = -r * r * r * (sums[1] * inv_h);
+        const float s = !POST ? 1.f : live ? rsqrtf(__fmaf_rn(sums[2], inv_h, a.eps)) : 0.f;
+        float inner = sums[3];           // of P w G y
+        if (has_x) inner += r * sums[4] + c * sums[5];
+        if (token && live && threadIdx.x == 0 && rank == 0)
+            reinterpret_cast<float*>(a.dgate.p)[t] = s * inner * (gate.sigmoid ? f * (1.f - f) : 1.f);
+        const float fs = f * s, cy = -fs * s * s * (inner * inv_h);
+        uint8_t* to_dh = a.dh.p + t0 * a.dh.ld + o_dh;
+        uint8_t* to_dy = a.dy.p + t0 * a.dy.ld + o_dy;
+#pragma unroll
+        for (int v = 0; v < kVpt; ++v) {
+            const bool stored = live && has[v];
+            Vec G = a.dout.p ? staged8<DH, PLANE>(st + L::kDout, v, a.dout.dtype) : same8(0.f);
+            if (has_x) {
+                const Vec k = kept8<PLANE>(own + L::kGain, v), h = staged8<DH, PLANE>(st + L::kOut, v, a.out.dtype);
+                const Vec d = staged8<DX, PLANE>(st + L::kDx, v, a.dx.dtype);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f32x2 dr = mul2(d.p[j], both(r));
+                    gain_sum[v].p[j] = fma2(dr, h.p[j], gain_sum[v].p[j]);
+                    G.p[j] = fma2(h.p[j], both(c), fma2(k.p[j], dr, G.p[j]));
+                }
+            }
+            if (stored) {
+                Vec o;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o.p[j] = mul2(G.p[j], both(a.residual_scale));
+                store8<DH>(to_dh, v * blockDim.x, a.dh.dtype, o);
+            }
+            const Vec p = kept8<PLANE>(own + L::kBranch, v), y = staged8<DY, PLANE>(st + L::kY, v, a.y.dtype);
+            if (full) {
+                Vec w = staged8<kAny, PLANE>(st + L::kGate, v, a.full.dtype), dw;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) dw.p[j] = mul2(mul2(G.p[j], p.p[j]), mul2(y.p[j], both(s)));
+                if (gate.sigmoid) {
+                    w = sigmoid8(w);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        dw.p[j] = mul2(dw.p[j], mul2(w.p[j], fma2(w.p[j], both(-1.f), both(1.f))));
+                }
+                if (a.dgate.p && stored)
+                    store8<kAny>(a.dgate.p + t0 * a.dgate.ld + offset(a.dgate), v * blockDim.x, a.dgate.dtype, dw);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) G.p[j] = mul2(G.p[j], w.p[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                G.p[j] = mul2(G.p[j], both(fs));
+                branch[v].p[j] = fma2(G.p[j], y.p[j], branch[v].p[j]);
+                G.p[j] = mul2(G.p[j], p.p[j]);
+                if (POST) G.p[j] = fma2(y.p[j], both(cy), G.p[j]);
+            }
+            if (stored) store8<DY>(to_dy, v * blockDim.x, a.dy.dtype, G);
+        }
+    }
+    // the block's column sums: its rows added up in shared memory (the stages are free), then to its part
+    const int64_t parts = gridDim.x / ranks, part = blockIdx.x / ranks;
+    const int which[2] = {a.sum_gain, a.sum_branch};
+    float* s_sum = reinterpret_cast<float*>(smem);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (which[k] < 0) continue;
+        uint8_t* out = reinterpret_cast<uint8_t*>(a.part + (which[k] * parts + part) * a.H);
+        if (blockDim.y > 1) __syncthreads();
+#pragma unroll
+        for (int v = 0; v < kVpt; ++v) {
+            if (!has[v]) continue;
+            const Vec& sum = k ? branch[v] : gain_sum[v];
+            if (blockDim.y == 1) store8<BQ_DT_F32>(out, vec0 + v * blockDim.x, 0, sum);
+            else store8<BQ_DT_F32>(smem, threadIdx.y * vecs + threadIdx.x + v * blockDim.x, 0, sum);
+        }
+        if (blockDim.y == 1) continue;
+        __syncthreads();
+        for (int i = tid; i < a.H; i += blockDim.x * blockDim.y) {   // blocks of several rows are not clusters
+            float sum = 0.f;
+            for (int j = 0; j < (int)blockDim.y; ++j) sum += s_sum[j * a.H + i];
+            reinterpret_cast<float*>(out)[i] = sum;
+        }
+    }
+    if (CLUSTER) cluster_sync();   // peers may still be reading this CTA's sums
+}
+
+struct SumArgs {
+    const float* part;   // [arrays][parts][H]
+    int64_t parts;
+    int H;
+    float *dgain, *dpost, *dgate;     // NULL: not computed
+    int sum_gain, sum_branch;
+    Columns columns;
+};
+
+constexpr int kSumThreads = 512;
+
+// The parts of 32 columns of one array (blockIdx.y) added up, each warp a share of them, and its gradients' constants.
+__global__ void __launch_bounds__(kSumThreads)
+sum_parts_kernel(const SumArgs a) {
+    constexpr int kWarps = kSumThreads / 32;
+    __shared__ float s_red[kWarps][32];
+    bq::grid_dependency_wait();
+    bq::allow_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    const float* part = a.part + (int64_t)blockIdx.y * a.parts * a.H;
+    float sum = 0.f;
+    if (c < a.H) {
+#pragma unroll 8
+        for (int64_t i = warp; i < a.parts; i += kWarps) sum += part[i * a.H + c];
+    }
+    s_red[warp][lane] = sum;
+    __syncthreads();
+    if (warp || c >= a.H) return;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) sum += s_red[w][lane];
+    if ((int)blockIdx.y == a.sum_gain) {
+        a.dgain[c] = sum;
+        return;
+    }
+    sum *= a.columns.scale;
+    const Gate& gate = a.columns.gate;
+    float f = 1.f, df = 1.f;
+    if (gate.kind == GATE_CHANNEL) {
+        f = load1(gate.p, c, gate.dtype);
+        if (gate.sigmoid) {
+            f = sigmoid_f(f);
+            df = f * (1.f - f);
+        }
+    }
+    if (a.dpost) a.dpost[c] = a.parts ? sum * f : 0.f;
+    if (a.dgate) a.dgate[c] = a.parts ? sum * df * (a.columns.post ? load1(a.columns.post, c, a.columns.gain_dtype) : 1.f) : 0.f;
+}
+
+// ---------------------------------------------------------------- host side
+// How a call's rows are spread: a cluster of CTAs per row, threads per row, rows of a block, rows in flight.
+struct Shape {
+    int cluster, slice, block, threads, rows, stages, stage_bytes, blocks;   // blocks: clusters in the grid
+    size_t smem;
+};
+
+constexpr int kMaxBlocks = 2 * kSms;
+constexpr size_t kSmemOfSm = 224 * 1024;
+
+// planes: of a row's vectors in a stage.
+Shape shape_of(int T, int H, int n_planes) {
+    Shape p{};
+    const int vecs = H / 8;
+    auto constants = [&] { return (size_t)4 * p.block * kVpt * 16; };
+    auto stage = [&] { return (size_t)n_planes * p.block * kVpt * 16; };
+    // a block of 512 threads holds up to 1024 vectors of a row; wider rows, and rows two of which do not fit into
+    // shared memory, are shared by a cluster
+    for (p.cluster = 1;; p.cluster *= 2) {
+        p.slice = (vecs + p.cluster - 1) / p.cluster;
+        p.block = p.slice > 256 * kVpt ? 512 : 256;
+        if (p.slice <= 512 * kVpt && constants() + 2 * stage() <= kSmemOfSm) break;
+    }
+    p.threads = ((p.slice + kVpt - 1) / kVpt + 31) / 32 * 32;
+    p.rows = p.cluster > 1 ? 1 : std::max(1, p.block / p.threads);
+    // two CTAs an SM where two rows of each fit, with a third row where that fits too
+    const int per_sm = p.block == 256 && constants() + 2 * stage() <= kSmemOfSm / 2 ? 2 : 1;
+    p.stages = constants() + 3 * stage() <= kSmemOfSm / per_sm ? 3 : 2;
+    p.stage_bytes = (int)stage();
+    p.smem = constants() + p.stages * stage();   // room for the block's column sums too, 32 bytes per vector
+    // clusters of 1, 2, 4 and 8 CTAs that this GPU holds at once, with one CTA an SM
+    const int held = p.cluster == 1 ? kSms : p.cluster == 2 ? 76 : p.cluster == 4 ? 36 : 15;
+    p.blocks = (int)std::min<int64_t>(held * per_sm, ((int64_t)T + p.rows - 1) / p.rows);
+    return p;
+}
+
+template <auto kernel>
+cudaError_t launch_rows(const Shape& p, const BackwardArgs& a, cudaStream_t st) {
+    // per device: the attribute is a property of the function on the current device
+    static std::atomic<bool> attr_set[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemOfSm);
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(true, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.blocks * p.cluster));
+    cfg.blockDim = dim3(p.threads, p.rows);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int DY, int DH, int DX, bool POST>
+cudaError_t launch_backward(const Shape& p, const BackwardArgs& a, cudaStream_t st) {
+    if (p.block == 256) return launch_rows<residual_norm_backward_kernel<DY, DH, DX, 256, POST, false>>(p, a, st);
+    return launch_rows<residual_norm_backward_kernel<DY, DH, DX, 512, POST, false>>(p, a, st);
+}
+
+template <bool POST>
+cudaError_t launch_cluster(const Shape& p, const BackwardArgs& a, cudaStream_t st) {
+    if (p.block == 256) return launch_rows<residual_norm_backward_kernel<kAny, kAny, kAny, 256, POST, true>>(p, a, st);
+    return launch_rows<residual_norm_backward_kernel<kAny, kAny, kAny, 512, POST, true>>(p, a, st);
+}
+
+}  // namespace
+
+extern "C" size_t bq_residual_norm_backward_workspace_bytes(int32_t T, int32_t H) {
+    if (T < 0 || H < 8 || H % 8 || H > kMaxH) return 0;
+    return (size_t)std::max(1, std::min(T, kMaxBlocks)) * H * 4 * 2;   // a part per block, of two sums
+}
+
+extern "C" bq_status bq_residual_norm_backward(const bq_residual_norm_desc* d, const void* y, int64_t ldy,
+                                               const void* h_out, int64_t ldho, const void* dh_out, int64_t lddho,
+                                               const void* dx, int64_t lddx, void* dy, int64_t lddy, void* dh,
+                                               int64_t lddh, float* dgain, float* dpost_gain, void* dgate,
+                                               int64_t lddgate, void* workspace, size_t workspace_bytes,
+                                               bq_stream_t stream) {
+    const char* name = "bq_residual_norm_backward";
+    bq_status s = check_desc(name, d, dx != nullptr);
+    if (s != BQ_OK) return s;
+    const bool channel = d->gate_kind == BQ_GATE_CHANNEL, full = d->gate_kind == BQ_GATE_FULL;
+    if ((dgain && d->T > 0 && !dx) || (dpost_gain && d->T > 0 && !d->post_gain) || (dgate && d->gate_kind == BQ_GATE_NONE))
+        return bq::fail(BQ_ERR_NULL, "%s: a gradient is asked for without what it belongs to (dgain: dx, dpost_gain: "
+                                     "post_gain, dgate: gate)", name);
+    if (!bq::aligned(dgain, 4) || !bq::aligned(dpost_gain, 4) || (!full && !bq::aligned(dgate, 4)))
+        return bq::fail(BQ_ERR_ALIGN, "%s: sums must be 4-byte aligned", name);
+    const bool sums = dgain || dpost_gain || (dgate && channel);
+    if (d->T == 0 && !sums) return BQ_OK;
+    if (d->T > 0) {
+        const int ys = bq::dtype_size(d->y_dtype), hs = bq::dtype_size(d->h_dtype);
+        if (!dx && !dh_out) return bq::fail(BQ_ERR_NULL, "%s: dx and dh_out are both NULL", name);
+        if ((s = bq::check_rows(name, "y", y, d->H, ldy, ys)) != BQ_OK ||
+            (dx && (s = bq::check_rows(name, "h_out", h_out, d->H, ldho, hs)) != BQ_OK) ||
+            (dh_out && (s = bq::check_rows(name, "dh_out", dh_out, d->H, lddho, hs)) != BQ_OK) ||
+            (dx && (s = bq::check_rows(name, "dx", dx, d->H, lddx, bq::dtype_size(d->x_dtype))) != BQ_OK) ||
+            (s = bq::check_rows(name, "dy", dy, d->H, lddy, ys)) != BQ_OK ||
+            (s = bq::check_rows(name, "dh", dh, d->H, lddh, hs)) != BQ_OK)
+            return s;
+        if (dgate && full &&
+            (s = bq::check_rows(name, "dgate", dgate, d->H, lddgate, bq::dtype_size(d->gate_dtype))) != BQ_OK)
+            return s;
+    }
+    if (sums) {
+        const size_t need = bq_residual_norm_backward_workspace_bytes(d->T, d->H);
+        if (!workspace || workspace_bytes < need)
+            return bq::fail(BQ_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu", name, workspace_bytes, need);
+        if (!bq::aligned(workspace, 16)) return bq::fail(BQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", name);
+    }
+    if ((s = bq::check_arch()) != BQ_OK) return s;
+    float* channel_gate = channel ? static_cast<float*>(dgate) : nullptr;
+    const int i_gain = dgain ? 0 : -1, i_branch = dpost_gain || channel_gate ? i_gain + 1 : -1;
+    const Columns columns = columns_of(d, dx != nullptr);
+    cudaStream_t st = (cudaStream_t)stream;
+    Shape p{};
+    if (d->T > 0) {
+        const int32_t x_dtype = dx ? d->x_dtype : d->h_dtype;
+        BackwardArgs a{};
+        a.T = d->T;
+        a.H = d->H;
+        a.y = rows(y, ldy, d->y_dtype);
+        a.out = rows(dx ? h_out : nullptr, ldho, d->h_dtype);
+        a.dout = rows(dh_out, lddho, d->h_dtype);
+        a.dx = rows(dx, lddx, x_dtype);
+        a.dy = rows(dy, lddy, d->y_dtype);
+        a.dh = rows(dh, lddh, d->h_dtype);
+        a.columns = columns;
+        if (full) a.full = rows(d->gate, d->ldgate, d->gate_dtype);
+        a.dgate = rows(dgate, full ? lddgate : 0, full ? d->gate_dtype : BQ_DT_F32);
+        a.residual_scale = d->residual_scale;
+        a.eps = d->eps;
+        a.part = static_cast<float*>(workspace);
+        a.sum_gain = i_gain;
+        a.sum_branch = i_branch;
+        cudaError_t e = cudaSuccess;
+        auto go = [&](auto type, auto post) {
+            using D = decltype(type);
+            constexpr bool POST = decltype(post)::value;
+            auto shape = [&](int per_vec) { p = shape_of(d->T, d->H, per_vec + (full ? 2 : 0)); };
+            shape(planes(D::y) + 2 * planes(D::h) + planes(D::x));
+            if (p.cluster > 1) shape(2 + 2 * 2 + 2);   // the clusters' kernels leave two planes for every type
+            if (p.rows > 1 && std::max({a.y.ld, a.out.ld, a.dout.ld, a.dx.ld, a.dy.ld, a.dh.ld, a.full.ld, a.dgate.ld}) >
+                                  (int64_t)INT32_MAX / 16) {
+                // offsets inside a block's rows are ints: rows that far apart are taken one at a time
+                p.rows = 1;
+                p.blocks = std::min(d->T, kMaxBlocks);
+            }
+            a.slice = p.slice;
+            a.stages = p.stages;
+            a.stage_bytes = p.stage_bytes;
+            e = p.cluster > 1 ? launch_cluster<POST>(p, a, st) : launch_backward<D::y, D::h, D::x, POST>(p, a, st);
+        };
+        with_types(d->y_dtype, d->h_dtype, x_dtype, [&](auto type) {
+            if (d->post_gain) go(type, std::true_type());
+            else go(type, std::false_type());
+        });
+        if ((s = launched(name, e)) != BQ_OK) return s;
+    }
+    if (!sums) return BQ_OK;
+    const SumArgs sum{static_cast<const float*>(workspace), p.blocks, d->H, dgain, dpost_gain, channel_gate, i_gain, i_branch,
+                      columns};
+    return launched(name, bq::launch_after(sum_parts_kernel, dim3((d->H + 31) / 32, (i_gain >= 0) + (i_branch >= 0)),
+                                           dim3(kSumThreads), 0, st, sum));
+}
