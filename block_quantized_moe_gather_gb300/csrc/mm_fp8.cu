@@ -13,6 +13,7 @@
 #include <atomic>
 
 #include "gemm_internal.cuh"
+#include "packed_f32.cuh"
 #include "row_chunks.cuh"
 #include "row_types.cuh"
 #include "tc_ptx.cuh"
@@ -20,6 +21,12 @@
 namespace {
 
 using namespace bq::tc;
+using bq::both;
+using bq::f32x2;
+using bq::fma2;
+using bq::mul2;
+using bq::parts_of;
+using bq::two;
 
 constexpr int kBlock = 128;        // K per scale, per TMA box (one 128-byte swizzle row) and per TMEM stage
 constexpr int kMaxExperts = 1024;
@@ -154,34 +161,75 @@ __device__ __forceinline__ uint32_t peer_load_u32(uint32_t addr, uint32_t rank) 
 
 __device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.f + expf(-g)); }
 
+// A load that stays where it is written (the compiler would move it to its use, a block later, and wait there).
+__device__ __forceinline__ float load_early(const float* p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
 // ---------------------------------------------------------------- ends
-// Activations other than SwiGLU, in place; the branch is the same for every thread.
+// The activations of the products' ends.  Two special-function instructions each (exp2, reciprocal) bound them, 2.1 us
+// for a tile of 128 x 256; what else they take is kept to less than that.  Both are off by 2 units in the last place at
+// most; results below the normal range become 0.
+__device__ __forceinline__ float exp2_approx(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+constexpr float kLog2E = 1.4426950408889634f;
+
+__device__ __forceinline__ float silu_end(float v) { return v * rcp_approx(1.f + exp2_approx(-kLog2E * v)); }
+
+__device__ __forceinline__ float gelu_tanh_end(float v) {   // (1 + tanh(u)) / 2 is sigmoid(2 u)
+    const float u = __fmaf_rn(0.044715f * v * v, v, v);
+    return v * rcp_approx(1.f + exp2_approx(-kLog2E * 1.5957691216057308f * u));
+}
+
+// Two gelus, v Phi(v).  The normal distribution's tail Phi(-|v|) = erfc(x) / 2, x = |v| / sqrt(2), by the rational
+// approximation 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical Functions: erfc(x) = t (a1 + t (a2 + ...))
+// exp(-x^2), t = 1 / (1 + p x), off by at most 1.5e-7.  v Phi(v) is then off by 0.75e-7 |v|, about a rounding of v.
+// (normcdff took 4 times as long.)
+__device__ __forceinline__ void gelu_end(float& v0, float& v1) {
+    const f32x2 a = two(fabsf(v0), fabsf(v1));
+    const float2 den = parts_of(fma2(a, both(0.3275911f * 0.70710678118654752f), both(1.f)));
+    const f32x2 t = two(rcp_approx(den.x), rcp_approx(den.y));
+    f32x2 q = fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+    q = fma2(t, q, both(0.5f * 1.421413741f));
+    q = fma2(t, q, both(0.5f * -0.284496736f));
+    q = fma2(t, q, both(0.5f * 0.254829592f));
+    const float2 e = parts_of(mul2(mul2(a, both(-0.5f * kLog2E)), a));
+    const f32x2 tail = mul2(mul2(q, t), two(exp2_approx(e.x), exp2_approx(e.y)));
+    const float2 low = parts_of(tail), high = parts_of(fma2(tail, both(-1.f), both(1.f)));
+    v0 *= v0 < 0.f ? low.x : high.x;
+    v1 *= v1 < 0.f ? low.y : high.y;
+}
+
+// Activations other than SwiGLU, in place.  The branch is the same for every thread, and outside the values' loop: the
+// code of one activation lies together.
 template <int N>
 __device__ __forceinline__ void activate(float (&v)[N], int act) {
-    switch (act) {
-        case BQ_ACT_SILU:
+    static_assert(N % 2 == 0, "");
+    auto all = [&](auto f) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = silu_f(v[i]);
-            break;
+        for (int i = 0; i < N; ++i) v[i] = f(v[i]);
+    };
+    switch (act) {
+        case BQ_ACT_SILU: all([](float x) { return silu_end(x); }); break;
         case BQ_ACT_GELU:
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = v[i] * normcdff(v[i]);
+            for (int i = 0; i < N; i += 2) gelu_end(v[i], v[i + 1]);
             break;
-        case BQ_ACT_GELU_TANH:   // (1 + tanh(u)) / 2 is sigmoid(2 u)
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const float u = 1.5957691216057308f * __fmaf_rn(0.044715f * v[i] * v[i], v[i], v[i]);
-                v[i] = __fdividef(v[i], 1.f + expf(-u));
-            }
-            break;
-        case BQ_ACT_RELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
-            break;
-        case BQ_ACT_RELU2:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i] * v[i];
-            break;
+        case BQ_ACT_GELU_TANH: all([](float x) { return gelu_tanh_end(x); }); break;
+        case BQ_ACT_RELU: all([](float x) { return x < 0.f ? 0.f : x; }); break;
+        case BQ_ACT_RELU2: all([](float x) { return x < 0.f ? 0.f : x * x; }); break;
         default: break;
     }
 }
@@ -197,11 +245,13 @@ __device__ __forceinline__ float residual_at(const Args& a, int64_t row, int c) 
     return a.residual ? load_value(a.residual, row * a.ldr + c, a.ydtype) : 0.f;
 }
 
-// One value's end, its residual loaded before (y may be the residual).
-__device__ __forceinline__ float end_of(const Args& a, float v, float residual) {
-    float f[1] = {v};
-    activate(f, a.act);
-    return __fmaf_rn(a.scale, f[0], residual);
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// Lines of a row of the residual, columns [c, c + cols) (bounded), on their way into the L2.
+__device__ __forceinline__ void prefetch_residual(const Args& a, int64_t row, int c, int cols) {
+    const int es = a.ydtype == BQ_DT_F32 ? 4 : 2, end = min(c + cols, a.cols);
+    const uint8_t* p = static_cast<const uint8_t*>(a.residual) + (row * a.ldr + c) * es;
+    for (int i = 0; i < (end - c) * es; i += 128) prefetch_l2(p + i);
 }
 
 // ---------------------------------------------------------------- work items
@@ -367,7 +417,7 @@ template <bool SWIGLU>
 __device__ __forceinline__ float lane_bias(const Args& a, int e, int c) {
     if (!a.bias || c >= a.cols) return 0.f;
     const int up = SWIGLU && (threadIdx.x & 16) ? a.cols : 0;
-    return __ldg(a.bias + (int64_t)e * a.n + up + c);
+    return load_early(a.bias + (int64_t)e * a.n + up + c);
 }
 
 // EPI: with an end (bias, activation, scale, residual).
@@ -425,6 +475,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     const int b0 = a.kb * rank / split, b1 = a.kb * (rank + 1) / split;
     const unsigned long long limit = a.wait_limit_ns;
 
+    float bias = 0.f;   // of the column that an epilogue thread has (an end's)
     const bool one = elect_one();
     bool ok = !(a.skip_copies == 3 && split > 1 ? rank & 1 : a.skip_copies);
     if (warp == 0) {
@@ -507,6 +558,13 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         ok = true;
         for (Items i(first, step, items, w_tiles); ok && i.more(); i.next()) {
             const Item it = i.get(chunks, a.E);
+            const int c = SWIGLU ? 64 * it.tile + 16 * quarter + (lane & 15) : 128 * it.tile + p;
+            if (EPI) {   // on their way while the weights are
+                bias = lane_bias<SWIGLU>(a, it.e, c);
+                const int c0 = SWIGLU ? c - (lane & 15) : c - lane;
+                if (a.residual && lane < it.rows && c0 < a.cols)
+                    prefetch_residual(a, (int64_t)it.row0 + lane, c0, SWIGLU ? 16 : 32);
+            }
             float acc[NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[t] = 0.f;
@@ -539,18 +597,17 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                     if (t < it.rows) red[t * 128 + p] = acc[t];
                 break;         // one item per cluster
             }
-            const int c = SWIGLU ? 64 * it.tile + 16 * quarter + (lane & 15) : 128 * it.tile + p;
             float res[NT];
             if (EPI) {
-                const float b = lane_bias<SWIGLU>(a, it.e, c);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) acc[t] += b;
+                for (int t = 0; t < NT; ++t) acc[t] += bias;
                 // the values that this thread stores: with SwiGLU those of every other row
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const int r = SWIGLU ? t + (lane >> 4) : t;
                     res[t] = (!SWIGLU || t % 2 == 0) && r < it.rows && c < a.cols ? residual_at(a, it.row0 + r, c) : 0.f;
                 }
+                if (!SWIGLU) activate(acc, a.act);
             }
             if (SWIGLU) {
                 // lanes 0-15 hold gate rows, 16-31 their up rows; each half finishes every other row of x
@@ -560,10 +617,8 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                         const float recv = __shfl_xor_sync(0xffffffffu, lane < 16 ? acc[t + 1] : acc[t], 16);
                         const float g = lane < 16 ? acc[t] : recv, u = lane < 16 ? recv : acc[t + 1];
                         const int r = t + (lane >> 4);
-                        const float v = silu_f(g) * u;
-                        if (r < it.rows)
-                            bq::store_value(a.y, (int64_t)(it.row0 + r) * a.ldy + c, a.ydtype,
-                                            EPI ? end_of(a, v, res[t]) : v);
+                        const float v = EPI ? __fmaf_rn(a.scale, silu_end(g) * u, res[t]) : silu_f(g) * u;
+                        if (r < it.rows) bq::store_value(a.y, (int64_t)(it.row0 + r) * a.ldy + c, a.ydtype, v);
                     }
                 }
             } else if (c < a.cols) {
@@ -571,7 +626,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                 for (int t = 0; t < NT; ++t)
                     if (t < it.rows)
                         bq::store_value(a.y, (int64_t)(it.row0 + t) * a.ldy + c, a.ydtype,
-                                        EPI ? end_of(a, acc[t], res[t]) : acc[t]);
+                                        EPI ? __fmaf_rn(a.scale, acc[t], res[t]) : acc[t]);
             }
         }
     }
@@ -587,7 +642,6 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
             const Item it = Items(first, step, items, w_tiles).get(chunks, a.E);
             const int c = SWIGLU ? 64 * it.tile + 16 * quarter + (lane & 15) : 128 * it.tile + p;
             constexpr int kAtOnce = 4;   // rows whose loads are in flight together
-            const float bias = EPI ? lane_bias<SWIGLU>(a, it.e, c) : 0.f;
             for (int t0 = rank; t0 < it.rows; t0 += kAtOnce * split) {
                 float part[kAtOnce][kMaxCluster] = {};
                 float res[kAtOnce];
@@ -607,21 +661,26 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                     }
                 }
                 if (__any_sync(0xffffffffu, aborted != 0)) break;
+                float v[kAtOnce];
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j) {
+                    v[j] = part[j][0];
+#pragma unroll
+                    for (int r = 1; r < kMaxCluster; ++r) v[j] += part[j][r];
+                    if (EPI) v[j] += bias;
+                    if (SWIGLU) {
+                        const float u = __shfl_xor_sync(0xffffffffu, v[j], 16);
+                        v[j] = (EPI ? silu_end(v[j]) : silu_f(v[j])) * u;
+                    }
+                }
+                if (EPI && !SWIGLU) activate(v, a.act);
 #pragma unroll
                 for (int j = 0; j < kAtOnce; ++j) {
                     const int t = t0 + j * split;
                     if (t >= it.rows) break;
-                    float v = part[j][0];
-#pragma unroll
-                    for (int r = 1; r < kMaxCluster; ++r) v += part[j][r];
-                    if (EPI) v += bias;
-                    if (SWIGLU) {
-                        const float u = __shfl_xor_sync(0xffffffffu, v, 16);
-                        v = silu_f(v) * u;
-                    }
-                    if (EPI) v = end_of(a, v, res[j]);
+                    if (EPI) v[j] = __fmaf_rn(a.scale, v[j], res[j]);
                     if (c < a.cols && (!SWIGLU || lane < 16))
-                        bq::store_value(a.y, (int64_t)(it.row0 + t) * a.ldy + c, a.ydtype, v);
+                        bq::store_value(a.y, (int64_t)(it.row0 + t) * a.ldy + c, a.ydtype, v[j]);
                 }
             }
         }
@@ -700,13 +759,6 @@ struct WideSmem {
 };
 static_assert(WideSmem::kBytes <= 232448 && WideSmem::kBars % 16 == 0 && WideSmem::S % 2 == 0, "smem");
 
-// A load that stays where it is written (the compiler would move it to its use, a block later, and wait there).
-__device__ __forceinline__ float load_early(const float* p) {
-    float v;
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
-    return v;
-}
-
 __device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&v)[32], float f) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) acc[i] = __fmaf_rn(__uint_as_float(v[i]), f, acc[i]);
@@ -765,29 +817,99 @@ __device__ __forceinline__ void store_rows(const Args& a, uint8_t* buf, const ui
     }
 }
 
-// Eight values of a row of the residual from column c on, as fp32; 0 where there is none (rows or columns behind the
-// last).  vectors: the matrix allows 16-byte loads.
-__device__ __forceinline__ void residual8(const Args& a, int64_t row, bool live, int c, bool vectors, float (&r)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = 0.f;
-    if (!a.residual || !live) return;
+__device__ __forceinline__ void load32(const void* p, uint4& lo, uint4& hi) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(lo.x), "=r"(lo.y), "=r"(lo.z), "=r"(lo.w), "=r"(hi.x), "=r"(hi.y), "=r"(hi.z), "=r"(hi.w)
+                 : "l"(p) : "memory");
+}
+
+// 128 bytes of a row of the residual from column c on (32 fp32 values, or 64), added to v: those columns that exist.
+// vectors: the matrix allows
+// 32-byte loads (whole sectors), which then are in flight together.
+template <int N>
+__device__ __forceinline__ void add_residual(const Args& a, int64_t row, int c, bool vectors, float* v) {
     const int64_t at = row * a.ldr + c;
-    if (vectors && c + 8 <= a.cols) {
-        if (a.ydtype == BQ_DT_F32) {
-            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + at);
-            const float4 lo = p[0], hi = p[1];
-            r[0] = lo.x; r[1] = lo.y; r[2] = lo.z; r[3] = lo.w;
-            r[4] = hi.x; r[5] = hi.y; r[6] = hi.z; r[7] = hi.w;
-        } else {
-            const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + at);
-            if (a.ydtype == BQ_DT_F16) bq::RowVec<BQ_DT_F16>::unpack(v, r);
-            else bq::RowVec<BQ_DT_BF16>::unpack(v, r);
+    const uint8_t* p = static_cast<const uint8_t*>(a.residual) + at * (N == 32 ? 4 : 2);
+    if (vectors && c + N <= a.cols) {
+        uint4 raw[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) load32(p + 16 * i, raw[i], raw[i + 1]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (N == 32) {
+                float f[4];
+                bq::RowVec<BQ_DT_F32>::unpack(raw[i], f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[4 * i + j] = __fmaf_rn(a.scale, v[4 * i + j], f[j]);
+            } else {
+                float f[8];
+                if (a.ydtype == BQ_DT_F16) bq::RowVec<BQ_DT_F16>::unpack(raw[i], f);
+                else bq::RowVec<BQ_DT_BF16>::unpack(raw[i], f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[(8 * i + j) % N] = __fmaf_rn(a.scale, v[(8 * i + j) % N], f[j]);
+            }
         }
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c + i < a.cols) r[i] = load_value(a.residual, at + i, a.ydtype);
+    for (int i = 0; i < N; ++i)
+        if (c + i < a.cols) v[i] = __fmaf_rn(a.scale, v[i], load_value(a.residual, at + i, a.ydtype));
+}
+
+// Bias of the values that a thread sums: acc[j] is column c0 + j of y, with SwiGLU the gate value of column c0 + j % 64
+// or its up value.  Each warp fetches its own copy to where its rows go through later: copies that nothing waits for
+// until the sums are done, and that need no registers meanwhile (a load into registers at this place made a block of K
+// 8% longer).
+template <bool SWIGLU>
+__device__ __forceinline__ void fetch_bias(const Args& a, int e, int c0, uint8_t* buf) {
+    if (!a.bias) return;
+    const float* bias = a.bias + (int64_t)e * a.n;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = 32 * i + (threadIdx.x & 31), c = min(c0 + (SWIGLU ? j & 63 : j), a.cols - 1);
+        copy4_async(smem_u32(buf) + 4 * j, bias + (SWIGLU && i >= 2 ? a.cols : 0) + c);
+    }
+}
+
+// A row's end, in place: column c0 + n of y in acc[n].
+template <bool SWIGLU>
+__device__ __forceinline__ void end_rows(const Args& a, float (&acc)[128], const uint8_t* buf, int64_t row, bool live, int c0,
+                                         bool vectors) {
+    constexpr int kCols = SWIGLU ? 64 : 128;
+    if (a.bias) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        const float4* b4 = reinterpret_cast<const float4*>(buf);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float4 b = b4[j];
+            acc[4 * j] += b.x;
+            acc[4 * j + 1] += b.y;
+            acc[4 * j + 2] += b.z;
+            acc[4 * j + 3] += b.w;
+        }
+        __syncwarp();   // the rows go through buf next
+    }
+    if (SWIGLU) {
+#pragma unroll
+        for (int n = 0; n < 64; ++n) acc[n] = silu_end(acc[n]) * acc[64 + n];
+    } else {
+        activate(acc, a.act);
+    }
+    if (!a.residual) {
+        if (a.scale != 1.f) {
+#pragma unroll
+            for (int n = 0; n < kCols; ++n) acc[n] *= a.scale;
+        }
+    } else if (live) {
+        if (a.ydtype == BQ_DT_F32) {
+#pragma unroll
+            for (int n = 0; n < kCols; n += 32) add_residual<32>(a, row, c0 + n, vectors, acc + n);
+        } else {
+#pragma unroll
+            for (int n = 0; n < kCols; n += 64) add_residual<64>(a, row, c0 + n, vectors, acc + n);
+        }
+    }
 }
 
 // EPI: with an end (bias, activation, scale, residual).
@@ -912,7 +1034,7 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         const int es = a.ydtype == BQ_DT_F32 ? 4 : 2;
         const uintptr_t y_align = reinterpret_cast<uintptr_t>(a.y) | (uintptr_t)(a.ldy * es);
         const bool aligned = y_align % 16 == 0, sectors = y_align % 32 == 0;
-        const bool vectors = (reinterpret_cast<uintptr_t>(a.residual) | (uintptr_t)(a.ldr * es)) % 16 == 0;
+        const bool vectors = (reinterpret_cast<uintptr_t>(a.residual) | (uintptr_t)(a.ldr * es)) % 32 == 0;
         // The slot in turn: its barriers (the second's 8 bytes behind the first's) and its columns, flipped by a bit.
         uint32_t bar_full = acc_full(half, 0), t = tmem + ((uint32_t)(32 * quarter) << 16) + half * A * 128, aph = 0;
         uint32_t bar_free = acc_empty(half, 0);
@@ -925,6 +1047,11 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             // this half's first column and the scale row of its columns, with SwiGLU of its gate columns and up columns
             const int c0 = kTileCols * it.tile + kTileCols / 2 * half;
             const int o_lo = min(c0 / kBlock, a.nb - 1) * a.kb, o_hi = o_lo + a.nb / 2 * a.kb;
+            uint8_t* buf = smem + M::kOut + (warp - 4) * 16 * kOutRow;
+            if (EPI) {   // on their way while the blocks are
+                fetch_bias<SWIGLU>(a, it.e, c0, buf);
+                if (a.residual && p < it.rows) prefetch_residual(a, (int64_t)it.row0 + p, c0, SWIGLU ? 64 : 128);
+            }
             float acc[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j) acc[j] = 0.f;
@@ -973,31 +1100,8 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             if (!ok) break;
             const int rows = it.rows - 32 * quarter;   // of this warp
             if (rows > 0) {
-                uint8_t* buf = smem + M::kOut + (warp - 4) * 16 * kOutRow;
                 const int64_t row0 = it.row0 + 32 * quarter;
-                if (EPI) {   // in place, where the plain product's values lie: column c0 + n of y in acc[n]
-                    const float* bias = a.bias ? a.bias + (int64_t)it.e * a.n : nullptr;
-                    constexpr int kCols = SWIGLU ? 64 : 128;
-#pragma unroll
-                    for (int n = 0; n < kCols; n += 8) {
-                        float f[8], r[8];
-                        residual8(a, row0 + lane, lane < rows, c0 + n, vectors, r);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int c = min(c0 + n + i, a.cols - 1);
-                            f[i] = acc[n + i];
-                            if (bias) f[i] += __ldg(bias + c);
-                            if (SWIGLU) {
-                                float u = acc[(64 + n + i) & 127];
-                                if (bias) u += __ldg(bias + a.cols + c);
-                                f[i] = silu_f(f[i]) * u;
-                            }
-                        }
-                        activate(f, a.act);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) acc[n + i] = __fmaf_rn(a.scale, f[i], r[i]);
-                    }
-                }
+                if (EPI) end_rows<SWIGLU>(a, acc, buf, row0 + lane, lane < rows, c0, vectors);
                 auto out = [&](int n) { return SWIGLU && !EPI ? silu_f(acc[n]) * acc[(64 + n) & 127] : acc[n]; };
                 auto out8 = [&](int n) {
                     const float f[8] = {out(n), out(n + 1), out(n + 2), out(n + 3), out(n + 4), out(n + 5), out(n + 6), out(n + 7)};

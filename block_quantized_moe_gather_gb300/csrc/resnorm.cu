@@ -13,6 +13,7 @@
 
 namespace {
 
+using namespace bq;
 using namespace bq::resnorm;
 
 struct ForwardArgs {

@@ -13,6 +13,7 @@
 
 namespace {
 
+using namespace bq;
 using namespace bq::resnorm;
 
 constexpr int kVpt = 2;   // vectors of a thread

@@ -4,9 +4,9 @@ Tolerance (u = 2^-24): the product v as in the plain products' tests,
 (259 + kb) u S, and u |v| for the bias.  An activation passes an error on by at
 most its largest slope (silu 1.1, gelu and its tanh form 1.13, relu 1, relu2
 2 |v|) and adds its own: silu (16 + |v|) u |y| (the exponent's argument, exp, the
-division), gelu 16 u |y| (normcdff is off by 5 units in the last place, 10 u),
-its tanh form (16 + 8 |w|) u |y| with w the exponent's argument; then two
-roundings, 2 u (|scale y| + |residual|), and the output's half step."""
+reciprocal), gelu 2 u |v| (an approximation of Phi off by 0.75e-7 = 1.3 u at
+most) + 16 u |y|, its tanh form (16 + 8 |w|) u |y| with w the exponent's argument;
+then two roundings, 2 u (|scale y| + |residual|), and the output's half step."""
 import numpy as np
 import pytest
 
@@ -31,7 +31,8 @@ def expected(x, xs, w, ws, out, act, bias, scale, residual):
     elif act == "relu2":
         err = 2 * np.abs(v) * err + err * err + 2 * U * np.abs(y)
     else:
-        own = {"silu": 16 + np.abs(v), "gelu": 16.0, "gelu_tanh": 16 + 8 * np.abs(1.6 * (v + 0.045 * v ** 3)), "relu": 0.0,
+        own = {"silu": 16 + np.abs(v), "gelu": 16.0 + 2 * np.abs(v) / np.maximum(np.abs(y), 1e-30),
+               "gelu_tanh": 16 + 8 * np.abs(1.6 * (v + 0.045 * v ** 3)), "relu": 0.0,
                "none": 0.0}[act]
         err = SLOPE[act] * err + own * U * np.abs(y)
     y, err = scale * y, abs(scale) * err + 2 * U * abs(scale) * np.abs(y)
