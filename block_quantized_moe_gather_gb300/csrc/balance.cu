@@ -13,20 +13,24 @@
 //                    s' = sigmoid(z) / (2 s)
 #include <algorithm>
 
+#include "packed_f32.cuh"
 #include "row_types.cuh"
 
 namespace {
 
+using namespace bq;
+
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSequences = 65536;
+constexpr float kLog2E = 1.4426950408889634f;
 
 enum { RULE_SOFTMAX = 0, RULE_SCORE = 1 };
 
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int off = 16; off; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-    return v;
+    // as ordered integers, one instruction; a NaN that is lost here is met again in the sum of exponentials
+    const int i = __float_as_int(v), m = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7fffffff));
+    return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -35,34 +39,124 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// sqrt(softplus(z)); below -20 softplus is exp(z) to 1e-9, and its root exp(z / 2) stays normal where exp(z) does not.
-__device__ __forceinline__ float score_of(float z) {
-    return z < -20.f ? expf(0.5f * z) : sqrtf(fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))));
+// exp2, reciprocal and square root of the special-function unit: off by 2 units in the last place at most, results and
+// arguments below the normal range become 0.  exp(v) = exp2(v log2 e) is off by |v| units more, from the argument.
+__device__ __forceinline__ float exp2_approx(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
 
-// Its derivative, sigmoid(z) / (2 score).
-__device__ __forceinline__ float score_slope(float z, float score) {
-    return z < -20.f ? 0.5f * score : 0.5f / ((1.f + expf(-z)) * score);
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
 
-// A row of logits in a warp: lane l holds experts l + 32 i (z; -inf behind the last).
-template <int NPER>
-__device__ __forceinline__ void load_row(const float* row, const float* bias, int E, int lane, float (&z)[NPER]) {
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) {
-        const int e = lane + 32 * i;
-        z[i] = e < E ? __ldg(row + e) : -INFINITY;
+__device__ __forceinline__ float sqrt_approx(float v) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float log_approx(float v) {   // off by 2^-22 and 2 units in the last place
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r * 0.69314718055994531f;
+}
+
+// log(1 + e) / e for e in [0, 1]: a polynomial fitted to it (largest relative error 5e-9, 1.2e-7 evaluated in fp32).
+__device__ __forceinline__ f32x2 log1p_ratio(f32x2 e) {
+    f32x2 q = fma2(e, both(-0.003243980884f), both(0.01985126273f));
+    q = fma2(q, e, both(-0.05695915927f));
+    q = fma2(q, e, both(0.1060361689f));
+    q = fma2(q, e, both(-0.1530557013f));
+    q = fma2(q, e, both(0.1967593147f));
+    q = fma2(q, e, both(-0.2495413214f));
+    q = fma2(q, e, both(0.3332996227f));
+    q = fma2(q, e, both(-0.4999990242f));
+    return fma2(q, e, both(0.9999999953f));
+}
+
+// sqrt(softplus(z)) of two logits.  With h = exp(-|z| / 2) and e = h^2, softplus is max(z, 0) + log(1 + e); below 0 its
+// root is h sqrt(log(1 + e) / e), which loses nothing where e does (h is normal down to z = -174).  slope: with the
+// derivative sigmoid(z) / (2 score) too.
+template <bool SLOPE>
+__device__ __forceinline__ void scores_of(float z0, float z1, float& s0, float& s1, float& d0, float& d1) {
+    const float2 a = parts_of(mul2(two(fabsf(z0), fabsf(z1)), both(-0.5f * kLog2E)));
+    const f32x2 h = two(exp2_approx(a.x), exp2_approx(a.y)), e = mul2(h, h), ratio = log1p_ratio(e);
+    const float2 hs = parts_of(h), low = parts_of(ratio), soft = parts_of(fma2(e, ratio, two(fmaxf(z0, 0.f), fmaxf(z1, 0.f))));
+    const float r0 = sqrt_approx(z0 < 0.f ? low.x : soft.x), r1 = sqrt_approx(z1 < 0.f ? low.y : soft.y);
+    s0 = z0 < 0.f ? hs.x * r0 : r0;
+    s1 = z1 < 0.f ? hs.y * r1 : r1;
+    if (SLOPE) {   // sigmoid(z) is 1 / (1 + e) from 0 on and e / (1 + e) below
+        const float2 den = parts_of(mul2(fma2(e, both(2.f), both(2.f)), two(r0, r1)));
+        d0 = (z0 < 0.f ? hs.x : 1.f) * rcp_approx(den.x);
+        d1 = (z1 < 0.f ? hs.y : 1.f) * rcp_approx(den.y);
     }
-    if (bias) {
-#pragma unroll
-        for (int i = 0; i < NPER; ++i)
-            if (lane + 32 * i < E) z[i] = __fadd_rn(z[i], __ldg(bias + lane + 32 * i));
-    }
 }
 
-// Softmax and log-sum-exp of a row.  A row of -inf only has probabilities 0 and a log-sum-exp counted as 0.
+// A warp's share of a row: lane l holds experts at(l, i), i < NPER: four in a row at a time where rows lie on 16-byte
+// boundaries (VEC), else 32 apart.  Values behind the last expert are -inf.
+template <int NPER, bool VEC>
+struct Share {
+    static __device__ __forceinline__ int at(int lane, int i) { return VEC ? 128 * (i >> 2) + 4 * lane + (i & 3) : lane + 32 * i; }
+
+    static __device__ __forceinline__ void load(const float* row, const float* bias, int E, int lane, float (&z)[NPER]) {
+        if (VEC) {
+#pragma unroll
+            for (int i = 0; i < NPER; i += 4) {
+                const bool in = at(lane, i) < E;
+                const float4 v = in ? __ldg(reinterpret_cast<const float4*>(row + at(lane, i)))
+                                    : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                z[i] = v.x; z[(i + 1) % NPER] = v.y; z[(i + 2) % NPER] = v.z; z[(i + 3) % NPER] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NPER; ++i) z[i] = at(lane, i) < E ? __ldg(row + at(lane, i)) : -INFINITY;
+        }
+        if (bias) {
+#pragma unroll
+            for (int i = 0; i < NPER; ++i)
+                if (at(lane, i) < E) z[i] = __fadd_rn(z[i], __ldg(bias + at(lane, i)));
+        }
+    }
+
+    static __device__ __forceinline__ void store(void* matrix, int64_t row, int dtype, int E, int lane, const float (&v)[NPER]) {
+        if (VEC) {
+#pragma unroll
+            for (int i = 0; i < NPER; i += 4) {
+                if (at(lane, i) >= E) continue;
+                const int64_t to = row * E + at(lane, i);
+                const float f[4] = {v[i], v[(i + 1) % NPER], v[(i + 2) % NPER], v[(i + 3) % NPER]};
+                if (dtype == BQ_DT_F32) {
+                    *reinterpret_cast<float4*>(static_cast<float*>(matrix) + to) = make_float4(f[0], f[1], f[2], f[3]);
+                } else if (dtype == BQ_DT_F16) {
+                    *reinterpret_cast<uint2*>(static_cast<__half*>(matrix) + to) =
+                        make_uint2(h2_as_u32(__floats2half2_rn(f[0], f[1])), h2_as_u32(__floats2half2_rn(f[2], f[3])));
+                } else {
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(matrix) + to) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NPER; ++i)
+                if (at(lane, i) < E) store_value(matrix, row * E + at(lane, i), dtype, v[i]);
+        }
+    }
+};
+
+// What the softmax of a row is made of: its largest logit m (0 for a row of -inf only), 1 / the sum of exp(z - m) and
+// the log-sum-exp (both 0 for such a row).
+struct Softmax {
+    float m, inv, lse;
+};
+
+// ex: the exponentials.
 template <int NPER>
-__device__ __forceinline__ void softmax_row(const float (&z)[NPER], float (&p)[NPER], float& lse) {
+__device__ __forceinline__ Softmax softmax_row(const float (&z)[NPER], float (&ex)[NPER]) {
     float m = z[0];
 #pragma unroll
     for (int i = 1; i < NPER; ++i) m = fmaxf(m, z[i]);
@@ -71,27 +165,30 @@ __device__ __forceinline__ void softmax_row(const float (&z)[NPER], float (&p)[N
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NPER; ++i) {
-        p[i] = expf(z[i] - m);
-        sum += p[i];
+        ex[i] = exp2_approx((z[i] - m) * kLog2E);
+        sum += ex[i];
     }
     sum = warp_sum(sum);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    lse = sum == 0.f ? 0.f : m + logf(sum);
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) p[i] *= inv;
+    return {m, sum == 0.f ? 0.f : rcp_approx(sum), sum == 0.f ? 0.f : m + log_approx(sum)};
 }
 
-// Scores over their sum, and 1 / the sum (0 where every score is).
-template <int NPER>
-__device__ __forceinline__ void score_row(const float (&z)[NPER], int E, int lane, float (&s)[NPER], float& inv) {
+// Scores (and slopes) of a row, and 1 / their sum (0 where every score is 0).
+template <bool SLOPE, int NPER>
+__device__ __forceinline__ float score_row(const float (&z)[NPER], float (&s)[NPER], float (&d)[NPER]) {
     float sum = 0.f;
+    if (NPER == 1) {
+        float unused0, unused1;
+        scores_of<SLOPE>(z[0], 0.f, s[0], unused0, d[0], unused1);
+        sum = s[0];
+    } else {
 #pragma unroll
-    for (int i = 0; i < NPER; ++i) {
-        s[i] = lane + 32 * i < E ? score_of(z[i]) : 0.f;
-        sum += s[i];
+        for (int i = 0; i < NPER; i += 2) {
+            scores_of<SLOPE>(z[i], z[(i + 1) % NPER], s[i], s[(i + 1) % NPER], d[i], d[(i + 1) % NPER]);
+            sum += s[i] + s[(i + 1) % NPER];
+        }
     }
-    sum = warp_sum(sum);
-    inv = sum == 0.f ? 0.f : 1.f / sum;
+    sum = warp_sum(sum);   // what lies behind the last expert has z = -inf and adds 0
+    return sum == 0.f ? 0.f : rcp_approx(sum);
 }
 
 // ---------------------------------------------------------------- sequences
@@ -105,29 +202,30 @@ __device__ __forceinline__ bool sequence(const int32_t* offsets, int s, int T, i
     return false;
 }
 
-// Sequences that have rows, and their rows (all threads; contains barriers).
-__device__ __forceinline__ void sequence_totals(const int32_t* offsets, int S, int T, int32_t* status, int* s_totals) {
-    if (threadIdx.x < 2) s_totals[threadIdx.x] = 0;
+struct Totals {
+    int used, rows;   // sequences that have rows, and their rows
+    int before;       // sequences that end at `row` or before it: the first that does not
+};
+
+// All threads of the CTA; contains barriers.
+__device__ __forceinline__ Totals sequence_totals(const int32_t* offsets, int S, int T, int row, int32_t* status) {
+    __shared__ int s_totals[3];
+    if (!offsets) return {T > 0, T, 0};
+    if (threadIdx.x < 3) s_totals[threadIdx.x] = 0;
     __syncthreads();
-    int used = 0, rows = 0;
+    int used = 0, rows = 0, before = 0;
     for (int s = threadIdx.x; s < S; s += blockDim.x) {
         int lo, hi;
+        before += __ldg(offsets + s + 1) <= row;
         if (sequence(offsets, s, T, status, lo, hi) && hi > lo) { ++used; rows += hi - lo; }
     }
-    if (used) {
+    if (used | before) {
         atomicAdd(&s_totals[0], used);
         atomicAdd(&s_totals[1], rows);
+        atomicAdd(&s_totals[2], before);
     }
     __syncthreads();
-}
-
-// First sequence that ends behind `row` (all threads of the CTA; contains barriers).
-__device__ __forceinline__ int first_sequence(const int32_t* offsets, int S, int row) {
-    int n = 0;
-    if (offsets)
-        for (int s = threadIdx.x; s - (int)threadIdx.x < S; s += blockDim.x)
-            n += __syncthreads_count(s < S && __ldg(offsets + s + 1) <= row);
-    return n;
+    return {s_totals[0], s_totals[1], s_totals[2]};
 }
 
 // ---------------------------------------------------------------- counts, mean probabilities, losses
@@ -142,6 +240,8 @@ struct BalanceArgs {
     float* part_p;       // [chunks + S][E]
     int32_t* part_c;     // [chunks + S][E]
     float* part_z;       // [chunks + S]
+    float* part_loss;    // [S * groups of 32 experts][2]
+    int* ended;          // CTAs of balance_finish_kernel that have ended
     int32_t* counts;
     float* probs;
     float* losses;
@@ -151,12 +251,14 @@ struct BalanceArgs {
 // The rows are cut into chunks of equal size, a CTA each, whatever sequences they belong to: one long sequence among
 // short ones takes no longer than many of equal length.  Chunk c leaves its sums over sequence s in slot c + s: along
 // rows that ascend, either c or s grows from one (chunk, sequence) to the next, so no two share a slot.
-template <int NPER, int RULE>
+template <int NPER, bool VEC, int RULE>
 __device__ __forceinline__ void chunk_sums(const BalanceArgs& a, float* s_red, int32_t* s_hist) {
+    using Row = Share<NPER, VEC>;
+    constexpr bool kAhead = NPER <= 8;   // the next row is loaded ahead, where there are registers for it
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t first = (int64_t)blockIdx.x * a.chunk_rows;
     const int row0 = (int)first, row1 = (int)min((int64_t)a.T, first + a.chunk_rows);
-    for (int s = first_sequence(a.offsets, a.S, row0); s < a.S; ++s) {
+    for (int s = sequence_totals(a.offsets, a.S, a.T, row0, a.status).before; s < a.S; ++s) {
         int lo, hi;
         sequence(a.offsets, s, a.T, a.status, lo, hi);
         if (lo >= row1) break;
@@ -164,27 +266,33 @@ __device__ __forceinline__ void chunk_sums(const BalanceArgs& a, float* s_red, i
         hi = min(hi, row1);
         if (lo >= hi) continue;
         for (int e = threadIdx.x; e < a.E; e += kThreads) s_hist[e] = 0;
+        float z[NPER], acc[NPER], z2 = 0.f;
+        if (kAhead && lo + warp < hi) Row::load(a.logits + (int64_t)(lo + warp) * a.E, a.bias, a.E, lane, z);
         __syncthreads();
         for (int64_t i = (int64_t)lo * a.k + threadIdx.x; i < (int64_t)hi * a.k; i += kThreads) {
             const int e = __ldg(a.ids + i);
             if (e >= 0 && e < a.E) atomicAdd(&s_hist[e], 1);
             else bq::set_device_error(a.status, BQ_DEV_BAD_EXPERT_ID);
         }
-        float acc[NPER], z2 = 0.f;
 #pragma unroll
         for (int i = 0; i < NPER; ++i) acc[i] = 0.f;
         for (int r = lo + warp; r < hi; r += kWarps) {
-            float z[NPER], p[NPER], lse, inv = 1.f;
-            load_row(a.logits + (int64_t)r * a.E, a.bias, a.E, lane, z);
-            softmax_row(z, p, lse);
-            if (RULE == RULE_SCORE) score_row(z, a.E, lane, p, inv);
+            float next[NPER], p[NPER], unused[NPER];
+            if (!kAhead) Row::load(a.logits + (int64_t)r * a.E, a.bias, a.E, lane, z);
+            else if (r + kWarps < hi) Row::load(a.logits + (int64_t)(r + kWarps) * a.E, a.bias, a.E, lane, next);
+            const Softmax soft = softmax_row(z, p);
+            float inv = soft.inv;
+            if (RULE == RULE_SCORE) inv = score_row<false>(z, p, unused);
 #pragma unroll
-            for (int i = 0; i < NPER; ++i) acc[i] = __fmaf_rn(p[i], inv, acc[i]);
-            z2 = __fmaf_rn(lse, lse, z2);
+            for (int i = 0; i < NPER; ++i) {
+                acc[i] = __fmaf_rn(p[i], inv, acc[i]);
+                if (kAhead) z[i] = next[i];
+            }
+            z2 = __fmaf_rn(soft.lse, soft.lse, z2);
         }
 #pragma unroll
         for (int i = 0; i < NPER; ++i)
-            if (lane + 32 * i < a.E) s_red[warp * a.E + lane + 32 * i] = acc[i];
+            if (Row::at(lane, i) < a.E) s_red[warp * a.E + Row::at(lane, i)] = acc[i];
         if (lane == 0) s_red[kWarps * a.E + warp] = z2;
         __syncthreads();
         const int64_t slot = (int64_t)blockIdx.x + s;
@@ -215,14 +323,62 @@ __device__ __forceinline__ float peer_load(const float* p, int rank) {
     return v;
 }
 
-// The slots of every sequence added up, by the CTAs of one cluster.  A group is 32 experts of a sequence; `share` warps
-// (a power of two) take a share of its slots each.
+// One warp's share of the slots of a group, 32 experts of a sequence (rows [lo, hi)): slots sub, sub + share, ...
+struct GroupSums {
+    float p;
+    int c;
+    float z2;    // per lane, of the first group of a sequence
+};
+
+__device__ __forceinline__ GroupSums add_slots(const BalanceArgs& a, int s, int block, int lo, int hi, int sub, int share) {
+    const int lane = threadIdx.x & 31, e = block * 32 + lane;
+    GroupSums r{0.f, 0, 0.f};
+    if (hi <= lo) return r;
+    const int64_t begin = lo / a.chunk_rows + (int64_t)s, end = (hi - 1) / a.chunk_rows + (int64_t)s + 1;
+    if (e < a.E) {
+        const float* from_p = a.part_p + e;
+        const int32_t* from_c = a.part_c + e;
+        int64_t i = begin + sub;
+        for (; i + 7 * share < end; i += 8 * share) {   // eight slots in flight together
+            float p[8];
+            int c[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                p[j] = from_p[(i + j * share) * a.E];
+                c[j] = from_c[(i + j * share) * a.E];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                r.p += p[j];
+                r.c += c[j];
+            }
+        }
+#pragma unroll 4
+        for (; i < end; i += share) {
+            r.p += from_p[i * a.E];
+            r.c += from_c[i * a.E];
+        }
+    }
+    if (block == 0)
+        for (int64_t i = begin + 32 * sub + lane; i < end; i += 32 * share) r.z2 += a.part_z[i];
+    return r;
+}
+
+// Counts and mean probability of an expert; its share of the balance loss.
+__device__ __forceinline__ float write_group(const BalanceArgs& a, int s, int e, int lo, int hi, float p, int c) {
+    const float n = (float)(hi - lo), mean = hi > lo ? p / n : 0.f;
+    a.counts[(int64_t)s * a.E + e] = c;
+    a.probs[(int64_t)s * a.E + e] = mean;
+    return hi > lo ? (float)c * ((float)a.E / ((float)a.k * n)) * mean : 0.f;
+}
+
+// The slots of every sequence added up, by the CTAs of one cluster; `share` warps (a power of two) have a share of a
+// group's slots each.  s_red, s_redc: a word per thread.
 __device__ __forceinline__ void finish(const BalanceArgs& a, int rank, int ranks, int share, float* s_red, int32_t* s_redc) {
-    __shared__ int s_totals[2];
     __shared__ float s_loss[2][kWarps];
     __shared__ float s_cta[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    sequence_totals(a.offsets, a.S, a.T, a.status, s_totals);
+    const Totals totals = sequence_totals(a.offsets, a.S, a.T, 0, a.status);
     const int blocks = (a.E + 31) / 32, sub = warp & (share - 1), at_once = kWarps / share;
     const int64_t groups = (int64_t)a.S * blocks;
     float balance = 0.f, z2 = 0.f;
@@ -231,38 +387,21 @@ __device__ __forceinline__ void finish(const BalanceArgs& a, int rank, int ranks
         const int s = (int)(g / blocks), block = (int)(g - (int64_t)s * blocks), e = block * 32 + lane;
         int lo = 0, hi = 0;
         if (g < groups) sequence(a.offsets, s, a.T, a.status, lo, hi);
-        float p = 0.f;
-        int c = 0;
-        if (hi > lo) {
-            const int64_t begin = lo / a.chunk_rows + (int64_t)s, end = (hi - 1) / a.chunk_rows + (int64_t)s + 1;
-            if (e < a.E) {
-#pragma unroll 8
-                for (int64_t i = begin + sub; i < end; i += share) {
-                    p += a.part_p[i * a.E + e];
-                    c += a.part_c[i * a.E + e];
-                }
-            }
-            if (block == 0)
-                for (int64_t i = begin + 32 * sub + lane; i < end; i += 32 * share) z2 += a.part_z[i];
-        }
+        GroupSums r = add_slots(a, s, block, lo, hi, sub, share);
+        z2 += r.z2;
         if (share > 1) {
-            s_red[threadIdx.x] = p;
-            s_redc[threadIdx.x] = c;
+            s_red[threadIdx.x] = r.p;
+            s_redc[threadIdx.x] = r.c;
             __syncthreads();
             if (sub == 0) {
                 for (int w = 1; w < share; ++w) {
-                    p += s_red[threadIdx.x + 32 * w];
-                    c += s_redc[threadIdx.x + 32 * w];
+                    r.p += s_red[threadIdx.x + 32 * w];
+                    r.c += s_redc[threadIdx.x + 32 * w];
                 }
             }
             __syncthreads();
         }
-        if (sub == 0 && g < groups && e < a.E) {
-            const float n = (float)(hi - lo), mean = hi > lo ? p / n : 0.f;
-            a.counts[(int64_t)s * a.E + e] = c;
-            a.probs[(int64_t)s * a.E + e] = mean;
-            if (hi > lo) balance += (float)c * ((float)a.E / ((float)a.k * n)) * mean;
-        }
+        if (sub == 0 && g < groups && e < a.E) balance += write_group(a, s, e, lo, hi, r.p, r.c);
     }
     balance = warp_sum(balance);
     z2 = warp_sum(z2);
@@ -278,7 +417,7 @@ __device__ __forceinline__ void finish(const BalanceArgs& a, int rank, int ranks
     if (rank == 0 && threadIdx.x < 2) {
         float v = 0.f;
         for (int r = 0; r < ranks; ++r) v += ranks > 1 ? peer_load(&s_cta[threadIdx.x], r) : s_cta[threadIdx.x];
-        const int n = s_totals[threadIdx.x];
+        const int n = threadIdx.x ? totals.rows : totals.used;
         a.losses[threadIdx.x] = n ? v / (float)n : 0.f;
     }
     if (ranks > 1) cluster_sync();   // rank 0 may still be reading
@@ -295,16 +434,17 @@ __device__ __forceinline__ int cluster_rank() {
 __host__ __device__ inline int sums_words(int E) { return kWarps * E + kWarps > kThreads ? kWarps * E + kWarps : kThreads; }
 inline size_t balance_smem(int E) { return ((size_t)sums_words(E) + std::max(E, kThreads)) * 4; }
 
-// ONE: the launch is one cluster, which also adds its slots up.
-template <int NPER, int RULE, bool ONE>
-__global__ void __launch_bounds__(kThreads)
-balance_kernel(const BalanceArgs a, int share) {
+// one: the launch is one cluster, which also adds its slots up.
+template <int NPER, bool VEC, int RULE>
+__global__ void __launch_bounds__(kThreads, NPER <= 8 ? 2 : 1)
+balance_kernel(const __grid_constant__ BalanceArgs a, int share, int one) {
     extern __shared__ float s_dyn[];
     bq::grid_dependency_wait();   // launched behind whatever precedes it on the stream
     bq::allow_dependents();
     int32_t* hist = reinterpret_cast<int32_t*>(s_dyn + sums_words(a.E));
-    chunk_sums<NPER, RULE>(a, s_dyn, hist);
-    if (ONE) {
+    if (!one && blockIdx.x == 0 && threadIdx.x == 0) *a.ended = 0;
+    chunk_sums<NPER, VEC, RULE>(a, s_dyn, hist);
+    if (one) {
         const int ranks = gridDim.x;
         if (ranks > 1) cluster_sync();   // the slots that the others wrote
         else __syncthreads();
@@ -312,13 +452,64 @@ balance_kernel(const BalanceArgs a, int share) {
     }
 }
 
+// Of many chunks: a CTA per group, its warps a share of the group's slots each.  The last CTA to end adds the groups'
+// losses up, in their order; balance_kernel has set the count of those that ended to 0.
 __global__ void __launch_bounds__(kThreads)
-balance_finish_kernel(const BalanceArgs a, int share) {
-    __shared__ float s_red[kThreads];
-    __shared__ int32_t s_redc[kThreads];
+balance_finish_kernel(const __grid_constant__ BalanceArgs a) {
+    __shared__ float s_red[kWarps][32];
+    __shared__ int32_t s_redc[kWarps][32];
+    __shared__ float s_sum[2][kWarps];
+    __shared__ int s_last;
     bq::grid_dependency_wait();
     bq::allow_dependents();
-    finish(a, cluster_rank(), gridDim.x, share, s_red, s_redc);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = (a.E + 31) / 32;
+    const int s = blockIdx.x / blocks, block = blockIdx.x - s * blocks, e = block * 32 + lane;
+    int lo, hi;
+    sequence(a.offsets, s, a.T, a.status, lo, hi);
+    GroupSums r = add_slots(a, s, block, lo, hi, warp, kWarps);
+    s_red[warp][lane] = r.p;
+    s_redc[warp][lane] = r.c;
+    r.z2 = warp_sum(r.z2);
+    if (lane == 0) s_sum[1][warp] = r.z2;
+    __syncthreads();
+    if (warp == 0) {
+        float z2 = 0.f, balance = 0.f;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            r.p += s_red[w][lane];
+            r.c += s_redc[w][lane];
+        }
+        for (int w = 0; w < kWarps; ++w) z2 += s_sum[1][w];
+        if (e < a.E) balance = write_group(a, s, e, lo, hi, r.p, r.c);
+        balance = warp_sum(balance);
+        if (lane == 0) {
+            a.part_loss[2 * blockIdx.x] = balance;
+            a.part_loss[2 * blockIdx.x + 1] = z2;
+            __threadfence();
+            s_last = atomicAdd(a.ended, 1) == (int)gridDim.x - 1;
+        }
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    const Totals totals = sequence_totals(a.offsets, a.S, a.T, 0, a.status);
+    float sum[2] = {0.f, 0.f};
+    for (int g = threadIdx.x; g < (int)gridDim.x; g += kThreads) {
+        sum[0] += __ldcg(a.part_loss + 2 * g);
+        sum[1] += __ldcg(a.part_loss + 2 * g + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        sum[i] = warp_sum(sum[i]);
+        if (lane == 0) s_sum[i][warp] = sum[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        float v = 0.f;
+        for (int w = 0; w < kWarps; ++w) v += s_sum[threadIdx.x][w];
+        const int n = threadIdx.x ? totals.rows : totals.used;
+        a.losses[threadIdx.x] = n ? v / (float)n : 0.f;
+    }
 }
 
 // ---------------------------------------------------------------- gradient
@@ -340,130 +531,238 @@ struct RouteGradArgs {
     int32_t* status;
 };
 
-// A warp per row, the whole gradient of the row in its registers: logits are read once, gradients written once.
-template <int NPER, int RULE, bool LOSSES>
-__global__ void __launch_bounds__(kThreads)
-route_backward_kernel(const RouteGradArgs a) {
-    extern __shared__ float s_dyn[];
-    __shared__ int s_totals[2];
+// What lane j < k has of its row's selected expert, as loaded: two rows ahead its id and gradient, one row ahead its
+// logit (a chain of two loads that a row would wait for).
+struct Pair {
+    int id = -1;
+    float dw = 0.f, z = -INFINITY;
+
+    __device__ __forceinline__ void load(const RouteGradArgs& a, int64_t r, int row1, int lane) {
+        id = -1;
+        if (r >= row1 || lane >= a.k) return;
+        id = __ldg(a.ids + r * a.k + lane);
+        dw = __ldg(a.dweights + r * a.k + lane);
+    }
+    __device__ __forceinline__ void load_logit(const RouteGradArgs& a, int64_t r) {
+        if (id < 0 || id >= a.E) return;   // reported when the row's turn comes, if it belongs to a sequence
+        z = __ldg(a.logits + r * a.E + id);
+        if (a.bias) z = __fadd_rn(z, __ldg(a.bias + id));
+    }
+};
+
+__device__ __forceinline__ float sum_of_eight(float v) {   // of lanes 0 .. 7, in each of them
+#pragma unroll
+    for (int off = 4; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// The gradient that the router weights bring: lane j < k gets its expert id (-1: none) and its share g.  Of lanes that
+// name the same expert the first gets the sum, the others -1.
+template <int RULE>
+__device__ __forceinline__ void selected(const RouteGradArgs& a, const Pair& p, int lane, int& id, float& g) {
+    id = p.id;
+    if (lane < a.k && (id < 0 || id >= a.E)) {
+        bq::set_device_error(a.status, BQ_DEV_BAD_EXPERT_ID);
+        id = -1;
+    }
+    if (RULE == RULE_SOFTMAX) {
+        const float m = warp_max(id >= 0 ? p.z : -INFINITY), ex = id >= 0 ? exp2_approx((p.z - m) * kLog2E) : 0.f;
+        const float w = __fdividef(ex, sum_of_eight(ex)), mean = sum_of_eight(id >= 0 ? w * p.dw : 0.f);
+        g = id >= 0 ? w * (p.dw - mean) : 0.f;
+    } else {
+        float score, slope, unused0, unused1;
+        scores_of<true>(p.z, 0.f, score, unused0, slope, unused1);
+        g = id >= 0 ? a.scale * p.dw * slope : 0.f;
+    }
+    // the same index twice (a router names none twice, a caller may): added in slot order
+    const uint32_t same = __match_any_sync(0xffffffffu, id >= 0 ? id : ~lane);
+    if (__any_sync(0xffffffffu, __popc(same) > 1)) {
+        float sum = 0.f;
+        for (int j = 0; j < a.k; ++j) {
+            const float gj = __shfl_sync(0xffffffffu, g, j);
+            if (same >> j & 1) sum += gj;
+        }
+        if (__popc(same) > 1) {
+            g = sum;
+            if (__ffs(same) - 1 != lane) id = -1;
+        }
+    }
+}
+
+// The rows of a CTA's chunk, a warp each, with the sequence that a row belongs to (rows ascend, so sequences do).
+struct Place {
+    int s, lo, hi;
+    bool fresh;   // the sequence changed
+
+    __device__ __forceinline__ bool find(const RouteGradArgs& a, int r) {
+        if (!a.offsets) return true;
+        while (s < a.S && r >= hi) {
+            sequence(a.offsets, s, a.T, a.status, lo, hi);
+            fresh = true;
+            if (r >= hi) ++s;
+        }
+        return r >= lo && r < hi;   // rows in none are left out
+    }
+};
+
+// A chunk's column sums: the warps' sums in warp order.
+__device__ __forceinline__ void write_part(const RouteGradArgs& a, const float* s_acc) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += s_acc[w * a.E + e];
+        a.part_b[(int64_t)blockIdx.x * a.E + e] = sum;
+    }
+}
+
+// With losses: a warp per row, the row's gradient of the losses in its registers.  Logits are read once and gradients
+// written once; the k selected values are then written again by the lanes that hold their share, each from its own
+// evaluation of the loss's gradient (cheaper than bringing the shares to the lanes that hold the experts).
+template <int NPER, bool VEC, int RULE>
+__global__ void __launch_bounds__(kThreads, NPER <= (RULE == RULE_SCORE ? 4 : 8) ? 2 : 1)
+route_backward_kernel(const __grid_constant__ RouteGradArgs a) {
+    using Row = Share<NPER, VEC>;
+    constexpr bool kAhead = NPER <= 8;   // the next row is loaded ahead, where there are registers for it
+    extern __shared__ float s_dyn[];   // with part_b: a row of sums per warp
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     bq::grid_dependency_wait();   // launched behind whatever precedes it on the stream
     bq::allow_dependents();
     const int64_t first = (int64_t)blockIdx.x * a.chunk_rows;
     const int row0 = (int)first, row1 = (int)min((int64_t)a.T, first + a.chunk_rows);
-    float per_seq = 0.f, per_row = 0.f;
-    if (LOSSES) {
-        sequence_totals(a.offsets, a.S, a.T, a.status, s_totals);
-        per_seq = __ldg(a.dlosses) * ((float)a.E / (float)a.k) / (float)max(1, s_totals[0]);
-        per_row = 2.f * __ldg(a.dlosses + 1) / (float)max(1, s_totals[1]);
+    float* s_acc = s_dyn + warp * a.E;
+    if (a.part_b)
+        for (int e = lane; e < a.E; e += 32) s_acc[e] = 0.f;
+    __syncwarp();
+    float z[NPER];
+    if (kAhead && row0 + warp < row1) Row::load(a.logits + (int64_t)(row0 + warp) * a.E, a.bias, a.E, lane, z);
+    Pair pair, pair1, pair2;
+    if (a.dweights) {
+        pair.load(a, row0 + warp, row1, lane);
+        pair1.load(a, (int64_t)row0 + warp + kWarps, row1, lane);
     }
-    int s = first_sequence(a.offsets, a.S, row0), lo = 0, hi = a.T;
-    if (a.offsets) lo = hi = -1;
-    float acc[NPER], weight[NPER];
+    const float dbalance = __ldg(a.dlosses), dz = __ldg(a.dlosses + 1);
+    const Totals totals = sequence_totals(a.offsets, a.S, a.T, row0, a.status);
+    const float per_seq = dbalance * ((float)a.E / (float)a.k) / (float)max(1, totals.used);
+    const float per_row = 2.f * dz / (float)max(1, totals.rows);
+    if (a.dweights) pair.load_logit(a, row0 + warp);
+    Place place{totals.before, a.offsets ? -1 : 0, a.offsets ? -1 : a.T, true};
+    float acc[NPER], weight[NPER], per_count = 0.f;
 #pragma unroll
     for (int i = 0; i < NPER; ++i) acc[i] = weight[i] = 0.f;
-    bool fresh = true;
     for (int r = row0 + warp; r < row1; r += kWarps) {
-        if (a.offsets) {   // rows ascend, so the sequences do too; rows in none are left out
-            while (s < a.S && r >= hi) {
-                sequence(a.offsets, s, a.T, a.status, lo, hi);
-                fresh = true;
-                if (r >= hi) ++s;
-            }
-            if (r < lo || r >= hi) continue;
-        }
-        if (LOSSES && fresh) {
-            const float n = (float)(hi - lo);
-#pragma unroll
-            for (int i = 0; i < NPER; ++i) {
-                const int e = lane + 32 * i;
-                weight[i] = e < a.E ? (float)__ldg(a.counts + (int64_t)s * a.E + e) * (per_seq / n / n) : 0.f;
-            }
-            fresh = false;
-        }
-        const float* row = a.logits + (int64_t)r * a.E;
-        // the selected experts, a lane each: their logit, weight and the gradient that the weights bring
-        int id = -1;
-        float dw = 0.f, zs = -INFINITY;
-        if (a.dweights && lane < a.k) {
-            id = __ldg(a.ids + (int64_t)r * a.k + lane);
-            if (id < 0 || id >= a.E) {
-                bq::set_device_error(a.status, BQ_DEV_BAD_EXPERT_ID);
-                id = -1;
-            } else {
-                dw = __ldg(a.dweights + (int64_t)r * a.k + lane);
-                zs = __ldg(row + id);
-                if (a.bias) zs = __fadd_rn(zs, __ldg(a.bias + id));
-            }
-        }
-        float d[NPER];
-#pragma unroll
-        for (int i = 0; i < NPER; ++i) d[i] = 0.f;
-        if (LOSSES) {
-            float z[NPER], p[NPER], lse;
-            load_row(row, a.bias, a.E, lane, z);
-            softmax_row(z, p, lse);
-            const float f = per_row * lse;
-            if (RULE == RULE_SOFTMAX) {
-                float dot = 0.f;
-#pragma unroll
-                for (int i = 0; i < NPER; ++i) dot = __fmaf_rn(p[i], weight[i], dot);
-                dot = warp_sum(dot);
-#pragma unroll
-                for (int i = 0; i < NPER; ++i) d[i] = p[i] * (weight[i] - dot + f);
-            } else {
-                float sc[NPER], inv, dot = 0.f;
-                score_row(z, a.E, lane, sc, inv);
-#pragma unroll
-                for (int i = 0; i < NPER; ++i) dot = __fmaf_rn(sc[i] * inv, weight[i], dot);
-                dot = warp_sum(dot);
-#pragma unroll
-                for (int i = 0; i < NPER; ++i) {
-                    const float t = sc[i] == 0.f ? 0.f : score_slope(z[i], sc[i]) * inv * (weight[i] - dot);
-                    d[i] = __fmaf_rn(p[i], f, t);
-                }
-            }
-        }
+        float next[NPER];
         if (a.dweights) {
-            float g;
-            if (RULE == RULE_SOFTMAX) {
-                const float m = warp_max(zs);
-                const float ex = id >= 0 ? expf(zs - m) : 0.f;
-                const float w = ex / warp_sum(ex);
-                const float mean = warp_sum(id >= 0 ? w * dw : 0.f);
-                g = w * (dw - mean);
-            } else {
-                const float sc = score_of(zs);
-                g = id >= 0 && sc != 0.f ? a.scale * dw * score_slope(zs, sc) : 0.f;
-            }
-            for (int j = 0; j < a.k; ++j) {
-                const int ej = __shfl_sync(0xffffffffu, id, j);
-                const float gj = __shfl_sync(0xffffffffu, g, j);
-                if (ej >= 0 && (ej & 31) == lane) {
+            pair1.load_logit(a, (int64_t)r + kWarps);
+            pair2.load(a, (int64_t)r + 2 * kWarps, row1, lane);
+        }
+        if (!kAhead) Row::load(a.logits + (int64_t)r * a.E, a.bias, a.E, lane, z);
+        else if (r + kWarps < row1) Row::load(a.logits + (int64_t)(r + kWarps) * a.E, a.bias, a.E, lane, next);
+        if (place.find(a, r)) {
+            const int32_t* counts = a.counts + (int64_t)place.s * a.E;
+            if (place.fresh) {
+                const float n = (float)(place.hi - place.lo);
+                per_count = per_seq / n / n;
 #pragma unroll
-                    for (int i = 0; i < NPER; ++i)
-                        if (ej >> 5 == i) d[i] += gj;
+                for (int i = 0; i < NPER; ++i)
+                    weight[i] = Row::at(lane, i) < a.E ? (float)__ldg(counts + Row::at(lane, i)) * per_count : 0.f;
+                place.fresh = false;
+            }
+            int id = -1;
+            float g = 0.f, own = 0.f;
+            const float zs = pair.z;
+            if (a.dweights) {
+                selected<RULE>(a, pair, lane, id, g);
+                if (id >= 0) own = (float)__ldg(counts + id) * per_count;
+            }
+            float d[NPER];
+            const Softmax soft = softmax_row(z, d);
+            const float f = per_row * soft.lse * soft.inv;
+            float dot = 0.f, base = 0.f;
+            if (RULE == RULE_SOFTMAX) {
+#pragma unroll
+                for (int i = 0; i < NPER; ++i) dot = __fmaf_rn(d[i], weight[i], dot);
+                dot = warp_sum(dot) * soft.inv;
+#pragma unroll
+                for (int i = 0; i < NPER; ++i) d[i] *= __fmaf_rn(weight[i] - dot, soft.inv, f);
+                if (id >= 0) base = exp2_approx((zs - soft.m) * kLog2E) * __fmaf_rn(own - dot, soft.inv, f);
+            } else {
+                float sc[NPER], slope[NPER];
+                const float inv = score_row<true>(z, sc, slope);
+#pragma unroll
+                for (int i = 0; i < NPER; ++i) dot = __fmaf_rn(sc[i], weight[i], dot);
+                dot = warp_sum(dot) * inv;
+#pragma unroll
+                for (int i = 0; i < NPER; ++i) d[i] = __fmaf_rn(d[i], f, slope[i] * inv * (weight[i] - dot));
+                if (id >= 0) {
+                    float score, change, unused0, unused1;
+                    scores_of<true>(zs, 0.f, score, unused0, change, unused1);
+                    base = __fmaf_rn(exp2_approx((zs - soft.m) * kLog2E), f, change * inv * (own - dot));
                 }
             }
-        }
+            Row::store(a.dlogits, r, a.dtype, a.E, lane, d);
+            __syncwarp();   // the row is written before its selected values are written again
+            if (id >= 0) store_value(a.dlogits, (int64_t)r * a.E + id, a.dtype, base + g);
+            if (a.part_b) {
+                if (id >= 0) s_acc[id] += g;
+                __syncwarp();
 #pragma unroll
-        for (int i = 0; i < NPER; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.E) bq::store_value(a.dlogits, (int64_t)r * a.E + e, a.dtype, d[i]);
-            acc[i] += d[i];
+                for (int i = 0; i < NPER; ++i) acc[i] += d[i];
+            }
+        }
+        pair = pair1;
+        pair1 = pair2;
+        if (kAhead) {
+#pragma unroll
+            for (int i = 0; i < NPER; ++i) z[i] = next[i];
         }
     }
     if (!a.part_b) return;
 #pragma unroll
     for (int i = 0; i < NPER; ++i)
-        if (lane + 32 * i < a.E) s_dyn[warp * a.E + lane + 32 * i] = acc[i];
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += s_dyn[w * a.E + e];
-        a.part_b[(int64_t)blockIdx.x * a.E + e] = sum;
+        if (Row::at(lane, i) < a.E) s_acc[Row::at(lane, i)] += acc[i];
+    write_part(a, s_dyn);
+}
+
+// Without losses: only the k selected values differ from 0, and only their logits are read.  wide: rows of 16-byte
+// vectors.
+template <int RULE>
+__global__ void __launch_bounds__(kThreads)
+route_weights_backward_kernel(const __grid_constant__ RouteGradArgs a, int wide) {
+    extern __shared__ float s_dyn[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    bq::grid_dependency_wait();   // launched behind whatever precedes it on the stream
+    bq::allow_dependents();
+    const int64_t first = (int64_t)blockIdx.x * a.chunk_rows;
+    const int row0 = (int)first, row1 = (int)min((int64_t)a.T, first + a.chunk_rows);
+    const int es = a.dtype == BQ_DT_F32 ? 4 : 2;
+    float* s_acc = s_dyn + warp * a.E;
+    if (a.part_b)
+        for (int e = lane; e < a.E; e += 32) s_acc[e] = 0.f;
+    __syncwarp();
+    Place place{sequence_totals(a.offsets, a.S, a.T, row0, a.status).before, a.offsets ? -1 : 0, a.offsets ? -1 : a.T, true};
+    for (int r = row0 + warp; r < row1; r += kWarps) {
+        if (!place.find(a, r)) continue;
+        uint8_t* row = static_cast<uint8_t*>(a.dlogits) + (int64_t)r * a.E * es;
+        if (wide) {
+            for (int i = lane; i < a.E * es / 16; i += 32) reinterpret_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int i = lane; i < a.E; i += 32) store_value(row, i, a.dtype, 0.f);
+        }
+        int id;
+        float g;
+        Pair pair;
+        pair.load(a, r, row1, lane);
+        pair.load_logit(a, r);
+        selected<RULE>(a, pair, lane, id, g);
+        __syncwarp();   // the zeros are written before the values
+        if (id >= 0) {
+            store_value(row, id, a.dtype, g);
+            if (a.part_b) s_acc[id] += g;
+        }
+        __syncwarp();
     }
+    if (a.part_b) write_part(a, s_dyn);
 }
 
 // out[e] = the sum of part[0..parts)[e], 32 columns a CTA.
@@ -507,14 +806,17 @@ Chunking balance_chunking(int T) { return T <= kOneClusterRows ? chunking(T, 8, 
 
 Chunking gradient_chunking(int T) { return chunking(T, 2 * kSms, kWarps); }
 
+// Calls f with the experts of a lane and whether they are taken four at a time.
 template <typename F>
-void with_nper(int E, F f) {
-    if (E <= 32) f(std::integral_constant<int, 1>());
-    else if (E <= 64) f(std::integral_constant<int, 2>());
-    else if (E <= 128) f(std::integral_constant<int, 4>());
-    else if (E <= 256) f(std::integral_constant<int, 8>());
-    else if (E <= 512) f(std::integral_constant<int, 16>());
-    else f(std::integral_constant<int, 32>());
+void with_share(int E, bool vec, F f) {
+    const std::true_type yes;
+    const std::false_type no;
+    if (E <= 32) f(std::integral_constant<int, 1>(), no);
+    else if (E <= 64) f(std::integral_constant<int, 2>(), no);
+    else if (E <= 128) vec ? f(std::integral_constant<int, 4>(), yes) : f(std::integral_constant<int, 4>(), no);
+    else if (E <= 256) vec ? f(std::integral_constant<int, 8>(), yes) : f(std::integral_constant<int, 8>(), no);
+    else if (E <= 512) vec ? f(std::integral_constant<int, 16>(), yes) : f(std::integral_constant<int, 16>(), no);
+    else vec ? f(std::integral_constant<int, 32>(), yes) : f(std::integral_constant<int, 32>(), no);
 }
 
 bq_status check_router(const char* name, int T, int E, int k, int scoring, const int32_t* offsets, int S) {
@@ -570,10 +872,11 @@ cudaError_t allow_smem(Kernel kernel, size_t smem) {
                              : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
-// Warps that share a group of experts: enough for about four slots each.
-int share_of(int64_t slots, int S) {
+// Warps that share a group of 32 experts of a sequence: as many as there are for it, but two slots each at least.
+int share_of(int warps, int64_t slots, int S, int E) {
+    const int64_t groups = (int64_t)S * ((E + 31) / 32);
     int share = 1;
-    while (share < kWarps && slots / S > 4 * share) share *= 2;
+    while (share < kWarps && 2 * share * groups <= warps && slots / S >= 4 * share) share *= 2;
     return share;
 }
 
@@ -582,7 +885,7 @@ int share_of(int64_t slots, int S) {
 extern "C" size_t bq_moe_balance_workspace_bytes(int32_t T, int32_t E, int32_t S) {
     if (T < 0 || E < 1 || E > 1024 || S < 1 || S > kMaxSequences) return 0;
     const size_t slots = (size_t)balance_chunking(T).chunks + S;
-    return 2 * up256(slots * E * 4) + up256(slots * 4);
+    return 2 * up256(slots * E * 4) + up256(slots * 4) + up256((size_t)S * ((E + 31) / 32) * 8) + 256;
 }
 
 extern "C" bq_status bq_moe_balance_loss(const float* logits, const float* bias, int32_t T, int32_t E,
@@ -609,24 +912,28 @@ extern "C" bq_status bq_moe_balance_loss(const float* logits, const float* bias,
     uint8_t* base = static_cast<uint8_t*>(workspace);
     const BalanceArgs a{logits, bias, T, E, k, ids, seq_offsets, S, c.rows, c.chunks, reinterpret_cast<float*>(base),
                         reinterpret_cast<int32_t*>(base + up256(slots * E * 4)),
-                        reinterpret_cast<float*>(base + 2 * up256(slots * E * 4)), counts, probs, losses,
-                        bq::device_status_ptr()};
-    const bool one = T <= kOneClusterRows;
-    const int share = share_of((int64_t)slots, S);
+                        reinterpret_cast<float*>(base + 2 * up256(slots * E * 4)),
+                        reinterpret_cast<float*>(base + 2 * up256(slots * E * 4) + up256(slots * 4)),
+                        reinterpret_cast<int*>(base + need - 256), counts, probs, losses, bq::device_status_ptr()};
+    const bool one = T <= kOneClusterRows, vec = E % 4 == 0 && bq::aligned(logits, 16);
+    const int ctas = std::max(1, c.chunks);
+    const int share = share_of(ctas * kWarps, slots, S, E);
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = cudaSuccess;
-    with_nper(E, [&](auto nper) {
+    with_share(E, vec, [&](auto nper, auto v) {
         constexpr int N = decltype(nper)::value;
+        constexpr bool VEC = decltype(v)::value;
         auto go = [&](auto kernel) {
             if ((e = allow_smem(kernel, balance_smem(E))) != cudaSuccess) return;
-            if (one) e = launch_cluster(kernel, std::max(1, c.chunks), balance_smem(E), st, a, share);
-            else e = bq::launch_after(kernel, dim3(c.chunks), dim3(kThreads), balance_smem(E), st, a, share);
+            if (one) e = launch_cluster(kernel, ctas, balance_smem(E), st, a, share, 1);
+            else e = bq::launch_after(kernel, dim3(ctas), dim3(kThreads), balance_smem(E), st, a, share, 0);
         };
-        if (scoring == BQ_SCORE_SQRTSOFTPLUS) one ? go(balance_kernel<N, RULE_SCORE, true>) : go(balance_kernel<N, RULE_SCORE, false>);
-        else one ? go(balance_kernel<N, RULE_SOFTMAX, true>) : go(balance_kernel<N, RULE_SOFTMAX, false>);
+        if (scoring == BQ_SCORE_SQRTSOFTPLUS) go(balance_kernel<N, VEC, RULE_SCORE>);
+        else go(balance_kernel<N, VEC, RULE_SOFTMAX>);
     });
     if ((s = launched(name, e)) != BQ_OK || one) return s;
-    return launched(name, launch_cluster(balance_finish_kernel, 8, 0, st, a, share));
+    return launched(name, bq::launch_after(balance_finish_kernel, dim3((unsigned)(S * ((E + 31) / 32))), dim3(kThreads), 0,
+                                           st, a));
 }
 
 extern "C" size_t bq_moe_route_backward_workspace_bytes(int32_t T, int32_t E) {
@@ -671,18 +978,23 @@ extern "C" bq_status bq_moe_route_backward(const float* logits, const float* bia
                           dtype, dbias ? static_cast<float*>(workspace) : nullptr, bq::device_status_ptr()};
     if (T > 0) {
         const size_t smem = dbias ? (size_t)kWarps * E * 4 : 0;
+        const bool score = scoring == BQ_SCORE_SQRTSOFTPLUS;
         cudaError_t e = cudaSuccess;
-        with_nper(E, [&](auto nper) {
-            constexpr int N = decltype(nper)::value;
-            auto go = [&](auto kernel) {
-                if ((e = allow_smem(kernel, smem)) != cudaSuccess) return;
-                e = bq::launch_after(kernel, dim3(c.chunks), dim3(kThreads), smem, st, a);
-            };
-            if (scoring == BQ_SCORE_SQRTSOFTPLUS)
-                dlosses ? go(route_backward_kernel<N, RULE_SCORE, true>) : go(route_backward_kernel<N, RULE_SCORE, false>);
-            else
-                dlosses ? go(route_backward_kernel<N, RULE_SOFTMAX, true>) : go(route_backward_kernel<N, RULE_SOFTMAX, false>);
-        });
+        auto go = [&](auto kernel, auto... more) {
+            if ((e = allow_smem(kernel, smem)) == cudaSuccess)
+                e = bq::launch_after(kernel, dim3(c.chunks), dim3(kThreads), smem, st, a, more...);
+        };
+        if (dlosses) {
+            const bool vec = E % 4 == 0 && bq::aligned(logits, 16) && bq::aligned(dlogits, 4 * es);
+            with_share(E, vec, [&](auto nper, auto v) {
+                constexpr int N = decltype(nper)::value;
+                constexpr bool VEC = decltype(v)::value;
+                score ? go(route_backward_kernel<N, VEC, RULE_SCORE>) : go(route_backward_kernel<N, VEC, RULE_SOFTMAX>);
+            });
+        } else {
+            const int wide = E * es % 16 == 0 && bq::aligned(dlogits, 16);
+            score ? go(route_weights_backward_kernel<RULE_SCORE>, wide) : go(route_weights_backward_kernel<RULE_SOFTMAX>, wide);
+        }
         if ((s = launched(name, e)) != BQ_OK) return s;
     }
     if (!dbias) return BQ_OK;
