@@ -527,7 +527,8 @@ struct RouteGradArgs {
     int chunk_rows;
     void* dlogits;
     int dtype;
-    float* part_b;           // [chunks][E] sums of the bias gradient, or NULL
+    float* part_b;           // [chunks][E] sums of the bias gradient, or NULL: it is not wanted
+    float* dbias;            // not NULL: the launch is one cluster, and writes it
     int32_t* status;
 };
 
@@ -605,15 +606,27 @@ struct Place {
     }
 };
 
-// A chunk's column sums: the warps' sums in warp order.
-__device__ __forceinline__ void write_part(const RouteGradArgs& a, const float* s_acc) {
+// A chunk's column sums: the warps' sums in warp order.  Where the launch is one cluster, its CTAs add the chunks up at
+// once, each a share of the columns, in the order of the chunks.
+__device__ __forceinline__ void write_part(const RouteGradArgs& a, float* s_acc) {
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += kThreads) {
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) sum += s_acc[w * a.E + e];
-        a.part_b[(int64_t)blockIdx.x * a.E + e] = sum;
+        if (a.dbias) s_acc[e] = sum;   // of the column's own thread, which has read it
+        else a.part_b[(int64_t)blockIdx.x * a.E + e] = sum;
     }
+    if (!a.dbias) return;
+    const int ranks = gridDim.x;
+    if (ranks > 1) cluster_sync();
+    else __syncthreads();
+    for (int e = blockIdx.x * kThreads + threadIdx.x; e < a.E; e += ranks * kThreads) {
+        float sum = 0.f;
+        for (int r = 0; r < ranks; ++r) sum += ranks > 1 ? peer_load(s_acc + e, r) : s_acc[e];
+        a.dbias[e] = sum;
+    }
+    if (ranks > 1) cluster_sync();   // peers may still be reading
 }
 
 // With losses: a warp per row, the row's gradient of the losses in its registers.  Logits are read once and gradients
@@ -804,7 +817,10 @@ constexpr int kOneClusterRows = 1024;
 
 Chunking balance_chunking(int T) { return T <= kOneClusterRows ? chunking(T, 8, kWarps) : chunking(T, 2 * kSms, kWarps); }
 
-Chunking gradient_chunking(int T) { return chunking(T, 2 * kSms, kWarps); }
+// One cluster for few rows where there is a bias gradient to add up over them.
+Chunking gradient_chunking(int T, bool bias) {
+    return bias && T <= kOneClusterRows ? chunking(T, 8, kWarps) : chunking(T, 2 * kSms, kWarps);
+}
 
 // Calls f with the experts of a lane and whether they are taken four at a time.
 template <typename F>
@@ -938,7 +954,7 @@ extern "C" bq_status bq_moe_balance_loss(const float* logits, const float* bias,
 
 extern "C" size_t bq_moe_route_backward_workspace_bytes(int32_t T, int32_t E) {
     if (T < 0 || E < 1 || E > 1024) return 0;
-    return up256((size_t)std::max(1, gradient_chunking(T).chunks) * E * 4);
+    return up256((size_t)std::max(1, gradient_chunking(T, true).chunks) * E * 4);
 }
 
 extern "C" bq_status bq_moe_route_backward(const float* logits, const float* bias, int32_t T, int32_t E,
@@ -964,7 +980,8 @@ extern "C" bq_status bq_moe_route_backward(const float* logits, const float* bia
     if (!bq::aligned(dlogits, es)) return bq::fail(BQ_ERR_ALIGN, "%s: dlogits must be aligned to its element", name);
     if ((bias || dbias) && scoring != BQ_SCORE_SOFTMAX)
         return bq::fail(BQ_ERR_SHAPE, "%s: under rule %d the bias only selects: pass NULL, it has no gradient", name, scoring);
-    const Chunking c = gradient_chunking(T);
+    const Chunking c = gradient_chunking(T, dbias != nullptr);
+    const bool one = dbias && T > 0 && T <= kOneClusterRows;
     if (dbias) {
         const size_t need = bq_moe_route_backward_workspace_bytes(T, E);
         if (!workspace || workspace_bytes < need)
@@ -975,14 +992,15 @@ extern "C" bq_status bq_moe_route_backward(const float* logits, const float* bia
     if ((s = bq::check_arch()) != BQ_OK) return s;
     cudaStream_t st = (cudaStream_t)stream;
     const RouteGradArgs a{logits, bias, T, E, k, ids, dweights, scale, counts, dlosses, seq_offsets, S, c.rows, dlogits,
-                          dtype, dbias ? static_cast<float*>(workspace) : nullptr, bq::device_status_ptr()};
+                          dtype, dbias ? static_cast<float*>(workspace) : nullptr, one ? dbias : nullptr, bq::device_status_ptr()};
     if (T > 0) {
         const size_t smem = dbias ? (size_t)kWarps * E * 4 : 0;
         const bool score = scoring == BQ_SCORE_SQRTSOFTPLUS;
         cudaError_t e = cudaSuccess;
         auto go = [&](auto kernel, auto... more) {
-            if ((e = allow_smem(kernel, smem)) == cudaSuccess)
-                e = bq::launch_after(kernel, dim3(c.chunks), dim3(kThreads), smem, st, a, more...);
+            if ((e = allow_smem(kernel, smem)) != cudaSuccess) return;
+            if (one) e = launch_cluster(kernel, c.chunks, smem, st, a, more...);
+            else e = bq::launch_after(kernel, dim3(c.chunks), dim3(kThreads), smem, st, a, more...);
         };
         if (dlosses) {
             const bool vec = E % 4 == 0 && bq::aligned(logits, 16) && bq::aligned(dlogits, 4 * es);
@@ -997,7 +1015,7 @@ extern "C" bq_status bq_moe_route_backward(const float* logits, const float* bia
         }
         if ((s = launched(name, e)) != BQ_OK) return s;
     }
-    if (!dbias) return BQ_OK;
+    if (!dbias || one) return BQ_OK;
     return launched(name, bq::launch_after(column_sums_kernel, dim3((E + 31) / 32), dim3(kThreads), 0, st,
                                            (const float*)workspace, T > 0 ? c.chunks : 0, E, dbias));
 }

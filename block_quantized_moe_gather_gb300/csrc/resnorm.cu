@@ -94,6 +94,134 @@ residual_norm_kernel(const __grid_constant__ ForwardArgs a) {
     }
 }
 
+// The same for many rows (a vector behind a row's last is zeros): blocks walk over them with the next rows on their way (resnorm.cuh) and the columns' constants
+// kept as fp32, so that the loads' latency and the conversions of the gains are not paid row by row.
+struct ManyArgs {
+    ForwardArgs f;
+    int stages, stage_bytes, at_stages, at_branch;   // bytes; at_branch -1: the branch's constant is scale alone
+};
+
+template <int DY, int DH, int DX, int THREADS, bool POST>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+residual_norm_many_kernel(const __grid_constant__ ManyArgs m) {
+    constexpr int PLANE = THREADS * kVpt * 16;
+    constexpr int kY = 0, kH = planes(DY) * PLANE, kFull = kH + planes(DH) * PLANE;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ SumBuf s_buf;
+    const ForwardArgs& a = m.f;
+    const Gate& gate = a.columns.gate;
+    const bool full = gate.kind == GATE_FULL;
+    const int vecs = a.H / 8, tid = threadIdx.y * blockDim.x + threadIdx.x;
+    bool has[kVpt];
+#pragma unroll
+    for (int v = 0; v < kVpt; ++v) has[v] = (int)(threadIdx.x + v * blockDim.x) < vecs;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y, block0 = (int64_t)blockIdx.x * blockDim.y;
+    const int end = m.at_stages + m.stages * m.stage_bytes;
+    uint8_t* own = smem + tid * 16;
+    zero_missing<PLANE>(own, end, has);
+    const uint32_t own_u32 = (uint32_t)__cvta_generic_to_shared(own);
+    // a thread's first vector in the rows of a block, from the block's first row on (the host made sure that it is an int)
+    auto offset = [&](int64_t ld, int dtype) {
+        return (int)threadIdx.y * (int)ld + (int)threadIdx.x * (dtype == BQ_DT_F32 ? 32 : 16);
+    };
+    const int o_y = offset(a.y.ld, a.y.dtype), o_h = offset(a.h.ld, a.h.dtype), o_full = offset(a.ld_full, gate.dtype);
+    const int o_out = offset(a.out.ld, a.out.dtype), o_x = offset(a.x.ld, a.x.dtype);
+    // launched behind whatever precedes it on the stream: nothing before this line touches global memory
+    bq::grid_dependency_wait();
+    bq::allow_dependents();
+    auto fetch_row = [&](int stage, int64_t r0) {
+        const uint32_t to = own_u32 + stage;
+        if (r0 + threadIdx.y < a.T) {
+            fetch<DY, PLANE>(to + kY, a.y.p + r0 * a.y.ld + o_y, a.y.dtype, has);
+            fetch<DH, PLANE>(to + kH, a.h.p + r0 * a.h.ld + o_h, a.h.dtype, has);
+            if (full) fetch<kAny, PLANE>(to + kFull, a.full + r0 * a.ld_full + o_full, gate.dtype, has);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int ahead = m.at_stages;
+    int64_t next = block0;
+    for (int i = 0; i < m.stages - 1; ++i) {
+        fetch_row(ahead, next);
+        ahead += m.stage_bytes;
+        next += step;
+    }
+    const bool branch = m.at_branch >= 0;
+    keep_columns<PLANE, POST>(own, branch ? own + m.at_branch : nullptr, a.columns, threadIdx.x, has);
+    const float inv_h = 1.f / (float)a.H;
+    int stage = m.at_stages, turn = 0;
+    for (int64_t t0 = block0; t0 < a.T; t0 += step) {
+        const int64_t t = t0 + threadIdx.y;
+        const bool live = t < a.T;
+        if (m.stages == 2) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        else asm volatile("cp.async.wait_group 1;" ::: "memory");
+        fetch_row(ahead, next);
+        next += step;
+        ahead = ahead + m.stage_bytes == end ? m.at_stages : ahead + m.stage_bytes;
+        const uint8_t* st = own + stage;
+        stage = stage + m.stage_bytes == end ? m.at_stages : stage + m.stage_bytes;
+        float f = token_factor(gate, t, live);
+        if (!branch) f *= a.columns.scale;
+        Vec r[kVpt];
+#pragma unroll
+        for (int v = 0; v < kVpt; ++v) r[v] = staged8<DY, PLANE>(st + kY, v, a.y.dtype);
+        if (POST) {
+            f32x2 squares = both(0.f);
+#pragma unroll
+            for (int v = 0; v < kVpt; ++v)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) squares = fma2(r[v].p[j], r[v].p[j], squares);
+            f *= rsqrtf(__fmaf_rn(row_sum(sum2(squares), s_buf, turn), inv_h, a.eps));
+        }
+        f32x2 squares = both(0.f);
+        uint8_t* to_out = a.out.p + t0 * a.out.ld + o_out;
+#pragma unroll
+        for (int v = 0; v < kVpt; ++v) {
+            const Vec o = staged8<DH, PLANE>(st + kH, v, a.h.dtype);
+            if (branch) {
+                const Vec c = kept8<PLANE>(own + m.at_branch, v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[v].p[j] = mul2(r[v].p[j], c.p[j]);
+            }
+            if (full) {
+                Vec w = staged8<kAny, PLANE>(st + kFull, v, gate.dtype);
+                if (gate.sigmoid) w = sigmoid8(w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[v].p[j] = mul2(r[v].p[j], w.p[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                r[v].p[j] = fma2(r[v].p[j], both(f), mul2(o.p[j], both(a.residual_scale)));
+                squares = fma2(r[v].p[j], r[v].p[j], squares);
+            }
+            if (live && has[v]) store8<DH>(to_out, v * blockDim.x, a.out.dtype, r[v]);
+        }
+        if (!a.x.p) continue;
+        const float norm = rsqrtf(__fmaf_rn(row_sum(sum2(squares), s_buf, turn), inv_h, a.eps));
+        uint8_t* to_x = a.x.p + t0 * a.x.ld + o_x;
+#pragma unroll
+        for (int v = 0; v < kVpt; ++v) {
+            const Vec c = kept8<PLANE>(own, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[v].p[j] = mul2(mul2(r[v].p[j], both(norm)), c.p[j]);
+            if (live && has[v]) store8<DX>(to_x, v * blockDim.x, a.x.dtype, r[v]);
+        }
+    }
+}
+
+template <auto kernel>
+cudaError_t launch_many(const ManyArgs& m, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
+    // per device: the attribute is a property of the function on the current device
+    static std::atomic<bool> attr_set[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemOfSm);
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(true, std::memory_order_release);
+    }
+    return bq::launch_after(kernel, grid, block, smem, st, m);
+}
+
 }  // namespace
 
 extern "C" bq_status bq_residual_norm(const bq_residual_norm_desc* d, const void* y, int64_t ldy, const void* h,
@@ -120,6 +248,31 @@ extern "C" bq_status bq_residual_norm(const bq_residual_norm_desc* d, const void
     const int threads = ((vecs + per - 1) / per + 31) / 32 * 32, per_cta = std::max(1, 256 / threads);
     const dim3 grid((unsigned)(((int64_t)d->T + per_cta - 1) / per_cta)), block(threads, per_cta);
     cudaError_t e = cudaSuccess;
+    // many rows, of which a block of 256 or 512 threads holds one or more
+    const int wide_block = vecs > 256 * kVpt ? 512 : 256;
+    const int64_t far = std::max({a.y.ld, a.h.ld, a.out.ld, a.x.ld, a.ld_full});
+    if (d->T > 2 * kSms && vecs <= 512 * kVpt && far <= INT32_MAX / 16) {
+        with_types(d->y_dtype, d->h_dtype, x_dtype, [&](auto type) {
+            using D = decltype(type);
+            const bool branch = d->post_gain || d->gate_kind == BQ_GATE_CHANNEL;
+            const int plane = wide_block * kVpt * 16, full = d->gate_kind == BQ_GATE_FULL ? planes(d->gate_dtype) : 0;
+            ManyArgs m{a, 2, (planes(D::y) + planes(D::h) + full) * plane, (branch ? 4 : 2) * plane, branch ? 2 * plane : -1};
+            auto smem = [&] { return (size_t)m.at_stages + (size_t)m.stages * m.stage_bytes; };
+            const int per_sm = (int)std::max<size_t>(1, std::min<size_t>(1024 / wide_block, kSmemOfSm / smem()));
+            if (smem() + m.stage_bytes <= kSmemOfSm / per_sm) m.stages = 3;
+            const int x_threads = ((vecs + kVpt - 1) / kVpt + 31) / 32 * 32, row_groups = std::max(1, wide_block / x_threads);
+            const int64_t blocks = std::min<int64_t>(kSms * per_sm, ((int64_t)d->T + row_groups - 1) / row_groups);
+            const dim3 g((unsigned)blocks), b(x_threads, row_groups);
+            cudaStream_t st = (cudaStream_t)stream;
+            if (wide_block == 256)
+                e = d->post_gain ? launch_many<residual_norm_many_kernel<D::y, D::h, D::x, 256, true>>(m, g, b, smem(), st)
+                                 : launch_many<residual_norm_many_kernel<D::y, D::h, D::x, 256, false>>(m, g, b, smem(), st);
+            else
+                e = d->post_gain ? launch_many<residual_norm_many_kernel<D::y, D::h, D::x, 512, true>>(m, g, b, smem(), st)
+                                 : launch_many<residual_norm_many_kernel<D::y, D::h, D::x, 512, false>>(m, g, b, smem(), st);
+        });
+        return launched(name, e);
+    }
     with_types(d->y_dtype, d->h_dtype, x_dtype, [&](auto type) {
         using D = decltype(type);
         auto go = [&](auto kernel) { e = bq::launch_after(kernel, grid, block, 0, (cudaStream_t)stream, a); };

@@ -196,7 +196,94 @@ __device__ __forceinline__ void row_sums(float (&v)[8], SumBuf& buf, int& turn, 
     for (int n = 0; n < 8; ++n) v[n] = __shfl_sync(0xffffffffu, t, n * at);
 }
 
+// ---------------------------------------------------------------- rows in flight
+// Each thread fetches the vectors that it will use itself, rows ahead, into shared memory of its own (cp.async): the
+// loads need no registers while they are in flight, and no barrier when they land.
+constexpr int kVpt = 2;   // vectors of a thread
+
+// Where a thread keeps its vectors of a row in flight: planes of 16 bytes per vector of the block (an fp32 vector takes
+// two), so that a warp's lie in distinct banks, and places that are constants.
+__host__ __device__ constexpr int planes(int dt) { return dt == BQ_DT_F16 || dt == BQ_DT_BF16 ? 1 : 2; }
+
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// A thread's vectors of a row into a stage.
+template <int DT, int PLANE>
+__device__ __forceinline__ void fetch(uint32_t dst, const uint8_t* src, int dtype, const bool (&has)[kVpt]) {
+    const bool wide = (DT == kAny ? dtype : DT) == BQ_DT_F32;
+#pragma unroll
+    for (int v = 0; v < kVpt; ++v) {
+        if (!has[v]) continue;
+        const uint8_t* p = src + v * (int)blockDim.x * (wide ? 32 : 16);
+        copy16_async(dst + v * (PLANE / kVpt), p);
+        if (wide) copy16_async(dst + v * (PLANE / kVpt) + PLANE, p + 16);
+    }
+}
+
+template <int DT, int PLANE>
+__device__ __forceinline__ Vec staged8(const uint8_t* at, int v, int dtype) {
+    const uint8_t* p = at + v * (PLANE / kVpt);
+    const uint4 lo = *reinterpret_cast<const uint4*>(p);
+    if ((DT == kAny ? dtype : DT) != BQ_DT_F32) return unpack8<DT>(lo, lo, dtype);
+    return unpack8<BQ_DT_F32>(lo, *reinterpret_cast<const uint4*>(p + PLANE), dtype);
+}
+
+template <int PLANE>
+__device__ __forceinline__ void keep8(uint8_t* at, int v, const Vec& x) {
+    uint8_t* p = at + v * (PLANE / kVpt);
+    *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(x.p[0], x.p[1]);
+    *reinterpret_cast<ulonglong2*>(p + PLANE) = make_ulonglong2(x.p[2], x.p[3]);
+}
+
+template <int PLANE>
+__device__ __forceinline__ Vec kept8(const uint8_t* at, int v) {
+    const uint8_t* p = at + v * (PLANE / kVpt);
+    const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(p), hi = *reinterpret_cast<const ulonglong2*>(p + PLANE);
+    return {{lo.x, lo.y, hi.x, hi.y}};
+}
+
+// Zeros in a thread's places of vectors that it does not have, up to `end` bytes.
+template <int PLANE>
+__device__ __forceinline__ void zero_missing(uint8_t* own, int end, const bool (&has)[kVpt]) {
+#pragma unroll
+    for (int v = 0; v < kVpt; ++v) {
+        if (has[v]) continue;
+        for (int i = v * (PLANE / kVpt); i < end; i += PLANE) *reinterpret_cast<uint4*>(own + i) = make_uint4(0, 0, 0, 0);
+    }
+}
+
+// A thread's column constants as fp32: gain, and scale * post_gain * (a gate per channel), while its first rows are on
+// their way.  to_branch NULL: scale alone, which is not kept.
+template <int PLANE, bool POST>
+__device__ __forceinline__ void keep_columns(uint8_t* to_gain, uint8_t* to_branch, const Columns& c, int vec0,
+                                             const bool (&has)[kVpt]) {
+#pragma unroll
+    for (int v = 0; v < kVpt; ++v) {
+        if (!has[v]) continue;
+        const int i = vec0 + v * blockDim.x;
+        if (c.gain) keep8<PLANE>(to_gain, v, load8<kAny>(c.gain, i, c.gain_dtype));
+        if (!to_branch) continue;
+        Vec b = same8(c.scale);
+        if (POST) {
+            const Vec p = load8<kAny>(c.post, i, c.gain_dtype);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b.p[j] = mul2(b.p[j], p.p[j]);
+        }
+        if (c.gate.kind == GATE_CHANNEL) {
+            Vec f = load8<kAny>(c.gate.p, i, c.gate.dtype);
+            if (c.gate.sigmoid) f = sigmoid8(f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b.p[j] = mul2(b.p[j], f.p[j]);
+        }
+        keep8<PLANE>(to_branch, v, b);
+    }
+}
+
 // ---------------------------------------------------------------- host side
+constexpr size_t kSmemOfSm = 224 * 1024;
+
 inline bq_status check_desc(const char* name, const bq_residual_norm_desc* d, bool x) {
     if (!d) return bq::fail(BQ_ERR_NULL, "%s: desc is NULL", name);
     if (d->T < 0 || d->H < 8 || d->H % 8 || d->H > kMaxH)

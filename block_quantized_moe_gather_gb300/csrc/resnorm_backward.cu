@@ -16,12 +16,6 @@ namespace {
 using namespace bq;
 using namespace bq::resnorm;
 
-constexpr int kVpt = 2;   // vectors of a thread
-
-// Where a thread keeps its vectors of a row in flight: planes of 16 bytes per vector of the block (an fp32 vector takes
-// two), so that a warp's lie in distinct banks, and places that are constants.
-__host__ __device__ constexpr int planes(int dt) { return dt == BQ_DT_F16 || dt == BQ_DT_BF16 ? 1 : 2; }
-
 template <int DY, int DH, int DX, int THREADS>
 struct Stage {
     static constexpr int kPlane = THREADS * kVpt * 16;
@@ -42,45 +36,6 @@ struct BackwardArgs {
     int sum_gain, sum_branch;       // which array each is, or -1
 };
 
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-// A thread's vectors of a row into a stage.
-template <int DT, int PLANE>
-__device__ __forceinline__ void fetch(uint32_t dst, const uint8_t* src, int dtype, const bool (&has)[kVpt]) {
-    const bool wide = (DT == kAny ? dtype : DT) == BQ_DT_F32;
-#pragma unroll
-    for (int v = 0; v < kVpt; ++v) {
-        if (!has[v]) continue;
-        const uint8_t* p = src + v * (int)blockDim.x * (wide ? 32 : 16);
-        copy16_async(dst + v * (PLANE / kVpt), p);
-        if (wide) copy16_async(dst + v * (PLANE / kVpt) + PLANE, p + 16);
-    }
-}
-
-template <int DT, int PLANE>
-__device__ __forceinline__ Vec staged8(const uint8_t* at, int v, int dtype) {
-    const uint8_t* p = at + v * (PLANE / kVpt);
-    const uint4 lo = *reinterpret_cast<const uint4*>(p);
-    if ((DT == kAny ? dtype : DT) != BQ_DT_F32) return unpack8<DT>(lo, lo, dtype);
-    return unpack8<BQ_DT_F32>(lo, *reinterpret_cast<const uint4*>(p + PLANE), dtype);
-}
-
-template <int PLANE>
-__device__ __forceinline__ void keep8(uint8_t* at, int v, const Vec& x) {
-    uint8_t* p = at + v * (PLANE / kVpt);
-    *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(x.p[0], x.p[1]);
-    *reinterpret_cast<ulonglong2*>(p + PLANE) = make_ulonglong2(x.p[2], x.p[3]);
-}
-
-template <int PLANE>
-__device__ __forceinline__ Vec kept8(const uint8_t* at, int v) {
-    const uint8_t* p = at + v * (PLANE / kVpt);
-    const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(p), hi = *reinterpret_cast<const ulonglong2*>(p + PLANE);
-    return {{lo.x, lo.y, hi.x, hi.y}};
-}
-
 // blockDim.x threads take a row (or a cluster's slice of one), a thread the vectors x, x + blockDim.x of it;
 // blockDim.y rows at a time.  Blocks walk over the rows; a thread's columns stay the same, so it adds their column sums
 // in registers.  Each thread fetches the vectors that it will use itself, rows ahead, into shared memory of its own
@@ -93,8 +48,6 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
     constexpr int PLANE = L::kPlane;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ SumBuf s_buf;
-    bq::grid_dependency_wait();   // launched behind whatever precedes it on the stream
-    bq::allow_dependents();
     const Gate& gate = a.columns.gate;
     const bool has_x = a.dx.p != nullptr, full = gate.kind == GATE_FULL;
     const bool token = gate.kind == GATE_TOKEN && a.dgate.p;   // its gradient is wanted
@@ -110,8 +63,11 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
     const int o_y = offset(a.y), o_out = offset(a.out), o_dx = offset(a.dx), o_dout = offset(a.dout);
     const int o_dy = offset(a.dy), o_dh = offset(a.dh);
     const int end = L::kConstants + a.stages * a.stage_bytes;
-    for (int i = tid * 16; i < end; i += THREADS * 16) *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
     uint8_t* own = smem + tid * 16;
+    zero_missing<PLANE>(own, end, has);
+    // launched behind whatever precedes it on the stream: nothing before this line touches global memory
+    bq::grid_dependency_wait();
+    bq::allow_dependents();
     const uint32_t own_u32 = (uint32_t)__cvta_generic_to_shared(own);
     auto fetch_row = [&](int stage, int64_t r0) {
         const uint32_t to = own_u32 + stage;
@@ -136,25 +92,7 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
         ahead += a.stage_bytes;
         next += step;
     }
-#pragma unroll
-    for (int v = 0; v < kVpt; ++v) {   // the constants of the thread's columns, while its first rows are on their way
-        if (!has[v]) continue;
-        const int i = vec0 + v * blockDim.x;
-        if (has_x) keep8<PLANE>(own + L::kGain, v, load8<kAny>(a.columns.gain, i, a.columns.gain_dtype));
-        Vec b = same8(a.columns.scale);
-        if (POST) {
-            const Vec p = load8<kAny>(a.columns.post, i, a.columns.gain_dtype);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) b.p[j] = mul2(b.p[j], p.p[j]);
-        }
-        if (gate.kind == GATE_CHANNEL) {
-            Vec f = load8<kAny>(gate.p, i, gate.dtype);
-            if (gate.sigmoid) f = sigmoid8(f);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) b.p[j] = mul2(b.p[j], f.p[j]);
-        }
-        keep8<PLANE>(own + L::kBranch, v, b);
-    }
+    keep_columns<PLANE, POST>(own + L::kGain, own + L::kBranch, a.columns, vec0, has);
     Vec gain_sum[kVpt], branch[kVpt];
 #pragma unroll
     for (int v = 0; v < kVpt; ++v) gain_sum[v] = branch[v] = same8(0.f);
@@ -356,7 +294,6 @@ struct Shape {
 };
 
 constexpr int kMaxBlocks = 2 * kSms;
-constexpr size_t kSmemOfSm = 224 * 1024;
 
 // planes: of a row's vectors in a stage.
 Shape shape_of(int T, int H, int n_planes) {
