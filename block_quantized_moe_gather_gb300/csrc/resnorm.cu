@@ -19,8 +19,7 @@ using namespace bq::resnorm;
 struct ForwardArgs {
     int T, H;
     Rows y, h, out, x;              // x.p NULL: not computed
-    const uint8_t* full;            // a gate per value, and its rows
-    int64_t ld_full;
+    Rows full;                      // a gate per value
     Columns columns;
     float residual_scale, eps;
 };
@@ -39,7 +38,7 @@ residual_norm_kernel(const __grid_constant__ ForwardArgs a) {
     const int vecs = a.H / 8;
     bool has[VPT];
     Vec r[VPT], o[VPT];
-    const uint8_t *y = a.y.p + t * a.y.ld, *h = a.h.p + t * a.h.ld;
+    const uint8_t *y = a.y.row(t), *h = a.h.row(t);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         const int i = threadIdx.x + v * blockDim.x;
@@ -69,7 +68,7 @@ residual_norm_kernel(const __grid_constant__ ForwardArgs a) {
             for (int j = 0; j < 4; ++j) r[v].p[j] = mul2(r[v].p[j], p.p[j]);
         }
         if (gate.kind >= GATE_CHANNEL) {
-            Vec w = load8<kAny>(gate.kind == GATE_FULL ? a.full + t * a.ld_full : gate.p, i, gate.dtype);
+            Vec w = load8<kAny>(gate.kind == GATE_FULL ? a.full.row(t) : gate.p, i, gate.dtype);
             if (gate.sigmoid) w = sigmoid8(w);
 #pragma unroll
             for (int j = 0; j < 4; ++j) r[v].p[j] = mul2(r[v].p[j], w.p[j]);
@@ -79,7 +78,7 @@ residual_norm_kernel(const __grid_constant__ ForwardArgs a) {
             r[v].p[j] = fma2(r[v].p[j], both(f), mul2(o[v].p[j], both(a.residual_scale)));
             squares = fma2(r[v].p[j], r[v].p[j], squares);
         }
-        store8<DH>(a.out.p + t * a.out.ld, i, a.out.dtype, r[v]);
+        store8<DH>(a.out.row(t), i, a.out.dtype, r[v]);
     }
     if (!a.x.p) return;
     const float norm = rsqrtf(__fmaf_rn(row_sum(sum2(squares), s_buf, turn), inv_h, a.eps));
@@ -90,7 +89,7 @@ residual_norm_kernel(const __grid_constant__ ForwardArgs a) {
         const Vec c = load8<kAny>(a.columns.gain, i, a.columns.gain_dtype);
 #pragma unroll
         for (int j = 0; j < 4; ++j) r[v].p[j] = mul2(mul2(r[v].p[j], both(norm)), c.p[j]);
-        store8<DX>(a.x.p + t * a.x.ld, i, a.x.dtype, r[v]);
+        store8<DX>(a.x.row(t), i, a.x.dtype, r[v]);
     }
 }
 
@@ -101,10 +100,10 @@ struct ManyArgs {
     int stages, stage_bytes, at_stages, at_branch;   // bytes; at_branch -1: the branch's constant is scale alone
 };
 
-template <int DY, int DH, int DX, int THREADS, bool POST>
+template <int DY, int DH, int DX, int THREADS, int VPT, bool POST>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 residual_norm_many_kernel(const __grid_constant__ ManyArgs m) {
-    constexpr int PLANE = THREADS * kVpt * 16;
+    constexpr int PLANE = THREADS * VPT * 16;
     constexpr int kY = 0, kH = planes(DY) * PLANE, kFull = kH + planes(DH) * PLANE;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ SumBuf s_buf;
@@ -112,29 +111,26 @@ residual_norm_many_kernel(const __grid_constant__ ManyArgs m) {
     const Gate& gate = a.columns.gate;
     const bool full = gate.kind == GATE_FULL;
     const int vecs = a.H / 8, tid = threadIdx.y * blockDim.x + threadIdx.x;
-    bool has[kVpt];
+    bool has[VPT];
 #pragma unroll
-    for (int v = 0; v < kVpt; ++v) has[v] = (int)(threadIdx.x + v * blockDim.x) < vecs;
+    for (int v = 0; v < VPT; ++v) has[v] = (int)(threadIdx.x + v * blockDim.x) < vecs;
     const int64_t step = (int64_t)gridDim.x * blockDim.y, block0 = (int64_t)blockIdx.x * blockDim.y;
     const int end = m.at_stages + m.stages * m.stage_bytes;
     uint8_t* own = smem + tid * 16;
     zero_missing<PLANE>(own, end, has);
     const uint32_t own_u32 = (uint32_t)__cvta_generic_to_shared(own);
     // a thread's first vector in the rows of a block, from the block's first row on (the host made sure that it is an int)
-    auto offset = [&](int64_t ld, int dtype) {
-        return (int)threadIdx.y * (int)ld + (int)threadIdx.x * (dtype == BQ_DT_F32 ? 32 : 16);
-    };
-    const int o_y = offset(a.y.ld, a.y.dtype), o_h = offset(a.h.ld, a.h.dtype), o_full = offset(a.ld_full, gate.dtype);
-    const int o_out = offset(a.out.ld, a.out.dtype), o_x = offset(a.x.ld, a.x.dtype);
+    auto offset = [&](const Rows& r) { return (int)threadIdx.y * r.ld16 * 16 + (int)threadIdx.x * vec_bytes(r.dtype); };
+    const int o_y = offset(a.y), o_h = offset(a.h), o_full = offset(a.full), o_out = offset(a.out), o_x = offset(a.x);
     // launched behind whatever precedes it on the stream: nothing before this line touches global memory
     bq::grid_dependency_wait();
     bq::allow_dependents();
     auto fetch_row = [&](int stage, int64_t r0) {
         const uint32_t to = own_u32 + stage;
         if (r0 + threadIdx.y < a.T) {
-            fetch<DY, PLANE>(to + kY, a.y.p + r0 * a.y.ld + o_y, a.y.dtype, has);
-            fetch<DH, PLANE>(to + kH, a.h.p + r0 * a.h.ld + o_h, a.h.dtype, has);
-            if (full) fetch<kAny, PLANE>(to + kFull, a.full + r0 * a.ld_full + o_full, gate.dtype, has);
+            fetch<DY, PLANE>(to + kY, a.y.row(r0) + o_y, a.y.dtype, has);
+            fetch<DH, PLANE>(to + kH, a.h.row(r0) + o_h, a.h.dtype, has);
+            if (full) fetch<DY, PLANE>(to + kFull, a.full.row(r0) + o_full, gate.dtype, has);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -161,29 +157,29 @@ residual_norm_many_kernel(const __grid_constant__ ManyArgs m) {
         stage = stage + m.stage_bytes == end ? m.at_stages : stage + m.stage_bytes;
         float f = token_factor(gate, t, live);
         if (!branch) f *= a.columns.scale;
-        Vec r[kVpt];
+        Vec r[VPT];
 #pragma unroll
-        for (int v = 0; v < kVpt; ++v) r[v] = staged8<DY, PLANE>(st + kY, v, a.y.dtype);
+        for (int v = 0; v < VPT; ++v) r[v] = staged8<DY, PLANE, VPT>(st + kY, v, a.y.dtype);
         if (POST) {
             f32x2 squares = both(0.f);
 #pragma unroll
-            for (int v = 0; v < kVpt; ++v)
+            for (int v = 0; v < VPT; ++v)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) squares = fma2(r[v].p[j], r[v].p[j], squares);
             f *= rsqrtf(__fmaf_rn(row_sum(sum2(squares), s_buf, turn), inv_h, a.eps));
         }
         f32x2 squares = both(0.f);
-        uint8_t* to_out = a.out.p + t0 * a.out.ld + o_out;
+        uint8_t* to_out = a.out.row(t0) + o_out;
 #pragma unroll
-        for (int v = 0; v < kVpt; ++v) {
-            const Vec o = staged8<DH, PLANE>(st + kH, v, a.h.dtype);
+        for (int v = 0; v < VPT; ++v) {
+            const Vec o = staged8<DH, PLANE, VPT>(st + kH, v, a.h.dtype);
             if (branch) {
-                const Vec c = kept8<PLANE>(own + m.at_branch, v);
+                const Vec c = kept8<PLANE, VPT>(own + m.at_branch, v);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) r[v].p[j] = mul2(r[v].p[j], c.p[j]);
             }
             if (full) {
-                Vec w = staged8<kAny, PLANE>(st + kFull, v, gate.dtype);
+                Vec w = staged8<DY, PLANE, VPT>(st + kFull, v, gate.dtype);
                 if (gate.sigmoid) w = sigmoid8(w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) r[v].p[j] = mul2(r[v].p[j], w.p[j]);
@@ -197,10 +193,10 @@ residual_norm_many_kernel(const __grid_constant__ ManyArgs m) {
         }
         if (!a.x.p) continue;
         const float norm = rsqrtf(__fmaf_rn(row_sum(sum2(squares), s_buf, turn), inv_h, a.eps));
-        uint8_t* to_x = a.x.p + t0 * a.x.ld + o_x;
+        uint8_t* to_x = a.x.row(t0) + o_x;
 #pragma unroll
-        for (int v = 0; v < kVpt; ++v) {
-            const Vec c = kept8<PLANE>(own, v);
+        for (int v = 0; v < VPT; ++v) {
+            const Vec c = kept8<PLANE, VPT>(own, v);
 #pragma unroll
             for (int j = 0; j < 4; ++j) r[v].p[j] = mul2(mul2(r[v].p[j], both(norm)), c.p[j]);
             if (live && has[v]) store8<DX>(to_x, v * blockDim.x, a.x.dtype, r[v]);
@@ -231,16 +227,18 @@ extern "C" bq_status bq_residual_norm(const bq_residual_norm_desc* d, const void
     bq_status s = check_desc(name, d, x != nullptr);
     if (s != BQ_OK || d->T == 0) return s;
     const int ys = bq::dtype_size(d->y_dtype), hs = bq::dtype_size(d->h_dtype);
-    if ((s = bq::check_rows(name, "y", y, d->H, ldy, ys)) != BQ_OK ||
-        (s = bq::check_rows(name, "h", h, d->H, ldh, hs)) != BQ_OK ||
-        (s = bq::check_rows(name, "h_out", h_out, d->H, ldho, hs)) != BQ_OK)
+    if ((s = check_matrix(name, "y", y, d->H, ldy, ys)) != BQ_OK ||
+        (s = check_matrix(name, "h", h, d->H, ldh, hs)) != BQ_OK ||
+        (s = check_matrix(name, "h_out", h_out, d->H, ldho, hs)) != BQ_OK)
         return s;
-    if (x && (s = bq::check_rows(name, "x", x, d->H, ldx, bq::dtype_size(d->x_dtype))) != BQ_OK) return s;
+    if (x && (s = check_matrix(name, "x", x, d->H, ldx, bq::dtype_size(d->x_dtype))) != BQ_OK) return s;
     if ((s = bq::check_arch()) != BQ_OK) return s;
     const int32_t x_dtype = x ? d->x_dtype : d->h_dtype;
+    const bool full_gate = d->gate_kind == BQ_GATE_FULL;
+    const int32_t full_dtype = full_gate ? d->gate_dtype : d->y_dtype;
     const ForwardArgs a{d->T, d->H, rows(y, ldy, d->y_dtype), rows(h, ldh, d->h_dtype), rows(h_out, ldho, d->h_dtype),
-                        rows(x, ldx, x_dtype), static_cast<const uint8_t*>(d->gate),
-                        d->ldgate * bq::dtype_size(d->gate_dtype), columns_of(d, x != nullptr), d->residual_scale, d->eps};
+                        rows(x, ldx, x_dtype), full_gate ? rows(d->gate, d->ldgate, d->gate_dtype) : Rows{},
+                        columns_of(d, x != nullptr), d->residual_scale, d->eps};
     // Threads of a row: for few rows a vector each, as far as 512 threads go; for many two, so that what a row costs a
     // warp beside its vectors is shared.
     const int vecs = d->H / 8;
@@ -248,32 +246,35 @@ extern "C" bq_status bq_residual_norm(const bq_residual_norm_desc* d, const void
     const int threads = ((vecs + per - 1) / per + 31) / 32 * 32, per_cta = std::max(1, 256 / threads);
     const dim3 grid((unsigned)(((int64_t)d->T + per_cta - 1) / per_cta)), block(threads, per_cta);
     cudaError_t e = cudaSuccess;
-    // many rows, of which a block of 256 or 512 threads holds one or more
-    const int wide_block = vecs > 256 * kVpt ? 512 : 256;
-    const int64_t far = std::max({a.y.ld, a.h.ld, a.out.ld, a.x.ld, a.ld_full});
-    if (d->T > 2 * kSms && vecs <= 512 * kVpt && far <= INT32_MAX / 16) {
-        with_types(d->y_dtype, d->h_dtype, x_dtype, [&](auto type) {
+    // many rows, of which a block of 256 or 512 threads holds one or more; two vectors a thread where one does not do
+    const int wide_block = vecs > 512 ? 512 : 256, vpt = vecs > 256 ? 2 : 1;
+    const int far = std::max({a.y.ld16, a.h.ld16, a.out.ld16, a.x.ld16, a.full.ld16});
+    if (d->T > 2 * kSms && vecs <= 1024 && far <= INT32_MAX / 256) {   // offsets inside a block's rows are ints
+        with_types(d->y_dtype, d->h_dtype, x_dtype, full_dtype, [&](auto type) {
             using D = decltype(type);
             const bool branch = d->post_gain || d->gate_kind == BQ_GATE_CHANNEL;
-            const int plane = wide_block * kVpt * 16, full = d->gate_kind == BQ_GATE_FULL ? planes(d->gate_dtype) : 0;
+            const int plane = wide_block * vpt * 16, full = full_gate ? planes(D::y) : 0;
             ManyArgs m{a, 2, (planes(D::y) + planes(D::h) + full) * plane, (branch ? 4 : 2) * plane, branch ? 2 * plane : -1};
             auto smem = [&] { return (size_t)m.at_stages + (size_t)m.stages * m.stage_bytes; };
-            const int per_sm = (int)std::max<size_t>(1, std::min<size_t>(1024 / wide_block, kSmemOfSm / smem()));
-            if (smem() + m.stage_bytes <= kSmemOfSm / per_sm) m.stages = 3;
-            const int x_threads = ((vecs + kVpt - 1) / kVpt + 31) / 32 * 32, row_groups = std::max(1, wide_block / x_threads);
+            const int per_sm = (int)std::max<size_t>(1, std::min<size_t>(1024 / wide_block, kSmemOfSm / (smem() + 2048)));
+            if (smem() + m.stage_bytes + 2048 <= kSmemOfSm / per_sm) m.stages = 3;
+            const int x_threads = ((vecs + vpt - 1) / vpt + 31) / 32 * 32, row_groups = std::max(1, wide_block / x_threads);
             const int64_t blocks = std::min<int64_t>(kSms * per_sm, ((int64_t)d->T + row_groups - 1) / row_groups);
             const dim3 g((unsigned)blocks), b(x_threads, row_groups);
             cudaStream_t st = (cudaStream_t)stream;
-            if (wide_block == 256)
-                e = d->post_gain ? launch_many<residual_norm_many_kernel<D::y, D::h, D::x, 256, true>>(m, g, b, smem(), st)
-                                 : launch_many<residual_norm_many_kernel<D::y, D::h, D::x, 256, false>>(m, g, b, smem(), st);
-            else
-                e = d->post_gain ? launch_many<residual_norm_many_kernel<D::y, D::h, D::x, 512, true>>(m, g, b, smem(), st)
-                                 : launch_many<residual_norm_many_kernel<D::y, D::h, D::x, 512, false>>(m, g, b, smem(), st);
+            auto go = [&](auto post) {
+                constexpr bool POST = decltype(post)::value;
+                if (vpt == 1) e = launch_many<residual_norm_many_kernel<D::y, D::h, D::x, 256, 1, POST>>(m, g, b, smem(), st);
+                else if (wide_block == 256)
+                    e = launch_many<residual_norm_many_kernel<D::y, D::h, D::x, 256, 2, POST>>(m, g, b, smem(), st);
+                else e = launch_many<residual_norm_many_kernel<D::y, D::h, D::x, 512, 2, POST>>(m, g, b, smem(), st);
+            };
+            if (d->post_gain) go(std::true_type());
+            else go(std::false_type());
         });
         return launched(name, e);
     }
-    with_types(d->y_dtype, d->h_dtype, x_dtype, [&](auto type) {
+    with_types(d->y_dtype, d->h_dtype, x_dtype, full_dtype, [&](auto type) {
         using D = decltype(type);
         auto go = [&](auto kernel) { e = bq::launch_after(kernel, grid, block, 0, (cudaStream_t)stream, a); };
         if (d->post_gain) {

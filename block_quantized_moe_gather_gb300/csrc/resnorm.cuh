@@ -19,14 +19,18 @@ enum { GATE_NONE = BQ_GATE_NONE, GATE_TOKEN = BQ_GATE_TOKEN, GATE_CHANNEL = BQ_G
 
 struct Rows {
     uint8_t* p;
-    int64_t ld;    // bytes
+    int ld16;      // from row to row, in units of 16 bytes: a product with a row number takes one instruction
     int dtype;
+
+    __device__ __forceinline__ uint8_t* row(int64_t t) const { return p + ((int64_t)(int)t * ld16) * 16; }
 };
 
 struct Gate {
     const uint8_t* p;
     int dtype, kind, sigmoid;
 };
+
+__host__ __device__ __forceinline__ int vec_bytes(int dtype) { return dtype == BQ_DT_F32 ? 32 : 16; }   // of eight values
 
 // Eight values of a row, in pairs: without the packed instructions these kernels would be bound by issue.
 struct Vec {
@@ -89,7 +93,14 @@ __device__ __forceinline__ float load1(const uint8_t* p, int64_t i, int dtype) {
     return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
 }
 
-__device__ __forceinline__ float sigmoid_f(float v) { return __fdividef(1.f, 1.f + expf(-v)); }
+// By the special-function unit's exp2 and reciprocal, off by 2 units in the last place each; the exponent's argument
+// adds |v| units to the exponential.
+__device__ __forceinline__ float sigmoid_f(float v) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * v));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
 
 __device__ __forceinline__ Vec sigmoid8(const Vec& v) {
     Vec r;
@@ -156,6 +167,26 @@ __device__ __forceinline__ float row_sum(float v, SumBuf& buf, int& turn) {
     return v;
 }
 
+// Two sums, the same way: a lane holds one of them after the first exchange.
+__device__ __forceinline__ void row_sums(float& v0, float& v1, SumBuf& buf, int& turn) {
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const bool upper = lane & 16;
+    float t = (upper ? v1 : v0) + __shfl_xor_sync(0xffffffffu, upper ? v0 : v1, 16);
+#pragma unroll
+    for (int off = 8; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+    if (warps > 1) {
+        float (*mine)[8] = buf.warp[turn] + threadIdx.y * warps;
+        if ((lane & 15) == 0) mine[threadIdx.x >> 5][lane >> 4] = t;
+        __syncthreads();
+        t = (lane & 15) < warps ? mine[lane & 15][lane >> 4] : 0.f;
+#pragma unroll
+        for (int off = 8; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+        turn ^= 1;
+    }
+    v0 = __shfl_sync(0xffffffffu, t, 0);
+    v1 = __shfl_sync(0xffffffffu, t, 16);
+}
+
 // Eight sums at once, of a row that a cluster's CTAs may share.  Three steps halve the sums that a lane holds while
 // they double the lanes added (7 exchanges instead of 24), and the warps' sums are added with a sum a lane.
 template <bool CLUSTER>
@@ -199,10 +230,8 @@ __device__ __forceinline__ void row_sums(float (&v)[8], SumBuf& buf, int& turn, 
 // ---------------------------------------------------------------- rows in flight
 // Each thread fetches the vectors that it will use itself, rows ahead, into shared memory of its own (cp.async): the
 // loads need no registers while they are in flight, and no barrier when they land.
-constexpr int kVpt = 2;   // vectors of a thread
-
-// Where a thread keeps its vectors of a row in flight: planes of 16 bytes per vector of the block (an fp32 vector takes
-// two), so that a warp's lie in distinct banks, and places that are constants.
+// Where a thread keeps its VPT vectors of a row in flight: planes of 16 bytes per vector of the block (an fp32 vector
+// takes two), so that a warp's lie in distinct banks, and places that are constants.
 __host__ __device__ constexpr int planes(int dt) { return dt == BQ_DT_F16 || dt == BQ_DT_BF16 ? 1 : 2; }
 
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
@@ -210,60 +239,60 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
 }
 
 // A thread's vectors of a row into a stage.
-template <int DT, int PLANE>
-__device__ __forceinline__ void fetch(uint32_t dst, const uint8_t* src, int dtype, const bool (&has)[kVpt]) {
+template <int DT, int PLANE, int VPT>
+__device__ __forceinline__ void fetch(uint32_t dst, const uint8_t* src, int dtype, const bool (&has)[VPT]) {
     const bool wide = (DT == kAny ? dtype : DT) == BQ_DT_F32;
 #pragma unroll
-    for (int v = 0; v < kVpt; ++v) {
+    for (int v = 0; v < VPT; ++v) {
         if (!has[v]) continue;
         const uint8_t* p = src + v * (int)blockDim.x * (wide ? 32 : 16);
-        copy16_async(dst + v * (PLANE / kVpt), p);
-        if (wide) copy16_async(dst + v * (PLANE / kVpt) + PLANE, p + 16);
+        copy16_async(dst + v * (PLANE / VPT), p);
+        if (wide) copy16_async(dst + v * (PLANE / VPT) + PLANE, p + 16);
     }
 }
 
-template <int DT, int PLANE>
+template <int DT, int PLANE, int VPT>
 __device__ __forceinline__ Vec staged8(const uint8_t* at, int v, int dtype) {
-    const uint8_t* p = at + v * (PLANE / kVpt);
+    const uint8_t* p = at + v * (PLANE / VPT);
     const uint4 lo = *reinterpret_cast<const uint4*>(p);
     if ((DT == kAny ? dtype : DT) != BQ_DT_F32) return unpack8<DT>(lo, lo, dtype);
     return unpack8<BQ_DT_F32>(lo, *reinterpret_cast<const uint4*>(p + PLANE), dtype);
 }
 
-template <int PLANE>
+template <int PLANE, int VPT>
 __device__ __forceinline__ void keep8(uint8_t* at, int v, const Vec& x) {
-    uint8_t* p = at + v * (PLANE / kVpt);
+    uint8_t* p = at + v * (PLANE / VPT);
     *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(x.p[0], x.p[1]);
     *reinterpret_cast<ulonglong2*>(p + PLANE) = make_ulonglong2(x.p[2], x.p[3]);
 }
 
-template <int PLANE>
+template <int PLANE, int VPT>
 __device__ __forceinline__ Vec kept8(const uint8_t* at, int v) {
-    const uint8_t* p = at + v * (PLANE / kVpt);
+    const uint8_t* p = at + v * (PLANE / VPT);
     const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(p), hi = *reinterpret_cast<const ulonglong2*>(p + PLANE);
     return {{lo.x, lo.y, hi.x, hi.y}};
 }
 
 // Zeros in a thread's places of vectors that it does not have, up to `end` bytes.
-template <int PLANE>
-__device__ __forceinline__ void zero_missing(uint8_t* own, int end, const bool (&has)[kVpt]) {
+template <int PLANE, int VPT>
+__device__ __forceinline__ void zero_missing(uint8_t* own, int end, const bool (&has)[VPT]) {
 #pragma unroll
-    for (int v = 0; v < kVpt; ++v) {
+    for (int v = 0; v < VPT; ++v) {
         if (has[v]) continue;
-        for (int i = v * (PLANE / kVpt); i < end; i += PLANE) *reinterpret_cast<uint4*>(own + i) = make_uint4(0, 0, 0, 0);
+        for (int i = v * (PLANE / VPT); i < end; i += PLANE) *reinterpret_cast<uint4*>(own + i) = make_uint4(0, 0, 0, 0);
     }
 }
 
 // A thread's column constants as fp32: gain, and scale * post_gain * (a gate per channel), while its first rows are on
 // their way.  to_branch NULL: scale alone, which is not kept.
-template <int PLANE, bool POST>
+template <int PLANE, bool POST, int VPT>
 __device__ __forceinline__ void keep_columns(uint8_t* to_gain, uint8_t* to_branch, const Columns& c, int vec0,
-                                             const bool (&has)[kVpt]) {
+                                             const bool (&has)[VPT]) {
 #pragma unroll
-    for (int v = 0; v < kVpt; ++v) {
+    for (int v = 0; v < VPT; ++v) {
         if (!has[v]) continue;
         const int i = vec0 + v * blockDim.x;
-        if (c.gain) keep8<PLANE>(to_gain, v, load8<kAny>(c.gain, i, c.gain_dtype));
+        if (c.gain) keep8<PLANE, VPT>(to_gain, v, load8<kAny>(c.gain, i, c.gain_dtype));
         if (!to_branch) continue;
         Vec b = same8(c.scale);
         if (POST) {
@@ -277,12 +306,20 @@ __device__ __forceinline__ void keep_columns(uint8_t* to_gain, uint8_t* to_branc
 #pragma unroll
             for (int j = 0; j < 4; ++j) b.p[j] = mul2(b.p[j], f.p[j]);
         }
-        keep8<PLANE>(to_branch, v, b);
+        keep8<PLANE, VPT>(to_branch, v, b);
     }
 }
 
 // ---------------------------------------------------------------- host side
 constexpr size_t kSmemOfSm = 224 * 1024;
+
+// Rows as check_rows, not further apart than Rows can say.
+inline bq_status check_matrix(const char* name, const char* what, const void* p, int cols, int64_t ld, int es) {
+    const bq_status s = bq::check_rows(name, what, p, cols, ld, es);
+    if (s == BQ_OK && ld * es / 16 > INT32_MAX)
+        return bq::fail(BQ_ERR_SHAPE, "%s: rows of %s are %lld elements apart", name, what, (long long)ld);
+    return s;
+}
 
 inline bq_status check_desc(const char* name, const bq_residual_norm_desc* d, bool x) {
     if (!d) return bq::fail(BQ_ERR_NULL, "%s: desc is NULL", name);
@@ -306,14 +343,14 @@ inline bq_status check_desc(const char* name, const bq_residual_norm_desc* d, bo
         return bq::fail(BQ_ERR_ALIGN, "%s: gains must be 16-byte aligned", name);
     if (!gated) return BQ_OK;
     const int es = bq::dtype_size(d->gate_dtype);
-    if (d->gate_kind == BQ_GATE_FULL) return bq::check_rows(name, "gate", d->gate, d->H, d->ldgate, es);
+    if (d->gate_kind == BQ_GATE_FULL) return check_matrix(name, "gate", d->gate, d->H, d->ldgate, es);
     if (!bq::aligned(d->gate, d->gate_kind == BQ_GATE_CHANNEL ? 16 : es))
         return bq::fail(BQ_ERR_ALIGN, "%s: the gate is not aligned", name);
     return BQ_OK;
 }
 
 inline Rows rows(const void* p, int64_t ld, int32_t dtype) {
-    return {static_cast<uint8_t*>(const_cast<void*>(p)), ld * bq::dtype_size(dtype), dtype};
+    return {static_cast<uint8_t*>(const_cast<void*>(p)), (int)(ld * bq::dtype_size(dtype) / 16), dtype};
 }
 
 inline Columns columns_of(const bq_residual_norm_desc* d, bool x) {
@@ -328,11 +365,13 @@ struct Types {
 };
 
 // Calls f with the row types as constants: one type for all, a 16-bit type with an fp32 block output (as this
-// library's MoE layer leaves it) or with an fp32 stream; other mixes read their types from the arguments.
+// library's MoE layer leaves it) or with an fp32 stream, and a gate per value (if there is one) of y's type; other mixes
+// read their types from the arguments.
 template <typename F>
-void with_types(int y, int h, int x, F f) {
+void with_types(int y, int h, int x, int gate, F f) {
     constexpr int F32 = BQ_DT_F32, F16 = BQ_DT_F16, BF16 = BQ_DT_BF16;
-    if (y == F32 && h == F32 && x == F32) f(Types<F32, F32, F32>());
+    if (gate != y) f(Types<kAny, kAny, kAny>());
+    else if (y == F32 && h == F32 && x == F32) f(Types<F32, F32, F32>());
     else if (y == F16 && h == F16 && x == F16) f(Types<F16, F16, F16>());
     else if (y == BF16 && h == BF16 && x == BF16) f(Types<BF16, BF16, BF16>());
     else if (y == F32 && h == F16 && x == F16) f(Types<F32, F16, F16>());

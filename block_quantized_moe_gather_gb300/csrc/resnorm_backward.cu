@@ -16,17 +16,17 @@ namespace {
 using namespace bq;
 using namespace bq::resnorm;
 
-template <int DY, int DH, int DX, int THREADS>
+template <int DY, int DH, int DX, int THREADS, int VPT>
 struct Stage {
-    static constexpr int kPlane = THREADS * kVpt * 16;
+    static constexpr int kPlane = THREADS * VPT * 16;
     static constexpr int kY = 0, kOut = kY + planes(DY) * kPlane, kDx = kOut + planes(DH) * kPlane;
-    static constexpr int kDout = kDx + planes(DX) * kPlane, kGate = kDout + planes(DH) * kPlane;   // two planes more
-    static constexpr int kGain = 0, kBranch = 2 * kPlane, kConstants = 4 * kPlane;   // fp32, in front of the stages
+    static constexpr int kDout = kDx + planes(DX) * kPlane, kGate = kDout + planes(DH) * kPlane;   // last
+    static constexpr int kGain = 0, kBranch = 2 * kPlane;   // constants, fp32, in front of the stages
 };
 
 struct BackwardArgs {
     int T, H, slice;                // slice: vectors of a row in this CTA (a cluster shares a row)
-    int stages, stage_bytes;
+    int stages, stage_bytes, at_stages;   // bytes
     Rows y, out, dout, dx;          // dout.p or dx.p NULL: no gradient comes that way
     Rows dy, dh;
     Columns columns;
@@ -41,28 +41,29 @@ struct BackwardArgs {
 // in registers.  Each thread fetches the vectors that it will use itself, rows ahead, into shared memory of its own
 // (cp.async): the loads need no registers while they are in flight, and no barrier when they land.  A vector behind the
 // row's last, and a row behind the last, is zeros there: the arithmetic goes over all alike.
-template <int DY, int DH, int DX, int THREADS, bool POST, bool CLUSTER>
+template <int DY, int DH, int DX, int THREADS, int VPT, bool POST, bool CLUSTER>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS)
 residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
-    using L = Stage<DY, DH, DX, THREADS>;
+    using L = Stage<DY, DH, DX, THREADS, VPT>;
     constexpr int PLANE = L::kPlane;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ SumBuf s_buf;
     const Gate& gate = a.columns.gate;
     const bool has_x = a.dx.p != nullptr, full = gate.kind == GATE_FULL;
+    const bool branch_kept = POST || gate.kind == GATE_CHANNEL;   // else its constant is scale alone
     const bool token = gate.kind == GATE_TOKEN && a.dgate.p;   // its gradient is wanted
     const int vecs = a.H / 8, tid = threadIdx.y * blockDim.x + threadIdx.x;
     const int ranks = CLUSTER ? (vecs + a.slice - 1) / a.slice : 1, rank = CLUSTER ? (int)cluster_rank() : 0;
     const int mine = min(a.slice, vecs - rank * a.slice), vec0 = rank * a.slice + threadIdx.x;
-    bool has[kVpt];
+    bool has[VPT];
 #pragma unroll
-    for (int v = 0; v < kVpt; ++v) has[v] = (int)(threadIdx.x + v * blockDim.x) < mine;
+    for (int v = 0; v < VPT; ++v) has[v] = (int)(threadIdx.x + v * blockDim.x) < mine;
     const int64_t step = (int64_t)(gridDim.x / ranks) * blockDim.y, block0 = (int64_t)(blockIdx.x / ranks) * blockDim.y;
     // a thread's first vector in the rows of a block, from the block's first row on (the host made sure that it is an int)
-    auto offset = [&](const Rows& m) { return (int)threadIdx.y * (int)m.ld + vec0 * (m.dtype == BQ_DT_F32 ? 32 : 16); };
+    auto offset = [&](const Rows& m) { return (int)threadIdx.y * m.ld16 * 16 + vec0 * vec_bytes(m.dtype); };
     const int o_y = offset(a.y), o_out = offset(a.out), o_dx = offset(a.dx), o_dout = offset(a.dout);
     const int o_dy = offset(a.dy), o_dh = offset(a.dh);
-    const int end = L::kConstants + a.stages * a.stage_bytes;
+    const int end = a.at_stages + a.stages * a.stage_bytes;
     uint8_t* own = smem + tid * 16;
     zero_missing<PLANE>(own, end, has);
     // launched behind whatever precedes it on the stream: nothing before this line touches global memory
@@ -72,32 +73,32 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
     auto fetch_row = [&](int stage, int64_t r0) {
         const uint32_t to = own_u32 + stage;
         if (r0 + threadIdx.y < a.T) {
-            fetch<DY, PLANE>(to + L::kY, a.y.p + r0 * a.y.ld + o_y, a.y.dtype, has);
+            fetch<DY, PLANE>(to + L::kY, a.y.row(r0) + o_y, a.y.dtype, has);
             if (has_x) {
-                fetch<DH, PLANE>(to + L::kOut, a.out.p + r0 * a.out.ld + o_out, a.out.dtype, has);
-                fetch<DX, PLANE>(to + L::kDx, a.dx.p + r0 * a.dx.ld + o_dx, a.dx.dtype, has);
+                fetch<DH, PLANE>(to + L::kOut, a.out.row(r0) + o_out, a.out.dtype, has);
+                fetch<DX, PLANE>(to + L::kDx, a.dx.row(r0) + o_dx, a.dx.dtype, has);
             }
-            if (a.dout.p) fetch<DH, PLANE>(to + L::kDout, a.dout.p + r0 * a.dout.ld + o_dout, a.dout.dtype, has);
-            if (full) fetch<kAny, PLANE>(to + L::kGate, a.full.p + r0 * a.full.ld + offset(a.full), a.full.dtype, has);
+            if (a.dout.p) fetch<DH, PLANE>(to + L::kDout, a.dout.row(r0) + o_dout, a.dout.dtype, has);
+            if (full) fetch<DY, PLANE>(to + L::kGate, a.full.row(r0) + offset(a.full), a.full.dtype, has);
         } else if (r0 < a.T) {
-            for (int i = 0; i < a.stage_bytes; i += PLANE / kVpt)
+            for (int i = 0; i < a.stage_bytes; i += PLANE / VPT)
                 *reinterpret_cast<uint4*>(own + stage + i) = make_uint4(0, 0, 0, 0);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    int ahead = L::kConstants;
+    int ahead = a.at_stages;
     int64_t next = block0;
     for (int i = 0; i < a.stages - 1; ++i) {
         fetch_row(ahead, next);
         ahead += a.stage_bytes;
         next += step;
     }
-    keep_columns<PLANE, POST>(own + L::kGain, own + L::kBranch, a.columns, vec0, has);
-    Vec gain_sum[kVpt], branch[kVpt];
+    keep_columns<PLANE, POST>(own + L::kGain, branch_kept ? own + L::kBranch : nullptr, a.columns, vec0, has);
+    Vec gain_sum[VPT], branch[VPT];
 #pragma unroll
-    for (int v = 0; v < kVpt; ++v) gain_sum[v] = branch[v] = same8(0.f);
+    for (int v = 0; v < VPT; ++v) gain_sum[v] = branch[v] = same8(0.f);
     const float inv_h = 1.f / (float)a.H;
-    int stage = L::kConstants, turn = 0;
+    int stage = a.at_stages, turn = 0;
     for (int64_t t0 = block0; t0 < a.T; t0 += step) {
         const int64_t t = t0 + threadIdx.y;
         const bool live = t < a.T;
@@ -105,19 +106,19 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
         else asm volatile("cp.async.wait_group 1;" ::: "memory");
         fetch_row(ahead, next);
         next += step;
-        ahead = ahead + a.stage_bytes == end ? L::kConstants : ahead + a.stage_bytes;
+        ahead = ahead + a.stage_bytes == end ? a.at_stages : ahead + a.stage_bytes;
         const uint8_t* st = own + stage;
-        stage = stage + a.stage_bytes == end ? L::kConstants : stage + a.stage_bytes;
+        stage = stage + a.stage_bytes == end ? a.at_stages : stage + a.stage_bytes;
         const float f = token_factor(gate, t, live);
         // sums over the row: h'^2, gain dx h', y^2, and P w y times dh', gain dx and h'
         f32x2 hh = both(0.f), dh = both(0.f), yy = both(0.f), in_dout = both(0.f), in_dx = both(0.f), in_h = both(0.f);
 #pragma unroll
-        for (int v = 0; v < kVpt; ++v) {
+        for (int v = 0; v < VPT; ++v) {
             Vec h, q;   // h', gain dx
             if (has_x) {
-                h = staged8<DH, PLANE>(st + L::kOut, v, a.out.dtype);
-                const Vec d = staged8<DX, PLANE>(st + L::kDx, v, a.dx.dtype);
-                q = kept8<PLANE>(own + L::kGain, v);
+                h = staged8<DH, PLANE, VPT>(st + L::kOut, v, a.out.dtype);
+                const Vec d = staged8<DX, PLANE, VPT>(st + L::kDx, v, a.dx.dtype);
+                q = kept8<PLANE, VPT>(own + L::kGain, v);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     q.p[j] = mul2(d.p[j], q.p[j]);
@@ -126,10 +127,10 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
                 }
             }
             if (!POST && !token) continue;
-            const Vec y = staged8<DY, PLANE>(st + L::kY, v, a.y.dtype);
-            Vec p = kept8<PLANE>(own + L::kBranch, v);
+            const Vec y = staged8<DY, PLANE, VPT>(st + L::kY, v, a.y.dtype);
+            Vec p = branch_kept ? kept8<PLANE, VPT>(own + L::kBranch, v) : same8(a.columns.scale);
             if (full) {
-                Vec w = staged8<kAny, PLANE>(st + L::kGate, v, a.full.dtype);
+                Vec w = staged8<DY, PLANE, VPT>(st + L::kGate, v, a.full.dtype);
                 if (gate.sigmoid) w = sigmoid8(w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) p.p[j] = mul2(p.p[j], w.p[j]);
@@ -147,13 +148,14 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
                 }
             }
             if (a.dout.p) {
-                const Vec o = staged8<DH, PLANE>(st + L::kDout, v, a.dout.dtype);
+                const Vec o = staged8<DH, PLANE, VPT>(st + L::kDout, v, a.dout.dtype);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) in_dout = fma2(p.p[j], o.p[j], in_dout);
             }
         }
         float sums[8] = {sum2(hh), sum2(dh), sum2(yy), sum2(in_dout), sum2(in_dx), sum2(in_h), 0.f, 0.f};
-        if (has_x || POST || token) row_sums<CLUSTER>(sums, s_buf, turn, ranks);
+        if (CLUSTER || POST || token) row_sums<CLUSTER>(sums, s_buf, turn, ranks);
+        else if (has_x) row_sums(sums[0], sums[1], s_buf, turn);
         // a row behind the last has sums of 0, whose roots would be infinite without eps
         const float r = live ? rsqrtf(__fmaf_rn(sums[0], inv_h, a.eps)) : 0.f, c = -r * r * r * (sums[1] * inv_h);
         const float s = !POST ? 1.f : live ? rsqrtf(__fmaf_rn(sums[2], inv_h, a.eps)) : 0.f;
@@ -162,15 +164,15 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
         if (token && live && threadIdx.x == 0 && rank == 0)
             reinterpret_cast<float*>(a.dgate.p)[t] = s * inner * (gate.sigmoid ? f * (1.f - f) : 1.f);
         const float fs = f * s, cy = -fs * s * s * (inner * inv_h);
-        uint8_t* to_dh = a.dh.p + t0 * a.dh.ld + o_dh;
-        uint8_t* to_dy = a.dy.p + t0 * a.dy.ld + o_dy;
+        uint8_t* to_dh = a.dh.row(t0) + o_dh;
+        uint8_t* to_dy = a.dy.row(t0) + o_dy;
 #pragma unroll
-        for (int v = 0; v < kVpt; ++v) {
+        for (int v = 0; v < VPT; ++v) {
             const bool stored = live && has[v];
-            Vec G = a.dout.p ? staged8<DH, PLANE>(st + L::kDout, v, a.dout.dtype) : same8(0.f);
+            Vec G = a.dout.p ? staged8<DH, PLANE, VPT>(st + L::kDout, v, a.dout.dtype) : same8(0.f);
             if (has_x) {
-                const Vec k = kept8<PLANE>(own + L::kGain, v), h = staged8<DH, PLANE>(st + L::kOut, v, a.out.dtype);
-                const Vec d = staged8<DX, PLANE>(st + L::kDx, v, a.dx.dtype);
+                const Vec k = kept8<PLANE, VPT>(own + L::kGain, v), h = staged8<DH, PLANE, VPT>(st + L::kOut, v, a.out.dtype);
+                const Vec d = staged8<DX, PLANE, VPT>(st + L::kDx, v, a.dx.dtype);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const f32x2 dr = mul2(d.p[j], both(r));
@@ -184,9 +186,9 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
                 for (int j = 0; j < 4; ++j) o.p[j] = mul2(G.p[j], both(a.residual_scale));
                 store8<DH>(to_dh, v * blockDim.x, a.dh.dtype, o);
             }
-            const Vec p = kept8<PLANE>(own + L::kBranch, v), y = staged8<DY, PLANE>(st + L::kY, v, a.y.dtype);
+            const Vec p = branch_kept ? kept8<PLANE, VPT>(own + L::kBranch, v) : same8(a.columns.scale), y = staged8<DY, PLANE, VPT>(st + L::kY, v, a.y.dtype);
             if (full) {
-                Vec w = staged8<kAny, PLANE>(st + L::kGate, v, a.full.dtype), dw;
+                Vec w = staged8<DY, PLANE, VPT>(st + L::kGate, v, a.full.dtype), dw;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) dw.p[j] = mul2(mul2(G.p[j], p.p[j]), mul2(y.p[j], both(s)));
                 if (gate.sigmoid) {
@@ -196,7 +198,7 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
                         dw.p[j] = mul2(dw.p[j], mul2(w.p[j], fma2(w.p[j], both(-1.f), both(1.f))));
                 }
                 if (a.dgate.p && stored)
-                    store8<kAny>(a.dgate.p + t0 * a.dgate.ld + offset(a.dgate), v * blockDim.x, a.dgate.dtype, dw);
+                    store8<DY>(a.dgate.row(t0) + offset(a.dgate), v * blockDim.x, a.dgate.dtype, dw);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) G.p[j] = mul2(G.p[j], w.p[j]);
             }
@@ -221,7 +223,7 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
         uint8_t* out = reinterpret_cast<uint8_t*>(a.part + (which[k] * parts + part) * a.H);
         if (blockDim.y > 1) __syncthreads();
 #pragma unroll
-        for (int v = 0; v < kVpt; ++v) {
+        for (int v = 0; v < VPT; ++v) {
             if (!has[v]) continue;
             const Vec& sum = k ? branch[v] : gain_sum[v];
             if (blockDim.y == 1) store8<BQ_DT_F32>(out, vec0 + v * blockDim.x, 0, sum);
@@ -289,32 +291,34 @@ sum_parts_kernel(const SumArgs a) {
 // ---------------------------------------------------------------- host side
 // How a call's rows are spread: a cluster of CTAs per row, threads per row, rows of a block, rows in flight.
 struct Shape {
-    int cluster, slice, block, threads, rows, stages, stage_bytes, blocks;   // blocks: clusters in the grid
+    int cluster, slice, block, vpt, threads, rows, stages, stage_bytes, at_stages, blocks;   // blocks: clusters in the grid
     size_t smem;
 };
 
-constexpr int kMaxBlocks = 2 * kSms;
+constexpr int kMaxBlocks = 3 * kSms;
 
-// planes: of a row's vectors in a stage.
-Shape shape_of(int T, int H, int n_planes) {
+// n_planes: of a row's vectors in a stage; n_constants: of the constants.
+Shape shape_of(int T, int H, int n_planes, int n_constants) {
     Shape p{};
     const int vecs = H / 8;
-    auto constants = [&] { return (size_t)4 * p.block * kVpt * 16; };
-    auto stage = [&] { return (size_t)n_planes * p.block * kVpt * 16; };
+    auto bytes = [&](int stages) { return (size_t)(n_constants + stages * n_planes) * p.block * p.vpt * 16; };
     // a block of 512 threads holds up to 1024 vectors of a row; wider rows, and rows two of which do not fit into
     // shared memory, are shared by a cluster
     for (p.cluster = 1;; p.cluster *= 2) {
         p.slice = (vecs + p.cluster - 1) / p.cluster;
-        p.block = p.slice > 256 * kVpt ? 512 : 256;
-        if (p.slice <= 512 * kVpt && constants() + 2 * stage() <= kSmemOfSm) break;
+        p.block = p.slice > 512 ? 512 : 256;
+        p.vpt = p.slice > 256 || p.cluster > 1 ? 2 : 1;
+        if (p.slice <= 1024 && bytes(2) <= kSmemOfSm) break;
     }
-    p.threads = ((p.slice + kVpt - 1) / kVpt + 31) / 32 * 32;
+    p.threads = ((p.slice + p.vpt - 1) / p.vpt + 31) / 32 * 32;
     p.rows = p.cluster > 1 ? 1 : std::max(1, p.block / p.threads);
-    // two CTAs an SM where two rows of each fit, with a third row where that fits too
-    const int per_sm = p.block == 256 && constants() + 2 * stage() <= kSmemOfSm / 2 ? 2 : 1;
-    p.stages = constants() + 3 * stage() <= kSmemOfSm / per_sm ? 3 : 2;
-    p.stage_bytes = (int)stage();
-    p.smem = constants() + p.stages * stage();   // room for the block's column sums too, 32 bytes per vector
+    // as many CTAs an SM as registers allow where two rows of each fit, with a third row where that fits too
+    int per_sm = p.block == 512 ? 1 : 2;
+    while (per_sm > 1 && (bytes(2) + 2048) * per_sm > kSmemOfSm) --per_sm;
+    p.stages = (bytes(3) + 2048) * per_sm <= kSmemOfSm ? 3 : 2;
+    p.stage_bytes = n_planes * p.block * p.vpt * 16;
+    p.at_stages = n_constants * p.block * p.vpt * 16;
+    p.smem = bytes(p.stages);   // room for the block's column sums too, 32 bytes per vector
     // clusters of 1, 2, 4 and 8 CTAs that this GPU holds at once, with one CTA an SM
     const int held = p.cluster == 1 ? kSms : p.cluster == 2 ? 76 : p.cluster == 4 ? 36 : 15;
     p.blocks = (int)std::min<int64_t>(held * per_sm, ((int64_t)T + p.rows - 1) / p.rows);
@@ -350,14 +354,15 @@ cudaError_t launch_rows(const Shape& p, const BackwardArgs& a, cudaStream_t st) 
 
 template <int DY, int DH, int DX, bool POST>
 cudaError_t launch_backward(const Shape& p, const BackwardArgs& a, cudaStream_t st) {
-    if (p.block == 256) return launch_rows<residual_norm_backward_kernel<DY, DH, DX, 256, POST, false>>(p, a, st);
-    return launch_rows<residual_norm_backward_kernel<DY, DH, DX, 512, POST, false>>(p, a, st);
+    if (p.vpt == 1) return launch_rows<residual_norm_backward_kernel<DY, DH, DX, 256, 1, POST, false>>(p, a, st);
+    if (p.block == 256) return launch_rows<residual_norm_backward_kernel<DY, DH, DX, 256, 2, POST, false>>(p, a, st);
+    return launch_rows<residual_norm_backward_kernel<DY, DH, DX, 512, 2, POST, false>>(p, a, st);
 }
 
 template <bool POST>
 cudaError_t launch_cluster(const Shape& p, const BackwardArgs& a, cudaStream_t st) {
-    if (p.block == 256) return launch_rows<residual_norm_backward_kernel<kAny, kAny, kAny, 256, POST, true>>(p, a, st);
-    return launch_rows<residual_norm_backward_kernel<kAny, kAny, kAny, 512, POST, true>>(p, a, st);
+    if (p.block == 256) return launch_rows<residual_norm_backward_kernel<kAny, kAny, kAny, 256, 2, POST, true>>(p, a, st);
+    return launch_rows<residual_norm_backward_kernel<kAny, kAny, kAny, 512, 2, POST, true>>(p, a, st);
 }
 
 }  // namespace
@@ -387,15 +392,15 @@ extern "C" bq_status bq_residual_norm_backward(const bq_residual_norm_desc* d, c
     if (d->T > 0) {
         const int ys = bq::dtype_size(d->y_dtype), hs = bq::dtype_size(d->h_dtype);
         if (!dx && !dh_out) return bq::fail(BQ_ERR_NULL, "%s: dx and dh_out are both NULL", name);
-        if ((s = bq::check_rows(name, "y", y, d->H, ldy, ys)) != BQ_OK ||
-            (dx && (s = bq::check_rows(name, "h_out", h_out, d->H, ldho, hs)) != BQ_OK) ||
-            (dh_out && (s = bq::check_rows(name, "dh_out", dh_out, d->H, lddho, hs)) != BQ_OK) ||
-            (dx && (s = bq::check_rows(name, "dx", dx, d->H, lddx, bq::dtype_size(d->x_dtype))) != BQ_OK) ||
-            (s = bq::check_rows(name, "dy", dy, d->H, lddy, ys)) != BQ_OK ||
-            (s = bq::check_rows(name, "dh", dh, d->H, lddh, hs)) != BQ_OK)
+        if ((s = check_matrix(name, "y", y, d->H, ldy, ys)) != BQ_OK ||
+            (dx && (s = check_matrix(name, "h_out", h_out, d->H, ldho, hs)) != BQ_OK) ||
+            (dh_out && (s = check_matrix(name, "dh_out", dh_out, d->H, lddho, hs)) != BQ_OK) ||
+            (dx && (s = check_matrix(name, "dx", dx, d->H, lddx, bq::dtype_size(d->x_dtype))) != BQ_OK) ||
+            (s = check_matrix(name, "dy", dy, d->H, lddy, ys)) != BQ_OK ||
+            (s = check_matrix(name, "dh", dh, d->H, lddh, hs)) != BQ_OK)
             return s;
         if (dgate && full &&
-            (s = bq::check_rows(name, "dgate", dgate, d->H, lddgate, bq::dtype_size(d->gate_dtype))) != BQ_OK)
+            (s = check_matrix(name, "dgate", dgate, d->H, lddgate, bq::dtype_size(d->gate_dtype))) != BQ_OK)
             return s;
     }
     if (sums) {
@@ -433,11 +438,12 @@ extern "C" bq_status bq_residual_norm_backward(const bq_residual_norm_desc* d, c
         auto go = [&](auto type, auto post) {
             using D = decltype(type);
             constexpr bool POST = decltype(post)::value;
-            auto shape = [&](int per_vec) { p = shape_of(d->T, d->H, per_vec + (full ? 2 : 0)); };
-            shape(planes(D::y) + 2 * planes(D::h) + planes(D::x));
-            if (p.cluster > 1) shape(2 + 2 * 2 + 2);   // the clusters' kernels leave two planes for every type
-            if (p.rows > 1 && std::max({a.y.ld, a.out.ld, a.dout.ld, a.dx.ld, a.dy.ld, a.dh.ld, a.full.ld, a.dgate.ld}) >
-                                  (int64_t)INT32_MAX / 16) {
+            const int constants = POST || channel ? 4 : 2;
+            auto shape = [&](int n) { p = shape_of(d->T, d->H, n, constants); };
+            shape((full ? 2 : 1) * planes(D::y) + 2 * planes(D::h) + planes(D::x));
+            if (p.cluster > 1) shape((full ? 2 : 1) * 2 + 2 * 2 + 2);   // the clusters' kernels leave two planes for every type
+            if (p.rows > 1 && std::max({a.y.ld16, a.out.ld16, a.dout.ld16, a.dx.ld16, a.dy.ld16, a.dh.ld16, a.full.ld16,
+                                        a.dgate.ld16}) > INT32_MAX / 256) {
                 // offsets inside a block's rows are ints: rows that far apart are taken one at a time
                 p.rows = 1;
                 p.blocks = std::min(d->T, kMaxBlocks);
@@ -445,9 +451,10 @@ extern "C" bq_status bq_residual_norm_backward(const bq_residual_norm_desc* d, c
             a.slice = p.slice;
             a.stages = p.stages;
             a.stage_bytes = p.stage_bytes;
+            a.at_stages = p.at_stages;
             e = p.cluster > 1 ? launch_cluster<POST>(p, a, st) : launch_backward<D::y, D::h, D::x, POST>(p, a, st);
         };
-        with_types(d->y_dtype, d->h_dtype, x_dtype, [&](auto type) {
+        with_types(d->y_dtype, d->h_dtype, x_dtype, full ? d->gate_dtype : d->y_dtype, [&](auto type) {
             if (d->post_gain) go(type, std::true_type());
             else go(type, std::false_type());
         });
