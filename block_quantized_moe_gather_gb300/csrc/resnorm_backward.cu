@@ -102,11 +102,14 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
     for (int64_t t0 = block0; t0 < a.T; t0 += step) {
         const int64_t t = t0 + threadIdx.y;
         const bool live = t < a.T;
-        if (a.stages == 2) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (a.stages == 1) fetch_row(ahead, t0);   // no room for a row ahead
+        if (a.stages < 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
         else asm volatile("cp.async.wait_group 1;" ::: "memory");
-        fetch_row(ahead, next);
-        next += step;
-        ahead = ahead + a.stage_bytes == end ? a.at_stages : ahead + a.stage_bytes;
+        if (a.stages > 1) {
+            fetch_row(ahead, next);
+            next += step;
+            ahead = ahead + a.stage_bytes == end ? a.at_stages : ahead + a.stage_bytes;
+        }
         const uint8_t* st = own + stage;
         stage = stage + a.stage_bytes == end ? a.at_stages : stage + a.stage_bytes;
         const float f = token_factor(gate, t, live);
@@ -260,8 +263,14 @@ sum_parts_kernel(const SumArgs a) {
     bq::allow_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     const float* part = a.part + (int64_t)blockIdx.y * a.parts * a.H;
-    float sum = 0.f;
+    const Gate& gate = a.columns.gate;
+    const bool branch = (int)blockIdx.y == a.sum_branch;
+    float f = 1.f, post = 1.f, sum = 0.f;   // the constants are on their way while the parts are
     if (c < a.H) {
+        if (branch && warp == 0) {
+            if (gate.kind == GATE_CHANNEL) f = load1(gate.p, c, gate.dtype);
+            if (a.columns.post) post = load1(a.columns.post, c, a.columns.gain_dtype);
+        }
 #pragma unroll 8
         for (int64_t i = warp; i < a.parts; i += kWarps) sum += part[i * a.H + c];
     }
@@ -270,22 +279,18 @@ sum_parts_kernel(const SumArgs a) {
     if (warp || c >= a.H) return;
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) sum += s_red[w][lane];
-    if ((int)blockIdx.y == a.sum_gain) {
+    if (!branch) {
         a.dgain[c] = sum;
         return;
     }
-    sum *= a.columns.scale;
-    const Gate& gate = a.columns.gate;
-    float f = 1.f, df = 1.f;
-    if (gate.kind == GATE_CHANNEL) {
-        f = load1(gate.p, c, gate.dtype);
-        if (gate.sigmoid) {
-            f = sigmoid_f(f);
-            df = f * (1.f - f);
-        }
+    float slope = 1.f;
+    if (gate.kind == GATE_CHANNEL && gate.sigmoid) {
+        f = sigmoid_f(f);
+        slope = f * (1.f - f);
     }
+    sum *= a.columns.scale;
     if (a.dpost) a.dpost[c] = a.parts ? sum * f : 0.f;
-    if (a.dgate) a.dgate[c] = a.parts ? sum * df * (a.columns.post ? load1(a.columns.post, c, a.columns.gain_dtype) : 1.f) : 0.f;
+    if (a.dgate) a.dgate[c] = a.parts ? sum * slope * post : 0.f;
 }
 
 // ---------------------------------------------------------------- host side
@@ -302,20 +307,21 @@ Shape shape_of(int T, int H, int n_planes, int n_constants) {
     Shape p{};
     const int vecs = H / 8;
     auto bytes = [&](int stages) { return (size_t)(n_constants + stages * n_planes) * p.block * p.vpt * 16; };
-    // a block of 512 threads holds up to 1024 vectors of a row; wider rows, and rows two of which do not fit into
+    auto fit = [&](int ctas) { return (bytes(2) + 2048) * ctas <= kSmemOfSm; };   // two rows of each
+    // a block of 512 threads holds up to 1024 vectors of a row; wider rows, and rows of which one does not fit into
     // shared memory, are shared by a cluster
     for (p.cluster = 1;; p.cluster *= 2) {
         p.slice = (vecs + p.cluster - 1) / p.cluster;
         p.block = p.slice > 512 ? 512 : 256;
-        p.vpt = p.slice > 256 || p.cluster > 1 ? 2 : 1;
-        if (p.slice <= 1024 && bytes(2) <= kSmemOfSm) break;
+        p.vpt = 2;
+        // two vectors a thread share what a row costs a warp beside them; one where that brings a second CTA to the SM
+        if (p.cluster == 1 && p.slice <= 256 && !fit(2)) p.vpt = 1;
+        if (p.slice <= 1024 && bytes(1) <= kSmemOfSm) break;
     }
     p.threads = ((p.slice + p.vpt - 1) / p.vpt + 31) / 32 * 32;
     p.rows = p.cluster > 1 ? 1 : std::max(1, p.block / p.threads);
-    // as many CTAs an SM as registers allow where two rows of each fit, with a third row where that fits too
-    int per_sm = p.block == 512 ? 1 : 2;
-    while (per_sm > 1 && (bytes(2) + 2048) * per_sm > kSmemOfSm) --per_sm;
-    p.stages = (bytes(3) + 2048) * per_sm <= kSmemOfSm ? 3 : 2;
+    const int per_sm = p.block == 256 && fit(2) ? 2 : 1;   // what the registers allow
+    p.stages = (bytes(3) + 2048) * per_sm <= kSmemOfSm ? 3 : bytes(2) <= kSmemOfSm ? 2 : 1;
     p.stage_bytes = n_planes * p.block * p.vpt * 16;
     p.at_stages = n_constants * p.block * p.vpt * 16;
     p.smem = bytes(p.stages);   // room for the block's column sums too, 32 bytes per vector
