@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_uint64, c_void_p
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -43,15 +44,10 @@ class MoEDescC(ctypes.Structure):
                 ("route_scale", c_float), ("reserved", c_int32)]
 
 
-class EpilogueC(ctypes.Structure):
-    _fields_ = [("act", c_int32), ("scale", c_float), ("bias", c_void_p), ("residual", c_void_p), ("ldr", c_int64)]
-
-
-class ResidualNormDescC(ctypes.Structure):
-    _fields_ = [(n, c_int32) for n in ("T", "H", "y_dtype", "h_dtype", "x_dtype", "gain_dtype", "gate_dtype", "gate_kind",
-                                       "gate_sigmoid")] + [
-        ("scale", c_float), ("residual_scale", c_float), ("eps", c_float), ("gain", c_void_p), ("post_gain", c_void_p),
-        ("gate", c_void_p), ("ldgate", c_int64)]
+# Host structs that are made anew for every call, as bytes in the layout of bq.h (a ctypes.Structure of that many fields
+# takes 1 us to make, a tenth of a small call; the bytes of an object lie on 16-byte boundaries).
+_EPILOGUE = struct.Struct("if2Pq")                  # bq_epilogue: act, scale, bias, residual, ldr
+_RESIDUAL_NORM_DESC = struct.Struct("9i3f3Pq")      # bq_residual_norm_desc, in its order
 
 
 _SIGS = {
@@ -106,14 +102,14 @@ _SIGS = {
     "bq_moe_mm_fp8_b128": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_int32,
                                      c_int32, c_int32, c_void_p, c_int32, c_int64, c_void_p]),
     "bq_mm_fp8_b128_epilogue": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32,
-                                          POINTER(EpilogueC), c_void_p, c_int32, c_int64, c_void_p]),
+                                          c_char_p, c_void_p, c_int32, c_int64, c_void_p]),
     "bq_moe_mm_fp8_b128_epilogue": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
-                                              c_int32, c_int32, POINTER(EpilogueC), c_void_p, c_int32, c_int64,
+                                              c_int32, c_int32, c_char_p, c_void_p, c_int32, c_int64,
                                               c_void_p]),
-    "bq_residual_norm": (c_int32, [POINTER(ResidualNormDescC), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+    "bq_residual_norm": (c_int32, [c_char_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
                                    c_void_p, c_int64, c_void_p]),
     "bq_residual_norm_backward_workspace_bytes": (c_size_t, [c_int32, c_int32]),
-    "bq_residual_norm_backward": (c_int32, [POINTER(ResidualNormDescC), c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+    "bq_residual_norm_backward": (c_int32, [c_char_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
                                             c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
                                             c_void_p, c_void_p, c_int64, c_void_p, c_size_t, c_void_p]),
     "bq_moe_balance_workspace_bytes": (c_size_t, [c_int32, c_int32, c_int32]),
@@ -603,7 +599,7 @@ ACT_BY_NAME = {"none": ACT_NONE, "swiglu": ACT_SWIGLU, "silu": ACT_SILU, "gelu":
 
 
 def _epilogue(where, swiglu, act, bias, bias_shape, residual, scale, dt, rows, cols):
-    """The C struct of a product's end, or None where it changes nothing."""
+    """bq_epilogue of a product's end, or None where it changes nothing."""
     if act is not None and act not in ACT_BY_NAME:
         _refuse(2, where, f"unknown activation {act!r}")
     code = ACT_SWIGLU if swiglu else ACT_NONE if act is None else ACT_BY_NAME[act]
@@ -613,7 +609,7 @@ def _epilogue(where, swiglu, act, bias, bias_shape, residual, scale, dt, rows, c
     pr, ldr = None, 0
     if residual is not None:
         pr, _, _, _, ldr = _rows_of(where, "residual", residual, rows, cols, dt)
-    return EpilogueC(code, scale, pb, pr, ldr)
+    return _EPILOGUE.pack(code, scale, pb or 0, pr or 0, ldr)
 
 
 def _gated(where, swiglu, act):
@@ -637,7 +633,7 @@ def mm_fp8_b128(x, x_scales, w, w_scales, y, swiglu: bool = False, stream=None, 
     if epi is None:
         _check(_lib.bq_mm_fp8_b128(px, pxs, m, pw, pws, n, k, sw, py, dt, ldy, st), where)
     else:
-        _check(_lib.bq_mm_fp8_b128_epilogue(px, pxs, m, pw, pws, n, k, ctypes.byref(epi), py, dt, ldy, st), where)
+        _check(_lib.bq_mm_fp8_b128_epilogue(px, pxs, m, pw, pws, n, k, epi, py, dt, ldy, st), where)
     return y
 
 
@@ -657,7 +653,7 @@ def moe_mm_fp8_b128(x, x_scales, offsets, w, w_scales, y, swiglu: bool = False, 
     if epi is None:
         _check(_lib.bq_moe_mm_fp8_b128(px, pxs, m, po, e, pw, pws, n, k, sw, py, dt, ldy, st), where)
     else:
-        _check(_lib.bq_moe_mm_fp8_b128_epilogue(px, pxs, m, po, e, pw, pws, n, k, ctypes.byref(epi), py, dt, ldy, st),
+        _check(_lib.bq_moe_mm_fp8_b128_epilogue(px, pxs, m, po, e, pw, pws, n, k, epi, py, dt, ldy, st),
                where)
     return y
 
@@ -697,8 +693,9 @@ def _norm_desc(where, t, h, dy, dh, dx, gain, post_gain, gate, gate_sigmoid, sca
     if gdt is not None and pdt != gdt:
         _refuse(4, where, f"gain has type {gain.dtype}, post_gain {post_gain.dtype}")
     kind, pgate, gate_dt, ldgate = _gate(where, gate, t, h)
-    return ResidualNormDescC(t, h, dy, dh, dx, DT_F32 if pdt is None else pdt, gate_dt, kind, int(bool(gate_sigmoid)),
-                             scale, residual_scale, eps, pg, pp, pgate, ldgate)
+    return kind, gate_dt, _RESIDUAL_NORM_DESC.pack(t, h, dy, dh, dx, DT_F32 if pdt is None else pdt, gate_dt, kind,
+                                                   int(bool(gate_sigmoid)), scale, residual_scale, eps, pg or 0, pp or 0,
+                                                   pgate or 0, ldgate)
 
 
 def residual_norm(y, h, h_out, x=None, gain=None, post_gain=None, gate=None, gate_sigmoid: bool = False,
@@ -716,8 +713,8 @@ def residual_norm(y, h, h_out, x=None, gain=None, post_gain=None, gate=None, gat
     px, dx, ldx = None, dh, 0
     if x is not None:
         px, dx, _, _, ldx = _rows_of(where, "x", x, t, n)
-    desc = _norm_desc(where, t, n, dy, dh, dx, gain, post_gain, gate, gate_sigmoid, scale, residual_scale, eps)
-    _check(_lib.bq_residual_norm(ctypes.byref(desc), py, ldy, ph, ldh, po, ldo, px, ldx, st), where)
+    _, _, desc = _norm_desc(where, t, n, dy, dh, dx, gain, post_gain, gate, gate_sigmoid, scale, residual_scale, eps)
+    _check(_lib.bq_residual_norm(desc, py, ldy, ph, ldh, po, ldo, px, ldx, st), where)
     return h_out, x
 
 
@@ -745,7 +742,7 @@ def residual_norm_backward(y, h_out, dh_out, dx, dy, dh, gain=None, post_gain=No
         po, _, _, _, ldo = _rows_of(where, "dh_out", dh_out, t, n, th)
     if dx is not None:
         px, tx, _, _, ldx = _rows_of(where, "dx", dx, t, n)
-    desc = _norm_desc(where, t, n, ty, th, tx, gain, post_gain, gate, gate_sigmoid, scale, residual_scale, eps)
+    kind, gate_dt, desc = _norm_desc(where, t, n, ty, th, tx, gain, post_gain, gate, gate_sigmoid, scale, residual_scale, eps)
     sums = [None if s is None else _dense(where, what, s, (n,), "f32")
             for what, s in (("dgain", dgain), ("dpost_gain", dpost_gain))]
     pgate, ldgate = None, 0
@@ -753,12 +750,12 @@ def residual_norm_backward(y, h_out, dh_out, dx, dy, dh, gain=None, post_gain=No
         if gate is None or dgate.shape != gate.shape:
             _refuse(2, where, f"dgate has shape {list(dgate.shape)}, the gate "
                               f"{None if gate is None else list(gate.shape)}")
-        if desc.gate_kind == GATE_FULL:
-            pgate, _, _, _, ldgate = _rows_of(where, "dgate", dgate, t, n, desc.gate_dtype)
+        if kind == GATE_FULL:
+            pgate, _, _, _, ldgate = _rows_of(where, "dgate", dgate, t, n, gate_dt)
         else:
             pgate = _dense(where, "dgate", dgate, gate.shape, "f32")
     pw, nw = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _check(_lib.bq_residual_norm_backward(ctypes.byref(desc), py, ldy, ph, ldh, po, ldo, px, ldx, pd, ldd, pg, ldg,
+    _check(_lib.bq_residual_norm_backward(desc, py, ldy, ph, ldh, po, ldo, px, ldx, pd, ldd, pg, ldg,
                                           *sums, pgate, ldgate, pw, nw, st), where)
     return dy, dh
 

@@ -1161,6 +1161,7 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                 }
             }
         }
+        if (EPI) asm volatile("cp.async.wait_all;" ::: "memory");   // a wait that ran out leaves a bias on its way
     }
     tc_fence_before();
     __syncthreads();

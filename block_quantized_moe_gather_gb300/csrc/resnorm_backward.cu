@@ -267,7 +267,7 @@ sum_parts_kernel(const SumArgs a) {
     const bool branch = (int)blockIdx.y == a.sum_branch;
     float f = 1.f, post = 1.f, sum = 0.f;   // the constants are on their way while the parts are
     if (c < a.H) {
-        if (branch && warp == 0) {
+        if (branch && warp == 0 && a.parts) {   // without rows the gate and the gains may be missing
             if (gate.kind == GATE_CHANNEL) f = load1(gate.p, c, gate.dtype);
             if (a.columns.post) post = load1(a.columns.post, c, a.columns.gain_dtype);
         }

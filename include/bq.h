@@ -596,13 +596,15 @@ bq_status bq_moe_mm_fp8_b128_epilogue(const uint8_t* x, const float* xscales, in
  *
  * y, h, h_out, x and their gradients: device rows of H elements of y_dtype (y,
  * dy), h_dtype (h, h_out, dh_out, dh) or x_dtype (x, dx), ld* elements apart.
- * H a multiple of 8, at most 16384; rows start and end on 16-byte boundaries.
+ * H a multiple of 8, at most 16384; rows start and end on 16-byte boundaries and
+ * lie less than 2^35 bytes apart.
  * gain, post_gain: gain_dtype [H], 16-byte aligned.  gate: gate_dtype, [T]
  * (aligned to its element), [H] (16-byte aligned) or rows like y.  Outputs must
  * not overlap inputs, but h_out may be h, and dh may be dh_out.
  * workspace of the backward pass: device, at least
  * bq_residual_norm_backward_workspace_bytes(T, H) bytes, 16-byte aligned; needed
- * only for dgain, dpost_gain and the dgate of a gate per channel.
+ * only for dgain, dpost_gain and the dgate of a gate per channel.  Calls that may
+ * overlap on the GPU (other streams, other captured graphs) need one each.
  * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_FORMAT (an unknown type), BQ_ERR_ALIGN,
  * BQ_ERR_WORKSPACE, BQ_ERR_CUDA.  T == 0: a no-op, but sums over rows become 0.
  */
@@ -672,7 +674,9 @@ bq_status bq_residual_norm_backward(const bq_residual_norm_desc* desc, const voi
  * [S][E]; losses fp32 [2]; all 4-byte aligned, dlogits to its element.  E in
  * 1..1024, k in 1..min(8, E), S in 1..65536.  workspace: device, 256-byte
  * aligned, at least bq_moe_balance_workspace_bytes(T, E, S) or
- * bq_moe_route_backward_workspace_bytes(T, E) bytes (0: invalid sizes).
+ * bq_moe_route_backward_workspace_bytes(T, E) bytes (0: invalid sizes); nothing in
+ * it is read before it is written.  Calls that may overlap on the GPU (other
+ * streams, other captured graphs) need one each.
  * Errors: BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_FORMAT, BQ_ERR_ALIGN,
  * BQ_ERR_WORKSPACE, BQ_ERR_CUDA.  T == 0: counts, probs, losses and dbias become 0.
  */
