@@ -163,13 +163,32 @@ __device__ __forceinline__ Softmax softmax_row(const float (&z)[NPER], float (&e
     m = warp_max(m);
     if (m == -INFINITY) m = 0.f;
     float sum = 0.f;
+    if (NPER == 1) {
+        sum = ex[0] = exp2_approx((z[0] - m) * kLog2E);
+    } else {
+        f32x2 total = both(0.f);
 #pragma unroll
-    for (int i = 0; i < NPER; ++i) {
-        ex[i] = exp2_approx((z[i] - m) * kLog2E);
-        sum += ex[i];
+        for (int i = 0; i < NPER; i += 2) {
+            const int j = (i + 1) % NPER;
+            const float2 d = parts_of(mul2(fma2(two(z[i], z[j]), both(1.f), both(-m)), both(kLog2E)));
+            ex[i] = exp2_approx(d.x);
+            ex[j] = exp2_approx(d.y);
+            total = fma2(two(ex[i], ex[j]), both(1.f), total);
+        }
+        sum = sum2(total);
     }
     sum = warp_sum(sum);
     return {m, sum == 0.f ? 0.f : rcp_approx(sum), sum == 0.f ? 0.f : m + log_approx(sum)};
+}
+
+// <x, y> over the warp's row.
+template <int NPER>
+__device__ __forceinline__ float row_dot(const float (&x)[NPER], const float (&y)[NPER]) {
+    if (NPER == 1) return warp_sum(x[0] * y[0]);
+    f32x2 dot = both(0.f);
+#pragma unroll
+    for (int i = 0; i < NPER; i += 2) dot = fma2(two(x[i], x[(i + 1) % NPER]), two(y[i], y[(i + 1) % NPER]), dot);
+    return warp_sum(sum2(dot));
 }
 
 // Scores (and slopes) of a row, and 1 / their sum (0 where every score is 0).
@@ -258,6 +277,8 @@ __device__ __forceinline__ void chunk_sums(const BalanceArgs& a, float* s_red, i
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t first = (int64_t)blockIdx.x * a.chunk_rows;
     const int row0 = (int)first, row1 = (int)min((int64_t)a.T, first + a.chunk_rows);
+    float z[NPER];
+    if (kAhead && row0 + warp < row1) Row::load(a.logits + (int64_t)(row0 + warp) * a.E, a.bias, a.E, lane, z);
     for (int s = sequence_totals(a.offsets, a.S, a.T, row0, a.status).before; s < a.S; ++s) {
         int lo, hi;
         sequence(a.offsets, s, a.T, a.status, lo, hi);
@@ -266,8 +287,8 @@ __device__ __forceinline__ void chunk_sums(const BalanceArgs& a, float* s_red, i
         hi = min(hi, row1);
         if (lo >= hi) continue;
         for (int e = threadIdx.x; e < a.E; e += kThreads) s_hist[e] = 0;
-        float z[NPER], acc[NPER], z2 = 0.f;
-        if (kAhead && lo + warp < hi) Row::load(a.logits + (int64_t)(lo + warp) * a.E, a.bias, a.E, lane, z);
+        float acc[NPER], z2 = 0.f;
+        if (kAhead && lo > row0 && lo + warp < hi) Row::load(a.logits + (int64_t)(lo + warp) * a.E, a.bias, a.E, lane, z);
         __syncthreads();
         for (int64_t i = (int64_t)lo * a.k + threadIdx.x; i < (int64_t)hi * a.k; i += kThreads) {
             const int e = __ldg(a.ids + i);
@@ -532,43 +553,49 @@ struct RouteGradArgs {
     int32_t* status;
 };
 
-// What lane j < k has of its row's selected expert, as loaded: two rows ahead its id and gradient, one row ahead its
-// logit (a chain of two loads that a row would wait for).
+// The selected experts of four of a warp's rows at a time: lane 8 q + j has expert j < k of the q-th (rows lie kWarps
+// apart).  Loaded ahead: the id and the gradient a batch of four ahead, the logit (a chain of two loads) with them.
 struct Pair {
     int id = -1;
     float dw = 0.f, z = -INFINITY;
 
-    __device__ __forceinline__ void load(const RouteGradArgs& a, int64_t r, int row1, int lane) {
+    __device__ __forceinline__ void load(const RouteGradArgs& a, int64_t first, int row1, int lane) {
+        const int64_t r = first + (lane >> 3) * kWarps;
         id = -1;
-        if (r >= row1 || lane >= a.k) return;
-        id = __ldg(a.ids + r * a.k + lane);
-        dw = __ldg(a.dweights + r * a.k + lane);
+        if (r >= row1 || (lane & 7) >= a.k) return;
+        id = __ldg(a.ids + r * a.k + (lane & 7));
+        dw = __ldg(a.dweights + r * a.k + (lane & 7));
     }
-    __device__ __forceinline__ void load_logit(const RouteGradArgs& a, int64_t r) {
-        if (id < 0 || id >= a.E) return;   // reported when the row's turn comes, if it belongs to a sequence
-        z = __ldg(a.logits + r * a.E + id);
+    __device__ __forceinline__ void load_logit(const RouteGradArgs& a, int64_t first, int lane) {
+        if (id < 0 || id >= a.E) return;
+        z = __ldg(a.logits + (first + (lane >> 3) * kWarps) * a.E + id);
         if (a.bias) z = __fadd_rn(z, __ldg(a.bias + id));
+    }
+    // An id that names no expert, reported when its row's turn comes (if that belongs to a sequence).
+    __device__ __forceinline__ void report(const RouteGradArgs& a, int q, int lane) const {
+        if (lane >> 3 == q && (lane & 7) < a.k && (id < 0 || id >= a.E)) bq::set_device_error(a.status, BQ_DEV_BAD_EXPERT_ID);
     }
 };
 
-__device__ __forceinline__ float sum_of_eight(float v) {   // of lanes 0 .. 7, in each of them
+__device__ __forceinline__ float sum_of_eight(float v) {
 #pragma unroll
     for (int off = 4; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
 }
 
-// The gradient that the router weights bring: lane j < k gets its expert id (-1: none) and its share g.  Of lanes that
-// name the same expert the first gets the sum, the others -1.
+// The gradient that the router weights bring to the four rows: each lane its expert id (-1: none) and its share g.  Of
+// lanes that name the same expert of a row the first gets the sum, the others -1.
 template <int RULE>
 __device__ __forceinline__ void selected(const RouteGradArgs& a, const Pair& p, int lane, int& id, float& g) {
-    id = p.id;
-    if (lane < a.k && (id < 0 || id >= a.E)) {
-        bq::set_device_error(a.status, BQ_DEV_BAD_EXPERT_ID);
-        id = -1;
-    }
+    id = p.id < a.E ? p.id : -1;
+    if (id < 0) id = -1;
     if (RULE == RULE_SOFTMAX) {
-        const float m = warp_max(id >= 0 ? p.z : -INFINITY), ex = id >= 0 ? exp2_approx((p.z - m) * kLog2E) : 0.f;
-        const float w = __fdividef(ex, sum_of_eight(ex)), mean = sum_of_eight(id >= 0 ? w * p.dw : 0.f);
+        float m = id >= 0 ? p.z : -INFINITY;
+#pragma unroll
+        for (int off = 4; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if (m == -INFINITY) m = 0.f;   // none selected, or all of them -inf: no weights, no gradient
+        const float ex = id >= 0 ? exp2_approx((p.z - m) * kLog2E) : 0.f, total = sum_of_eight(ex);
+        const float w = total == 0.f ? 0.f : __fdividef(ex, total), mean = sum_of_eight(id >= 0 ? w * p.dw : 0.f);
         g = id >= 0 ? w * (p.dw - mean) : 0.f;
     } else {
         float score, slope, unused0, unused1;
@@ -576,12 +603,13 @@ __device__ __forceinline__ void selected(const RouteGradArgs& a, const Pair& p, 
         g = id >= 0 ? a.scale * p.dw * slope : 0.f;
     }
     // the same index twice (a router names none twice, a caller may): added in slot order
-    const uint32_t same = __match_any_sync(0xffffffffu, id >= 0 ? id : ~lane);
+    const uint32_t same = __match_any_sync(0xffffffffu, id >= 0 ? 4 * id + (lane >> 3) : ~lane);
     if (__any_sync(0xffffffffu, __popc(same) > 1)) {
         float sum = 0.f;
         for (int j = 0; j < a.k; ++j) {
-            const float gj = __shfl_sync(0xffffffffu, g, j);
-            if (same >> j & 1) sum += gj;
+            const int from = (lane & 24) + j;
+            const float gj = __shfl_sync(0xffffffffu, g, from);
+            if (same >> from & 1) sum += gj;
         }
         if (__popc(same) > 1) {
             g = sum;
@@ -649,28 +677,31 @@ route_backward_kernel(const __grid_constant__ RouteGradArgs a) {
     __syncwarp();
     float z[NPER];
     if (kAhead && row0 + warp < row1) Row::load(a.logits + (int64_t)(row0 + warp) * a.E, a.bias, a.E, lane, z);
-    Pair pair, pair1, pair2;
-    if (a.dweights) {
-        pair.load(a, row0 + warp, row1, lane);
-        pair1.load(a, (int64_t)row0 + warp + kWarps, row1, lane);
-    }
+    Pair pair, ahead;
+    if (a.dweights) pair.load(a, (int64_t)row0 + warp, row1, lane);
     const float dbalance = __ldg(a.dlosses), dz = __ldg(a.dlosses + 1);
     const Totals totals = sequence_totals(a.offsets, a.S, a.T, row0, a.status);
     const float per_seq = dbalance * ((float)a.E / (float)a.k) / (float)max(1, totals.used);
     const float per_row = 2.f * dz / (float)max(1, totals.rows);
-    if (a.dweights) pair.load_logit(a, row0 + warp);
+    if (a.dweights) pair.load_logit(a, (int64_t)row0 + warp, lane);
     Place place{totals.before, a.offsets ? -1 : 0, a.offsets ? -1 : a.T, true};
     float acc[NPER], weight[NPER], per_count = 0.f;
 #pragma unroll
     for (int i = 0; i < NPER; ++i) acc[i] = weight[i] = 0.f;
+    int id = -1, q = 0;
+    float g = 0.f;
     for (int r = row0 + warp; r < row1; r += kWarps) {
         float next[NPER];
-        if (a.dweights) {
-            pair1.load_logit(a, (int64_t)r + kWarps);
-            pair2.load(a, (int64_t)r + 2 * kWarps, row1, lane);
-        }
         if (!kAhead) Row::load(a.logits + (int64_t)r * a.E, a.bias, a.E, lane, z);
         else if (r + kWarps < row1) Row::load(a.logits + (int64_t)(r + kWarps) * a.E, a.bias, a.E, lane, next);
+        if (a.dweights) {
+            if (q == 0) {
+                selected<RULE>(a, pair, lane, id, g);
+                ahead.load(a, (int64_t)r + 4 * kWarps, row1, lane);
+            } else if (q == 1) {
+                ahead.load_logit(a, (int64_t)r + 3 * kWarps, lane);
+            }
+        }
         if (place.find(a, r)) {
             const int32_t* counts = a.counts + (int64_t)place.s * a.E;
             if (place.fresh) {
@@ -681,50 +712,43 @@ route_backward_kernel(const __grid_constant__ RouteGradArgs a) {
                     weight[i] = Row::at(lane, i) < a.E ? (float)__ldg(counts + Row::at(lane, i)) * per_count : 0.f;
                 place.fresh = false;
             }
-            int id = -1;
-            float g = 0.f, own = 0.f;
-            const float zs = pair.z;
-            if (a.dweights) {
-                selected<RULE>(a, pair, lane, id, g);
-                if (id >= 0) own = (float)__ldg(counts + id) * per_count;
-            }
-            float d[NPER];
+            const bool mine = lane >> 3 == q && id >= 0;
+            const float own = mine ? (float)__ldg(counts + id) * per_count : 0.f;
+            float d[NPER], base = 0.f;
             const Softmax soft = softmax_row(z, d);
             const float f = per_row * soft.lse * soft.inv;
-            float dot = 0.f, base = 0.f;
             if (RULE == RULE_SOFTMAX) {
+                // p (weight - <p, weight> + per_row lse), p = d inv
+                const float rest = __fmaf_rn(-row_dot(d, weight) * soft.inv, soft.inv, f);
 #pragma unroll
-                for (int i = 0; i < NPER; ++i) dot = __fmaf_rn(d[i], weight[i], dot);
-                dot = warp_sum(dot) * soft.inv;
-#pragma unroll
-                for (int i = 0; i < NPER; ++i) d[i] *= __fmaf_rn(weight[i] - dot, soft.inv, f);
-                if (id >= 0) base = exp2_approx((zs - soft.m) * kLog2E) * __fmaf_rn(own - dot, soft.inv, f);
+                for (int i = 0; i < NPER; ++i) d[i] *= __fmaf_rn(weight[i], soft.inv, rest);
+                if (mine) base = exp2_approx((pair.z - soft.m) * kLog2E) * __fmaf_rn(own, soft.inv, rest);
             } else {
                 float sc[NPER], slope[NPER];
-                const float inv = score_row<true>(z, sc, slope);
-#pragma unroll
-                for (int i = 0; i < NPER; ++i) dot = __fmaf_rn(sc[i], weight[i], dot);
-                dot = warp_sum(dot) * inv;
+                const float inv = score_row<true>(z, sc, slope), dot = row_dot(sc, weight) * inv;
 #pragma unroll
                 for (int i = 0; i < NPER; ++i) d[i] = __fmaf_rn(d[i], f, slope[i] * inv * (weight[i] - dot));
-                if (id >= 0) {
+                if (mine) {
                     float score, change, unused0, unused1;
-                    scores_of<true>(zs, 0.f, score, unused0, change, unused1);
-                    base = __fmaf_rn(exp2_approx((zs - soft.m) * kLog2E), f, change * inv * (own - dot));
+                    scores_of<true>(pair.z, 0.f, score, unused0, change, unused1);
+                    base = __fmaf_rn(exp2_approx((pair.z - soft.m) * kLog2E), f, change * inv * (own - dot));
                 }
             }
             Row::store(a.dlogits, r, a.dtype, a.E, lane, d);
             __syncwarp();   // the row is written before its selected values are written again
-            if (id >= 0) store_value(a.dlogits, (int64_t)r * a.E + id, a.dtype, base + g);
+            if (mine) store_value(a.dlogits, (int64_t)r * a.E + id, a.dtype, base + g);
+            if (a.dweights) pair.report(a, q, lane);
             if (a.part_b) {
-                if (id >= 0) s_acc[id] += g;
+                if (mine) s_acc[id] += g;
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < NPER; ++i) acc[i] += d[i];
             }
         }
-        pair = pair1;
-        pair1 = pair2;
+        if (++q == 4) {
+            q = 0;
+            pair = ahead;
+        }
         if (kAhead) {
 #pragma unroll
             for (int i = 0; i < NPER; ++i) z[i] = next[i];
@@ -754,7 +778,15 @@ route_weights_backward_kernel(const __grid_constant__ RouteGradArgs a, int wide)
         for (int e = lane; e < a.E; e += 32) s_acc[e] = 0.f;
     __syncwarp();
     Place place{sequence_totals(a.offsets, a.S, a.T, row0, a.status).before, a.offsets ? -1 : 0, a.offsets ? -1 : a.T, true};
-    for (int r = row0 + warp; r < row1; r += kWarps) {
+    Pair pair;
+    int id = -1, q = 0;
+    float g = 0.f;
+    for (int r = row0 + warp; r < row1; r += kWarps, q = (q + 1) & 3) {
+        if (q == 0) {
+            pair.load(a, r, row1, lane);
+            pair.load_logit(a, r, lane);
+            selected<RULE>(a, pair, lane, id, g);
+        }
         if (!place.find(a, r)) continue;
         uint8_t* row = static_cast<uint8_t*>(a.dlogits) + (int64_t)r * a.E * es;
         if (wide) {
@@ -762,17 +794,12 @@ route_weights_backward_kernel(const __grid_constant__ RouteGradArgs a, int wide)
         } else {
             for (int i = lane; i < a.E; i += 32) store_value(row, i, a.dtype, 0.f);
         }
-        int id;
-        float g;
-        Pair pair;
-        pair.load(a, r, row1, lane);
-        pair.load_logit(a, r);
-        selected<RULE>(a, pair, lane, id, g);
         __syncwarp();   // the zeros are written before the values
-        if (id >= 0) {
+        if (lane >> 3 == q && id >= 0) {
             store_value(row, id, a.dtype, g);
             if (a.part_b) s_acc[id] += g;
         }
+        pair.report(a, q, lane);
         __syncwarp();
     }
     if (a.part_b) write_part(a, s_dyn);

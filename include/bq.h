@@ -664,6 +664,7 @@ bq_status bq_residual_norm_backward(const bq_residual_norm_desc* desc, const voi
  * call; selection and counts are constants.
  *   softmax rules:  dlogits[ids[j]] += w_j * (dweights_j - sum_i w_i dweights_i), w over the k selected
  *   score rule:     dlogits[ids[j]] += scale * dweights_j * score'(z)
+ * (selected logits that are all -inf bring none)
  * ids are read only with dweights; those outside [0, E) set
  * BQ_DEV_BAD_EXPERT_ID and are left out of the k.  dlogits: device [T][E] of
  * `dtype`, computed in fp32 and rounded once; rows that belong to no sequence

@@ -168,11 +168,11 @@ def route_backward(logits, ids, dweights, scoring="softmax", bias=None, scale=1.
             dw = _f64(dweights)[r, on]
             if scoring == "sqrtsoftplus":
                 g = scale * dw * slope[r, at]
-            elif on:
+            elif on and z[r, at].max() > -np.inf:
                 ex = np.exp(z[r, at] - z[r, at].max())
                 w = ex / ex.sum()
                 g = w * (dw - (w * dw).sum())
-            else:
+            else:              # none, or all of them -inf: no gradient
                 continue
             np.add.at(d[r], at, g)
     ranges = _ranges(t, offsets)

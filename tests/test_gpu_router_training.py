@@ -193,6 +193,25 @@ def test_masked_and_extreme_logits(lib, rule):
     assert np.isfinite(p).all()
 
 
+@pytest.mark.parametrize("rule", RULES)
+def test_selected_logits_of_minus_infinity(lib, rule):
+    import torch
+    logits = np.full((6, 40), -np.inf, dtype=np.float32)
+    logits[1, 3], logits[2, :5] = 1.0, [1.0, 2.0, 3.0, -np.inf, 0.0]
+    logits[4:] = np.random.default_rng(3).standard_normal((2, 40))
+    ids = np.array([[0, 1, 2]] * 2 + [[0, 2, 3], [3, 0, 1], [5, 6, 7], [39, 0, 20]], dtype=np.int32)
+    ids[1, 0] = 3
+    dw = np.array([[1.0, 2.0, -1.0]] * 6, dtype=np.float32)
+    counts = torch.ones(1, 40, dtype=torch.int32, device="cuda")
+    for dl in (None, np.array([2.0, 0.5], dtype=np.float32)):
+        d = torch.full((6, 40), np.nan, device="cuda")
+        lib.moe_route_backward(dev(logits), dev(ids), dev(dw), d, scoring=lib.SCORING_BY_NAME[rule], counts=counts,
+                               dlosses=None if dl is None else dev(dl))
+        want = O.route_backward(logits, ids, dw, rule, counts=np.ones((1, 40)), dlosses=dl)
+        np.testing.assert_allclose(f64(d), want, atol=1e-5)
+    assert not d[0].any()
+
+
 def test_bad_ids_and_offsets_are_reported(lib):
     import torch
     g = np.random.default_rng(13)
