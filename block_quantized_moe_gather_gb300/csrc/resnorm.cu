@@ -24,7 +24,7 @@ struct ForwardArgs {
     float residual_scale, eps;
 };
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 1024;
 
 // blockDim.x threads take a row, a thread the vectors x, x + blockDim.x, ... of it; blockDim.y rows a CTA.
 template <int DY, int DH, int DX, int VPT, bool POST>
@@ -242,7 +242,7 @@ extern "C" bq_status bq_residual_norm(const bq_residual_norm_desc* d, const void
     // Threads of a row: for few rows a vector each, as far as 512 threads go; for many two, so that what a row costs a
     // warp beside its vectors is shared.
     const int vecs = d->H / 8;
-    const int per = vecs > 2 * kMaxThreads ? 4 : vecs > kMaxThreads || d->T > kSms ? 2 : 1;
+    const int per = vecs > 512 || d->T > kSms ? 2 : 1;
     const int threads = ((vecs + per - 1) / per + 31) / 32 * 32, per_cta = std::max(1, 256 / threads);
     const dim3 grid((unsigned)(((int64_t)d->T + per_cta - 1) / per_cta)), block(threads, per_cta);
     cudaError_t e = cudaSuccess;
@@ -279,12 +279,10 @@ extern "C" bq_status bq_residual_norm(const bq_residual_norm_desc* d, const void
         auto go = [&](auto kernel) { e = bq::launch_after(kernel, grid, block, 0, (cudaStream_t)stream, a); };
         if (d->post_gain) {
             if (per == 1) go(residual_norm_kernel<D::y, D::h, D::x, 1, true>);
-            else if (per == 2) go(residual_norm_kernel<D::y, D::h, D::x, 2, true>);
-            else go(residual_norm_kernel<kAny, kAny, kAny, 4, true>);
+            else go(residual_norm_kernel<D::y, D::h, D::x, 2, true>);
         } else {
             if (per == 1) go(residual_norm_kernel<D::y, D::h, D::x, 1, false>);
-            else if (per == 2) go(residual_norm_kernel<D::y, D::h, D::x, 2, false>);
-            else go(residual_norm_kernel<kAny, kAny, kAny, 4, false>);
+            else go(residual_norm_kernel<D::y, D::h, D::x, 2, false>);
         }
     });
     return launched(name, e);

@@ -146,11 +146,11 @@ __device__ __forceinline__ float peer_load(const float* p, int rank) {
 // What the sums over a row go through.  Consecutive sums take different halves, so a half is written again only
 // behind the barrier of the sum between.
 struct SumBuf {
-    float warp[2][16][8];
+    float warp[2][32][8];
     float cta[2][8];
 };
 
-// One sum over the threads of a row, the same in each: lanes and warps (16 at most) by butterflies.
+// One sum over the threads of a row, the same in each: lanes and warps (32 at most) by butterflies.
 __device__ __forceinline__ float row_sum(float v, SumBuf& buf, int& turn) {
 #pragma unroll
     for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -159,15 +159,15 @@ __device__ __forceinline__ float row_sum(float v, SumBuf& buf, int& turn) {
     float (*mine)[8] = buf.warp[turn] + threadIdx.y * warps;
     if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5][0] = v;
     __syncthreads();
-    const int w = threadIdx.x & 15;
+    const int w = threadIdx.x & 31;
     v = w < warps ? mine[w][0] : 0.f;
 #pragma unroll
-    for (int off = 8; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     turn ^= 1;
     return v;
 }
 
-// Two sums, the same way: a lane holds one of them after the first exchange.
+// Two sums of 16 warps at most, the same way: a lane holds one of them after the first exchange.
 __device__ __forceinline__ void row_sums(float& v0, float& v1, SumBuf& buf, int& turn) {
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const bool upper = lane & 16;
