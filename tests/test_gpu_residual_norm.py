@@ -155,6 +155,15 @@ def test_gates_and_norms(lib, gate, sig, post, t, h, types):
         check_backward(lib, c, out, with_dx, with_dh)
 
 
+@pytest.mark.parametrize("types", [TYPES[2], TYPES[4], TYPES[5]], ids="-".join)
+@pytest.mark.parametrize("t,h,gate,post", [(330, 8192, "full", True), (400, 4096, "full", True), (310, 8192, "channel", True),
+                                           (311, 8200, "full", True), (305, 2056, "token", False), (900, 64, "full", True)])
+def test_many_wide_rows(lib, types, t, h, gate, post):
+    """Rows of which few, or none ahead, fit into shared memory; more rows than blocks."""
+    c = Case(t, t, h, types, "f32", post, gate, True, 0.5, 1.0)
+    check_backward(lib, c, check_forward(lib, c))
+
+
 def test_a_prefill_batch(lib):
     c = Case(1, 2047, 4096, TYPES[1], "bf16", True, "channel", False, 1.0, 1.0)
     out = check_forward(lib, c)
