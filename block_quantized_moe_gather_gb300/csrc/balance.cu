@@ -23,6 +23,7 @@ using namespace bq;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSequences = 65536;
+constexpr int kMaxRows = INT32_MAX - 64;   // a warp's row behind its last, 16 further on, is still an int
 constexpr float kLog2E = 1.4426950408889634f;
 
 enum { RULE_SOFTMAX = 0, RULE_SCORE = 1 };
@@ -863,7 +864,7 @@ void with_share(int E, bool vec, F f) {
 }
 
 bq_status check_router(const char* name, int T, int E, int k, int scoring, const int32_t* offsets, int S) {
-    if (T < 0) return bq::fail(BQ_ERR_SHAPE, "%s: T = %d < 0", name, T);
+    if (T < 0 || T > kMaxRows) return bq::fail(BQ_ERR_SHAPE, "%s: T = %d outside [0, %d]", name, T, kMaxRows);
     if (E < 1 || E > 1024) return bq::fail(BQ_ERR_SHAPE, "%s: E = %d outside [1, 1024]", name, E);
     if (k < 1 || k > 8 || k > E) return bq::fail(BQ_ERR_SHAPE, "%s: k = %d outside [1, min(8, E)]", name, k);
     if ((int64_t)T * k > (int64_t)INT32_MAX)
@@ -926,7 +927,7 @@ int share_of(int warps, int64_t slots, int S, int E) {
 }  // namespace
 
 extern "C" size_t bq_moe_balance_workspace_bytes(int32_t T, int32_t E, int32_t S) {
-    if (T < 0 || E < 1 || E > 1024 || S < 1 || S > kMaxSequences) return 0;
+    if (T < 0 || T > kMaxRows || E < 1 || E > 1024 || S < 1 || S > kMaxSequences) return 0;
     const size_t slots = (size_t)balance_chunking(T).chunks + S;
     return 2 * up256(slots * E * 4) + up256(slots * 4) + up256((size_t)S * ((E + 31) / 32) * 8) + 256;
 }
@@ -980,7 +981,7 @@ extern "C" bq_status bq_moe_balance_loss(const float* logits, const float* bias,
 }
 
 extern "C" size_t bq_moe_route_backward_workspace_bytes(int32_t T, int32_t E) {
-    if (T < 0 || E < 1 || E > 1024) return 0;
+    if (T < 0 || T > kMaxRows || E < 1 || E > 1024) return 0;
     return up256((size_t)std::max(1, gradient_chunking(T, true).chunks) * E * 4);
 }
 

@@ -672,8 +672,8 @@ bq_status bq_residual_norm_backward(const bq_residual_norm_desc* desc, const voi
  * rows written (BQ_SCORE_SOFTMAX only), or NULL; it alone needs the workspace.
  *
  * logits: device fp32 [T][E]; ids int32 [T][k]; counts int32 [S][E]; probs fp32
- * [S][E]; losses fp32 [2]; all 4-byte aligned, dlogits to its element.  E in
- * 1..1024, k in 1..min(8, E), S in 1..65536.  workspace: device, 256-byte
+ * [S][E]; losses fp32 [2]; all 4-byte aligned, dlogits to its element.  T at
+ * most 2^31 - 65 and T * k below 2^31, E in 1..1024, k in 1..min(8, E), S in 1..65536.  workspace: device, 256-byte
  * aligned, at least bq_moe_balance_workspace_bytes(T, E, S) or
  * bq_moe_route_backward_workspace_bytes(T, E) bytes (0: invalid sizes); nothing in
  * it is read before it is written.  Calls that may overlap on the GPU (other

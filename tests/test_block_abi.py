@@ -134,3 +134,11 @@ def test_host_structs_have_the_size_that_the_header_gives(bq, tmp_path):
     subprocess.run([cc, "-I", os.path.join(os.path.dirname(PKG), "include"), str(src), "-o", str(exe)], check=True)
     got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
     assert got == [bq._EPILOGUE.size, 16, 24, bq._RESIDUAL_NORM_DESC.size, 36, 72]
+
+
+def test_more_rows_than_an_int_steps_over_are_refused(bq):
+    n = 2 ** 31 - 1
+    assert balance(bq, T=n, E=1, k=1, n=1 << 40) == SHAPE
+    assert gradient(bq, T=n, E=1, k=1) == SHAPE
+    assert bq.moe_balance_workspace_bytes(n, 1, 1) == 0 and bq.moe_route_backward_workspace_bytes(n, 1) == 0
+    assert bq.moe_balance_workspace_bytes(n - 64, 1, 1) > 0
