@@ -159,14 +159,15 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
         float sums[8] = {sum2(hh), sum2(dh), sum2(yy), sum2(in_dout), sum2(in_dx), sum2(in_h), 0.f, 0.f};
         if (CLUSTER || POST || token) row_sums<CLUSTER>(sums, s_buf, turn, ranks);
         else if (has_x) row_sums(sums[0], sums[1], s_buf, turn);
-        // a row behind the last has sums of 0, whose roots would be infinite without eps
-        const float r = live ? rsqrtf(__fmaf_rn(sums[0], inv_h, a.eps)) : 0.f, c = -r * r * r * (sums[1] * inv_h);
+        // a row behind the last has sums of 0, whose roots would be infinite without eps; cubes of the roots are taken
+        // factor by factor, as they leave fp32's range where their products with the sums do not
+        const float r = live ? rsqrtf(__fmaf_rn(sums[0], inv_h, a.eps)) : 0.f, c = -r * (r * (r * (sums[1] * inv_h)));
         const float s = !POST ? 1.f : live ? rsqrtf(__fmaf_rn(sums[2], inv_h, a.eps)) : 0.f;
         float inner = sums[3];           // of P w G y
         if (has_x) inner += r * sums[4] + c * sums[5];
         if (token && live && threadIdx.x == 0 && rank == 0)
             reinterpret_cast<float*>(a.dgate.p)[t] = s * inner * (gate.sigmoid ? f * (1.f - f) : 1.f);
-        const float fs = f * s, cy = -fs * s * s * (inner * inv_h);
+        const float fs = f * s, cy = -fs * (s * (s * (inner * inv_h)));
         uint8_t* to_dh = a.dh.row(t0) + o_dh;
         uint8_t* to_dy = a.dy.row(t0) + o_dy;
 #pragma unroll

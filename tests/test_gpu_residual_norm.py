@@ -164,6 +164,19 @@ def test_many_wide_rows(lib, types, t, h, gate, post):
     check_backward(lib, c, check_forward(lib, c))
 
 
+@pytest.mark.parametrize("h", [4096, 9000])
+@pytest.mark.parametrize("which", ["y", "h"])
+def test_gradients_of_tiny_rows_without_eps(lib, which, h):
+    """1 / rms is 2^45: its cube leaves fp32's range, what it is multiplied with brings the product back."""
+    c = Case(3, 9, h, TYPES[2], "f32", True, "channel", True, 0.5, 1.25)
+    c.more["eps"] = 0.0
+    if which == "y":
+        c.y, c.y64 = c.y * 2.0 ** -46, c.y64 * 2.0 ** -46
+    else:
+        c.h_in, c.h64 = c.h_in * 2.0 ** -46, c.h64 * 2.0 ** -46
+    check_backward(lib, c, c.h_in)
+
+
 def test_a_prefill_batch(lib):
     c = Case(1, 2047, 4096, TYPES[1], "bf16", True, "channel", False, 1.0, 1.0)
     out = check_forward(lib, c)
