@@ -25,6 +25,7 @@ struct ForwardArgs {
 };
 
 constexpr int kMaxThreads = 1024;
+constexpr int kThreadsOfGpu = 1024 * kSms;   // of residual_norm_kernel that fit at once: 64 registers each
 
 // blockDim.x threads take a row, a thread the vectors x, x + blockDim.x, ... of it; blockDim.y rows a CTA.
 template <int DY, int DH, int DX, int VPT, bool POST>
@@ -244,18 +245,22 @@ extern "C" bq_status bq_residual_norm(const bq_residual_norm_desc* d, const void
     const ForwardArgs a{d->T, d->H, rows(y, ldy, d->y_dtype), rows(h, ldh, d->h_dtype), rows(h_out, ldho, d->h_dtype),
                         rows(x, ldx, x_dtype), full_gate ? rows(d->gate, d->ldgate, d->gate_dtype) : Rows{},
                         columns_of(d, x != nullptr), d->residual_scale, d->eps};
-    // Threads of a row: for few rows a vector each, as far as 512 threads go; for many two, so that what a row costs a
-    // warp beside its vectors is shared.
+    // Threads of a row: a vector each while all rows are on the SMs at once that way (200 x 2048 2.8 us against 3.4 with
+    // two, 200 x 4096 3.4 against 3.7; 600 x 4096 8.7 against 6.0); rows of one warp leave it no fewer threads with two
+    // (4000 x 256 3.3 us with one, 2.8 with two).
     const int vecs = d->H / 8;
-    const int per = vecs > 512 || d->T > kSms ? 2 : 1;
+    const int64_t all_vecs = (int64_t)d->T * vecs;
+    const int per = vecs > 512 || vecs <= 32 || all_vecs > kThreadsOfGpu ? 2 : 1;
     const int threads = ((vecs + per - 1) / per + 31) / 32 * 32, per_cta = std::max(1, 256 / threads);
     const dim3 grid((unsigned)(((int64_t)d->T + per_cta - 1) / per_cta)), block(threads, per_cta);
     cudaError_t e = cudaSuccess;
     bool done = false;
-    // many rows, of which a block of 256 or 512 threads holds one or more; two vectors a thread where one does not do
+    // More rows than the SMs hold at once with two vectors a thread, of which a block of 256 or 512 threads holds one or
+    // more; two vectors a thread where one does not do.  (600 x 4096: 7.6 us this way, 6.0 loaded directly; 1216 x 2048
+    // 6.9 and 6.1; 912 x 4096 8.5 and 9.8; 1824 x 2048 8.7 and 9.9; 2048 x 4096 14.4 and 16.2.)
     const int wide_block = vecs > 512 ? 512 : 256, vpt = vecs > 256 ? 2 : 1;
     const int far = std::max({a.y.ld16, a.h.ld16, a.out.ld16, a.x.ld16, a.full.ld16});
-    if (d->T > 2 * kSms && vecs <= 1024 && far <= INT32_MAX / 256) {   // offsets inside a block's rows are ints
+    if (all_vecs > 2 * kThreadsOfGpu && vecs <= 1024 && far <= INT32_MAX / 256) {   // offsets inside a block's rows are ints
         with_types(d->y_dtype, d->h_dtype, x_dtype, full_dtype, [&](auto type) {
             using D = decltype(type);
             const bool branch = d->post_gain || d->gate_kind == BQ_GATE_CHANNEL;
