@@ -216,29 +216,44 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
             if (stored) store8<DY>(to_dy, v * blockDim.x, a.dy.dtype, G);
         }
     }
-    // the block's column sums: its rows added up in shared memory (the stages are free), then to its part
+    // The block's column sums, to its part: a block of one row has them in its threads; of several, they are added up in
+    // shared memory (the stages and constants are free, and hold more than two sums).
     const int64_t parts = gridDim.x / ranks, part = blockIdx.x / ranks;
-    const int which[2] = {a.sum_gain, a.sum_branch};
-    float* s_sum = reinterpret_cast<float*>(smem);
+    auto part_of = [&](int which) { return reinterpret_cast<uint8_t*>(a.part + (which * parts + part) * a.H); };
     asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        if (which[k] < 0) continue;
-        uint8_t* out = reinterpret_cast<uint8_t*>(a.part + (which[k] * parts + part) * a.H);
-        if (blockDim.y > 1) __syncthreads();
+    if (blockDim.y == 1) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             if (!has[v]) continue;
-            const Vec& sum = k ? branch[v] : gain_sum[v];
-            if (blockDim.y == 1) store8<BQ_DT_F32>(out, vec0 + v * blockDim.x, 0, sum);
-            else store8<BQ_DT_F32>(smem, threadIdx.y * vecs + threadIdx.x + v * blockDim.x, 0, sum);
+            if (a.sum_gain >= 0) store8<BQ_DT_F32>(part_of(a.sum_gain), vec0 + v * blockDim.x, 0, gain_sum[v]);
+            if (a.sum_branch >= 0) store8<BQ_DT_F32>(part_of(a.sum_branch), vec0 + v * blockDim.x, 0, branch[v]);
         }
-        if (blockDim.y == 1) continue;
+    } else if (a.sum_gain >= 0 || a.sum_branch >= 0) {   // blocks of several rows are not clusters
+        const int rows = blockDim.y, quads = 2 * vecs;
+        float4* s_sum = reinterpret_cast<float4*>(smem);   // [array][row][quads]
         __syncthreads();
-        for (int i = tid; i < a.H; i += blockDim.x * blockDim.y) {   // blocks of several rows are not clusters
-            float sum = 0.f;
-            for (int j = 0; j < (int)blockDim.y; ++j) sum += s_sum[j * a.H + i];
-            reinterpret_cast<float*>(out)[i] = sum;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            if (!has[v]) continue;
+            const int at = threadIdx.y * vecs + threadIdx.x + v * blockDim.x;
+            if (a.sum_gain >= 0) store8<BQ_DT_F32>(smem, at, 0, gain_sum[v]);
+            if (a.sum_branch >= 0) store8<BQ_DT_F32>(smem + (int64_t)a.sum_branch * rows * quads * 16, at, 0, branch[v]);
+        }
+        __syncthreads();
+        const int arrays = 1 + max(a.sum_gain, a.sum_branch);
+        for (int i = tid; i < arrays * quads; i += blockDim.x * rows) {
+            const int k = i >= quads, c = i - k * quads;
+            const float4* from = s_sum + k * rows * quads + c;
+            float4 sum = from[0];
+#pragma unroll 4
+            for (int j = 1; j < rows; ++j) {
+                const float4 t = from[j * quads];
+                sum.x += t.x;
+                sum.y += t.y;
+                sum.z += t.z;
+                sum.w += t.w;
+            }
+            reinterpret_cast<float4*>(part_of(k))[c] = sum;
         }
     }
     if (CLUSTER) cluster_sync();   // peers may still be reading this CTA's sums
@@ -315,8 +330,11 @@ Shape shape_of(int T, int H, int n_planes, int n_constants) {
         p.slice = (vecs + p.cluster - 1) / p.cluster;
         p.block = p.slice > 512 ? 512 : 256;
         p.vpt = 2;
-        // two vectors a thread share what a row costs a warp beside them; one where that brings a second CTA to the SM
-        if (p.cluster == 1 && p.slice <= 256 && !fit(2)) p.vpt = 1;
+        // Two vectors a thread share what a row costs a warp beside them (16384 x 2048 bf16 71 us, one a thread 88; 2400 x
+        // 512 10.6 and 10.5).  One where that brings a second CTA to the SM (2048 x 1536 fp32 25.2 us against 27.6), where
+        // rows are a warp each way (2400 x 256 7.8 against 8.8), and where a block an SM takes all rows (16 x 2048 5.2
+        // against 6.5, 300 x 1024 6.0 against 7.4; 600 x 1024 8.1 and 7.5).
+        if (p.cluster == 1 && p.slice <= 256 && (!fit(2) || p.slice <= 32 || (int64_t)T * p.slice <= kSms * 256)) p.vpt = 1;
         if (p.slice <= 1024 && bytes(1) <= kSmemOfSm) break;
     }
     p.threads = ((p.slice + p.vpt - 1) / p.vpt + 31) / 32 * 32;
@@ -325,7 +343,7 @@ Shape shape_of(int T, int H, int n_planes, int n_constants) {
     p.stages = (bytes(3) + 2048) * per_sm <= kSmemOfSm ? 3 : bytes(2) <= kSmemOfSm ? 2 : 1;
     p.stage_bytes = n_planes * p.block * p.vpt * 16;
     p.at_stages = n_constants * p.block * p.vpt * 16;
-    p.smem = bytes(p.stages);   // room for the block's column sums too, 32 bytes per vector
+    p.smem = bytes(p.stages);   // room for the block's two column sums too, 64 bytes per vector: six planes at least
     // clusters of 1, 2, 4 and 8 CTAs that this GPU holds at once, with one CTA an SM
     const int held = p.cluster == 1 ? kSms : p.cluster == 2 ? 76 : p.cluster == 4 ? 36 : 15;
     p.blocks = (int)std::min<int64_t>(held * per_sm, ((int64_t)T + p.rows - 1) / p.rows);
