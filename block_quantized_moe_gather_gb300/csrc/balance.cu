@@ -841,11 +841,14 @@ Chunking chunking(int T, int most, int least) {
     return {rows, (int)(((int64_t)T + rows - 1) / rows)};
 }
 
-constexpr int kOneClusterRows = 1024;
+// As many rows go to one cluster, which adds its chunks' sums up itself: what a second launch costs the host (1.2 us) is
+// saved, and on the GPU both take the same (200 x 256: statistics 6.1 us, gradient with that of the bias 5.8 and 5.6 in
+// two launches; 400 x 128 6.5 and 6.0, 6.4 and 4.8).
+constexpr int kOneClusterRows = 256;
 
 Chunking balance_chunking(int T) { return T <= kOneClusterRows ? chunking(T, 8, kWarps) : chunking(T, 2 * kSms, kWarps); }
 
-// One cluster for few rows where there is a bias gradient to add up over them.
+// There the cluster is for the sums of a bias gradient.
 Chunking gradient_chunking(int T, bool bias) {
     return bias && T <= kOneClusterRows ? chunking(T, 8, kWarps) : chunking(T, 2 * kSms, kWarps);
 }
