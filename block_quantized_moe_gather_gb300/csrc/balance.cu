@@ -261,7 +261,7 @@ struct BalanceArgs {
     int32_t* part_c;     // [chunks + S][E]
     float* part_z;       // [chunks + S]
     float* part_loss;    // [S * groups of 32 experts][2]
-    int* ended;          // CTAs of balance_finish_kernel that have ended
+    int* ended;          // CTAs of balance_finish_kernel that have ended; sequences that have rows; their rows
     int32_t* counts;
     float* probs;
     float* losses;
@@ -280,7 +280,13 @@ __device__ __forceinline__ void chunk_sums(const BalanceArgs& a, float* s_red, i
     const int row0 = (int)first, row1 = (int)min((int64_t)a.T, first + a.chunk_rows);
     float z[NPER];
     if (kAhead && row0 + warp < row1) Row::load(a.logits + (int64_t)(row0 + warp) * a.E, a.bias, a.E, lane, z);
-    for (int s = sequence_totals(a.offsets, a.S, a.T, row0, a.status).before; s < a.S; ++s) {
+    const Totals totals = sequence_totals(a.offsets, a.S, a.T, row0, a.status);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {   // for balance_finish_kernel
+        a.ended[0] = 0;
+        a.ended[1] = totals.used;
+        a.ended[2] = totals.rows;
+    }
+    for (int s = totals.before; s < a.S; ++s) {
         int lo, hi;
         sequence(a.offsets, s, a.T, a.status, lo, hi);
         if (lo >= row1) break;
@@ -464,7 +470,6 @@ balance_kernel(const __grid_constant__ BalanceArgs a, int share, int one) {
     bq::grid_dependency_wait();   // launched behind whatever precedes it on the stream
     bq::allow_dependents();
     int32_t* hist = reinterpret_cast<int32_t*>(s_dyn + sums_words(a.E));
-    if (!one && blockIdx.x == 0 && threadIdx.x == 0) *a.ended = 0;
     chunk_sums<NPER, VEC, RULE>(a, s_dyn, hist);
     if (one) {
         const int ranks = gridDim.x;
@@ -482,12 +487,14 @@ balance_finish_kernel(const __grid_constant__ BalanceArgs a) {
     __shared__ int32_t s_redc[kWarps][32];
     __shared__ float s_sum[2][kWarps];
     __shared__ int s_last;
-    bq::grid_dependency_wait();
-    bq::allow_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = (a.E + 31) / 32;
     const int s = blockIdx.x / blocks, block = blockIdx.x - s * blocks, e = block * 32 + lane;
+    // balance_kernel does not write the offsets, and lets this kernel start only once what came before it has ended: they
+    // are read before the wait
     int lo, hi;
     sequence(a.offsets, s, a.T, a.status, lo, hi);
+    bq::grid_dependency_wait();
+    bq::allow_dependents();
     GroupSums r = add_slots(a, s, block, lo, hi, warp, kWarps);
     s_red[warp][lane] = r.p;
     s_redc[warp][lane] = r.c;
@@ -514,7 +521,7 @@ balance_finish_kernel(const __grid_constant__ BalanceArgs a) {
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    const Totals totals = sequence_totals(a.offsets, a.S, a.T, 0, a.status);
+    const int n = threadIdx.x < 2 ? __ldcg(a.ended + 1 + threadIdx.x) : 0;
     float sum[2] = {0.f, 0.f};
     for (int g = threadIdx.x; g < (int)gridDim.x; g += kThreads) {
         sum[0] += __ldcg(a.part_loss + 2 * g);
@@ -529,7 +536,6 @@ balance_finish_kernel(const __grid_constant__ BalanceArgs a) {
     if (threadIdx.x < 2) {
         float v = 0.f;
         for (int w = 0; w < kWarps; ++w) v += s_sum[threadIdx.x][w];
-        const int n = threadIdx.x ? totals.rows : totals.used;
         a.losses[threadIdx.x] = n ? v / (float)n : 0.f;
     }
 }

@@ -275,18 +275,20 @@ __global__ void __launch_bounds__(kSumThreads)
 sum_parts_kernel(const SumArgs a) {
     constexpr int kWarps = kSumThreads / 32;
     __shared__ float s_red[kWarps][32];
-    bq::grid_dependency_wait();
-    bq::allow_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     const float* part = a.part + (int64_t)blockIdx.y * a.parts * a.H;
     const Gate& gate = a.columns.gate;
     const bool branch = (int)blockIdx.y == a.sum_branch;
-    float f = 1.f, post = 1.f, sum = 0.f;   // the constants are on their way while the parts are
+    float f = 1.f, post = 1.f, sum = 0.f;
+    // Behind residual_norm_backward_kernel, which writes neither gains nor gate and lets this kernel start only once
+    // what came before it has ended: the constants are read before the wait.
+    if (branch && warp == 0 && c < a.H && a.parts) {   // without rows (and that kernel) the gate and the gains may be missing
+        if (gate.kind == GATE_CHANNEL) f = load1(gate.p, c, gate.dtype);
+        if (a.columns.post) post = load1(a.columns.post, c, a.columns.gain_dtype);
+    }
+    bq::grid_dependency_wait();
+    bq::allow_dependents();
     if (c < a.H) {
-        if (branch && warp == 0 && a.parts) {   // without rows the gate and the gains may be missing
-            if (gate.kind == GATE_CHANNEL) f = load1(gate.p, c, gate.dtype);
-            if (a.columns.post) post = load1(a.columns.post, c, a.columns.gain_dtype);
-        }
 #pragma unroll 8
         for (int64_t i = warp; i < a.parts; i += kWarps) sum += part[i * a.H + c];
     }
