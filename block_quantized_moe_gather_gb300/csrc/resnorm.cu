@@ -9,6 +9,12 @@
 //   G = dh' + r gain dx - h' r^3 mean(gain dx h'),   dgain = sum_t dx h' r
 //   dh = residual_scale G,   D = scale G,   dgate = D b (times g (1 - g) under a sigmoid)
 //   dpost = sum_t D g y s,   dy = s post D g - y s^3 mean(post D g y), or D g without a post norm
+//
+// Every value of y and h is read once and every value of h' and x written once; with many rows that is what bounds the
+// pass (GB300, bf16, post norm, gate per channel: 8192 x 4096 44 us, 6.1 TB/s; 2048 x 4096 15.3 us, 4.4 TB/s, of which
+// about 4 us are the start and the last rows).  A row has two sums that depend on one another (y^2, then h'^2), so rows
+// loaded when their turn comes leave the memory idle in between: where rows outnumber what the SMs hold at once, blocks
+// fetch theirs ahead.  Few rows are bound by the latency of one (1 x 4096 2.1 us).
 #include "resnorm.cuh"
 
 namespace {
@@ -94,8 +100,10 @@ residual_norm_kernel(const __grid_constant__ ForwardArgs a) {
     }
 }
 
-// The same for many rows (a vector behind a row's last is zeros): blocks walk over them with the next rows on their way (resnorm.cuh) and the columns' constants
-// kept as fp32, so that the loads' latency and the conversions of the gains are not paid row by row.
+// The same for many rows (a vector behind a row's last is zeros): blocks walk over them with the next rows on their way
+// (resnorm.cuh) and the columns' constants kept as fp32, so that the loads' latency and the conversions of the gains are
+// not paid row by row.  2048 x 4096 bf16: 14.4 us (rows loaded directly 16.2); it issues in half of the cycles, at 24
+// warps an SM.
 struct ManyArgs {
     ForwardArgs f;
     int stages, stage_bytes, at_stages, at_branch;   // bytes; at_branch -1: the branch's constant is scale alone

@@ -9,6 +9,15 @@
 // folded in at the end.  The sum of P w G y is linear in G = dh' + r gain dx - h' c:
 // its three parts need neither r nor c, so every sum over a row is formed in one
 // pass and one barrier, and a second pass writes all outputs.
+//
+// Four rows are read and two written (GB300, bf16, post norm, gate per channel:
+// 8192 x 4096 72 us, 5.6 TB/s; 2048 x 4096 27 us, 3.7 TB/s; fp32 stream and a gate
+// per value 2047 x 2048 23.6 us).  What bounds it there is issue and latency: the
+// sums and both rows' worth of packed arithmetic take 114 to 122 registers, so an
+// SM holds 16 warps, which issue in half of the cycles; the column sums' second
+// kernel takes 3 to 5 us.  Steps that led here, 2048 x 4096: rows fetched ahead
+// 85 -> 48 us, packed arithmetic and constants kept as fp32 37, two blocks an SM
+// 31, all sums of a row in one barrier 28.
 #include "resnorm.cuh"
 
 namespace {
@@ -190,7 +199,8 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
                 for (int j = 0; j < 4; ++j) o.p[j] = mul2(G.p[j], both(a.residual_scale));
                 store8<DH>(to_dh, v * blockDim.x, a.dh.dtype, o);
             }
-            const Vec p = branch_kept ? kept8<PLANE, VPT>(own + L::kBranch, v) : same8(a.columns.scale), y = staged8<DY, PLANE, VPT>(st + L::kY, v, a.y.dtype);
+            const Vec p = branch_kept ? kept8<PLANE, VPT>(own + L::kBranch, v) : same8(a.columns.scale);
+            const Vec y = staged8<DY, PLANE, VPT>(st + L::kY, v, a.y.dtype);
             if (full) {
                 Vec w = staged8<DY, PLANE, VPT>(st + L::kGate, v, a.full.dtype), dw;
 #pragma unroll
@@ -271,6 +281,8 @@ struct SumArgs {
 constexpr int kSumThreads = 512;
 
 // The parts of 32 columns of one array (blockIdx.y) added up, each warp a share of them, and its gradients' constants.
+// Bound by latency: 304 parts of two sums of 4096 columns (10 MB, in the L2) take 3 to 4 us behind the first kernel.
+// All 19 parts of a warp in flight at once, or blocks of 1024 threads, took longer.
 __global__ void __launch_bounds__(kSumThreads)
 sum_parts_kernel(const SumArgs a) {
     constexpr int kWarps = kSumThreads / 32;
