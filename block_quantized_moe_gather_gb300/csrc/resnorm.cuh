@@ -238,17 +238,20 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// A thread's vectors of a row into a stage.
+// A thread's vector v of a row into a stage; all of its vectors.
+template <int DT, int PLANE, int VPT>
+__device__ __forceinline__ void fetch_one(uint32_t dst, const uint8_t* src, int dtype, int v) {
+    const bool wide = (DT == kAny ? dtype : DT) == BQ_DT_F32;
+    const uint8_t* p = src + v * (int)blockDim.x * (wide ? 32 : 16);
+    copy16_async(dst + v * (PLANE / VPT), p);
+    if (wide) copy16_async(dst + v * (PLANE / VPT) + PLANE, p + 16);
+}
+
 template <int DT, int PLANE, int VPT>
 __device__ __forceinline__ void fetch(uint32_t dst, const uint8_t* src, int dtype, const bool (&has)[VPT]) {
-    const bool wide = (DT == kAny ? dtype : DT) == BQ_DT_F32;
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        if (!has[v]) continue;
-        const uint8_t* p = src + v * (int)blockDim.x * (wide ? 32 : 16);
-        copy16_async(dst + v * (PLANE / VPT), p);
-        if (wide) copy16_async(dst + v * (PLANE / VPT) + PLANE, p + 16);
-    }
+    for (int v = 0; v < VPT; ++v)
+        if (has[v]) fetch_one<DT, PLANE, VPT>(dst, src, dtype, v);
 }
 
 template <int DT, int PLANE, int VPT>

@@ -79,25 +79,34 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
     bq::grid_dependency_wait();
     bq::allow_dependents();
     const uint32_t own_u32 = (uint32_t)__cvta_generic_to_shared(own);
+    auto fetch_vector = [&](uint32_t to, int64_t r0, int v) {
+        fetch_one<DY, PLANE, VPT>(to + L::kY, a.y.row(r0) + o_y, a.y.dtype, v);
+        if (has_x) {
+            fetch_one<DH, PLANE, VPT>(to + L::kOut, a.out.row(r0) + o_out, a.out.dtype, v);
+            fetch_one<DX, PLANE, VPT>(to + L::kDx, a.dx.row(r0) + o_dx, a.dx.dtype, v);
+        }
+        if (a.dout.p) fetch_one<DH, PLANE, VPT>(to + L::kDout, a.dout.row(r0) + o_dout, a.dout.dtype, v);
+        if (full) fetch_one<DY, PLANE, VPT>(to + L::kGate, a.full.row(r0) + offset(a.full), a.full.dtype, v);
+    };
     auto fetch_row = [&](int stage, int64_t r0) {
         const uint32_t to = own_u32 + stage;
         if (r0 + threadIdx.y < a.T) {
-            fetch<DY, PLANE>(to + L::kY, a.y.row(r0) + o_y, a.y.dtype, has);
-            if (has_x) {
-                fetch<DH, PLANE>(to + L::kOut, a.out.row(r0) + o_out, a.out.dtype, has);
-                fetch<DX, PLANE>(to + L::kDx, a.dx.row(r0) + o_dx, a.dx.dtype, has);
-            }
-            if (a.dout.p) fetch<DH, PLANE>(to + L::kDout, a.dout.row(r0) + o_dout, a.dout.dtype, has);
-            if (full) fetch<DY, PLANE>(to + L::kGate, a.full.row(r0) + offset(a.full), a.full.dtype, has);
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+                if (has[v]) fetch_vector(to, r0, v);
         } else if (r0 < a.T) {
             for (int i = 0; i < a.stage_bytes; i += PLANE / VPT)
                 *reinterpret_cast<uint4*>(own + stage + i) = make_uint4(0, 0, 0, 0);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    // With room for one row only (blocks of 512 threads with one row at a time), a vector's place is filled again once the
+    // vector has been used for the last time (2048 x 8192 fp32 124 us, 127 with the whole row fetched at its turn; fp32
+    // stream between bf16 rows 88 and 92).
+    const bool refill = THREADS * VPT == 1024 && a.stages == 1;
     int ahead = a.at_stages;
     int64_t next = block0;
-    for (int i = 0; i < a.stages - 1; ++i) {
+    for (int i = 0; i < max(a.stages - 1, 1); ++i) {
         fetch_row(ahead, next);
         ahead += a.stage_bytes;
         next += step;
@@ -111,12 +120,10 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
     for (int64_t t0 = block0; t0 < a.T; t0 += step) {
         const int64_t t = t0 + threadIdx.y;
         const bool live = t < a.T;
-        if (a.stages == 1) fetch_row(ahead, t0);   // no room for a row ahead
         if (a.stages < 3) asm volatile("cp.async.wait_group 0;" ::: "memory");
         else asm volatile("cp.async.wait_group 1;" ::: "memory");
-        if (a.stages > 1) {
+        if (!refill) {
             fetch_row(ahead, next);
-            next += step;
             ahead = ahead + a.stage_bytes == end ? a.at_stages : ahead + a.stage_bytes;
         }
         const uint8_t* st = own + stage;
@@ -224,7 +231,10 @@ residual_norm_backward_kernel(const __grid_constant__ BackwardArgs a) {
                 if (POST) G.p[j] = fma2(y.p[j], both(cy), G.p[j]);
             }
             if (stored) store8<DY>(to_dy, v * blockDim.x, a.dy.dtype, G);
+            if (refill && has[v] && next < a.T) fetch_vector(own_u32 + a.at_stages, next, v);   // behind all uses above
         }
+        if (refill) asm volatile("cp.async.commit_group;" ::: "memory");
+        next += step;
     }
     // The block's column sums, to its part: a block of one row has them in its threads; of several, they are added up in
     // shared memory (the stages and constants are free, and hold more than two sums).
@@ -393,15 +403,10 @@ cudaError_t launch_rows(const Shape& p, const BackwardArgs& a, cudaStream_t st) 
 
 template <int DY, int DH, int DX, bool POST>
 cudaError_t launch_backward(const Shape& p, const BackwardArgs& a, cudaStream_t st) {
+    if (p.cluster > 1) return launch_rows<residual_norm_backward_kernel<DY, DH, DX, 512, 2, POST, true>>(p, a, st);
     if (p.vpt == 1) return launch_rows<residual_norm_backward_kernel<DY, DH, DX, 256, 1, POST, false>>(p, a, st);
     if (p.block == 256) return launch_rows<residual_norm_backward_kernel<DY, DH, DX, 256, 2, POST, false>>(p, a, st);
     return launch_rows<residual_norm_backward_kernel<DY, DH, DX, 512, 2, POST, false>>(p, a, st);
-}
-
-template <bool POST>
-cudaError_t launch_cluster(const Shape& p, const BackwardArgs& a, cudaStream_t st) {
-    if (p.block == 256) return launch_rows<residual_norm_backward_kernel<kAny, kAny, kAny, 256, 2, POST, true>>(p, a, st);
-    return launch_rows<residual_norm_backward_kernel<kAny, kAny, kAny, 512, 2, POST, true>>(p, a, st);
 }
 
 }  // namespace
@@ -478,9 +483,7 @@ extern "C" bq_status bq_residual_norm_backward(const bq_residual_norm_desc* d, c
             using D = decltype(type);
             constexpr bool POST = decltype(post)::value;
             const int constants = POST || channel ? 4 : 2;
-            auto shape = [&](int n) { p = shape_of(d->T, d->H, n, constants); };
-            shape((full ? 2 : 1) * planes(D::y) + 2 * planes(D::h) + planes(D::x));
-            if (p.cluster > 1) shape((full ? 2 : 1) * 2 + 2 * 2 + 2);   // the clusters' kernels leave two planes for every type
+            p = shape_of(d->T, d->H, (full ? 2 : 1) * planes(D::y) + 2 * planes(D::h) + planes(D::x), constants);
             if (p.rows > 1 && std::max({a.y.ld16, a.out.ld16, a.dout.ld16, a.dx.ld16, a.dy.ld16, a.dh.ld16, a.full.ld16,
                                         a.dgate.ld16}) > INT32_MAX / 256) {
                 // offsets inside a block's rows are ints: rows that far apart are taken one at a time
@@ -491,7 +494,7 @@ extern "C" bq_status bq_residual_norm_backward(const bq_residual_norm_desc* d, c
             a.stages = p.stages;
             a.stage_bytes = p.stage_bytes;
             a.at_stages = p.at_stages;
-            e = p.cluster > 1 ? launch_cluster<POST>(p, a, st) : launch_backward<D::y, D::h, D::x, POST>(p, a, st);
+            e = launch_backward<D::y, D::h, D::x, POST>(p, a, st);
         };
         with_types(d->y_dtype, d->h_dtype, x_dtype, full ? d->gate_dtype : d->y_dtype, [&](auto type) {
             if (d->post_gain) go(type, std::true_type());
