@@ -15,7 +15,7 @@
 // A warp takes a row, its logits in registers, the next row's on their way.  The logits are read once (and the
 // gradient written once), but issue bounds both passes before memory does (GB300, 16384 x 256, k = 8): the statistics
 // of scores over 9 sequences take 12.7 us, 2.5 at the copy bandwidth, of which the first kernel has 8 (three
-// special-function instructions a logit, packed arithmetic, 56% of the issue slots at 24 warps an SM; 3.4 rows a warp
+// special-function instructions a logit, packed arithmetic, 55% of the issue slots at 30 warps an SM; 3.4 rows a warp
 // leave a fifth of the last round idle) and the second, a chain of latencies, 4; the gradient of weights and losses
 // under the softmax rule takes 10.3 us, 5.1 at the copy bandwidth.  Few rows are latency (129 x 128: statistics 6.2 us,
 // gradient of weights alone 4.1).

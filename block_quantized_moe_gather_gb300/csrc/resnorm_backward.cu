@@ -11,9 +11,9 @@
 // pass and one barrier, and a second pass writes all outputs.
 //
 // Four rows are read and two written (GB300, bf16, post norm, gate per channel:
-// 8192 x 4096 72 us, 5.6 TB/s; 2048 x 4096 27 us, 3.7 TB/s; fp32 stream and a gate
-// per value 2047 x 2048 23.6 us).  What bounds it there is issue and latency: the
-// sums and both rows' worth of packed arithmetic take 114 to 122 registers, so an
+// 8192 x 4096 71 us, 5.7 TB/s; 2048 x 4096 27 us, 3.7 TB/s; fp32 stream and a gate
+// per value 2047 x 2048 24 us).  What bounds it there is issue and latency: the
+// sums and both rows' worth of packed arithmetic take 114 to 120 registers, so an
 // SM holds 16 warps, which issue in half of the cycles; the column sums' second
 // kernel takes 3 to 5 us.  Steps that led here, 2048 x 4096: rows fetched ahead
 // 85 -> 48 us, packed arithmetic and constants kept as fp32 37, two blocks an SM

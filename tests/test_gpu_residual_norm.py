@@ -219,6 +219,28 @@ def test_strides_and_in_place(lib):
         assert (w[-1] == 7).all() and (w[:, :8] == 7).all() and (w[:, 8 + 256:] == 7).all()
 
 
+@pytest.mark.parametrize("t,h", [(400, 8192), (320, 16384)])
+def test_wide_rows_in_place(lib, t, h):
+    """Rows fetched ahead (one at a time, and by a cluster) are not those that are written."""
+    import torch
+    c = Case(t, t, h, TYPES[2], "f32", True, "channel", True, 0.5, 1.0)
+    e = torch.empty_like
+    out, x = lib.residual_norm(c.y, c.h_in, e(c.h_in), e(c.y), **c.args())
+    ws = torch.empty(lib.residual_norm_backward_workspace_bytes(t, h), dtype=torch.uint8, device="cuda")
+
+    def back(dh):
+        sums = [torch.full((h,), np.nan, device="cuda") for _ in range(3)]
+        dy, _ = lib.residual_norm_backward(c.y, out, c.dh_out, c.dx, e(c.y), dh, **c.args(), dgain=sums[0], dpost_gain=sums[1],
+                                           dgate=sums[2], workspace=ws)
+        return [dy, dh, *sums]
+
+    want = back(e(c.dh_out))
+    for a, b in zip(want, back(c.dh_out)):      # dh is dh_out
+        assert (a == b).all()
+    lib.residual_norm(c.y, c.h_in, c.h_in, x2 := e(x), **c.args())      # h_out is h
+    assert (c.h_in == out).all() and (x2 == x).all()
+
+
 def test_no_rows_and_no_x(lib):
     import torch
     h, h_out = torch.randn(4, 64, device="cuda"), torch.empty(4, 64, device="cuda")
