@@ -177,6 +177,19 @@ def test_gradients_of_tiny_rows_without_eps(lib, which, h):
     check_backward(lib, c, c.h_in)
 
 
+@pytest.mark.parametrize("types", [TYPES[1], TYPES[3], TYPES[5]], ids="-".join)
+@pytest.mark.parametrize("t,h,gate,post", [(40001, 64, "token", True), (5003, 520, "channel", False), (1301, 2056, "full", True),
+                                           (622, 4104, "none", True), (313, 8000, "token", False)])
+def test_more_rows_than_fit_at_once(lib, types, t, h, gate, post):
+    """Blocks of one to eight rows that walk over the rows, and end inside a block's rows."""
+    check_forward(lib, Case(t, t, h, types, types[2], post, gate, True, 0.5, 1.25))
+
+
+def test_many_rows_of_few_values(lib):
+    c = Case(5, 9001, 72, TYPES[4], "f32", True, "channel", True, 0.5, 1.0)
+    check_backward(lib, c, check_forward(lib, c))
+
+
 def test_a_prefill_batch(lib):
     c = Case(1, 2047, 4096, TYPES[1], "bf16", True, "channel", False, 1.0, 1.0)
     out = check_forward(lib, c)
