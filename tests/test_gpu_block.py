@@ -240,3 +240,49 @@ def test_a_residual_beyond_32_bit_offsets(lib):
         want = O.product_end(v, f64(bias), "relu", 0.5, r)
         np.testing.assert_allclose(f64(y[a:a + 2]), want, rtol=2.0 ** -8, atol=1e-5)
     assert lib.device_status() == lib.DEV_OK
+
+
+def test_calls_behind_what_writes_their_inputs(lib):
+    """Second kernels read the gate, the gains and the offsets while the first is ending: written by a kernel or a copy just
+    before the call, on the same stream, they are the new ones; on two streams at once too."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(5)
+    t, h, e, k, n = 500, 1024, 64, 4, 6
+    rows = [torch.randn(t, h, generator=g, device="cuda") for _ in range(4)]
+    gates = torch.randn(n, h, generator=g, device="cuda")
+    logits = torch.randn(t, e, generator=g, device="cuda")
+    ids = torch.topk(logits, k).indices.int()
+    cuts = torch.randint(0, t + 1, (n, 4), generator=g, device="cuda").sort(1).values.int()
+
+    def state():
+        new = (lambda *s, d=torch.float32: torch.empty(*s, dtype=d, device="cuda"))
+        return dict(gate=new(h), post=new(h), off=new(4, d=torch.int32), dy=new(t, h), dh=new(t, h), dgain=new(h), dpost=new(h),
+                    dgate=new(h), counts=new(3, e, d=torch.int32), probs=new(3, e), losses=new(2),
+                    ws=new(lib.residual_norm_backward_workspace_bytes(t, h), d=torch.uint8),
+                    wb=new(lib.moe_balance_workspace_bytes(t, e, 3), d=torch.uint8))
+
+    def step(s, i):
+        torch.mul(gates[i], 1.0, out=s["gate"])
+        torch.add(gates[i], 2.0, out=s["post"])
+        lib.residual_norm_backward(*rows, s["dy"], s["dh"], gain=gates[0], post_gain=s["post"], gate=s["gate"], gate_sigmoid=True,
+                                   dgain=s["dgain"], dpost_gain=s["dpost"], dgate=s["dgate"], workspace=s["ws"])
+        s["off"].copy_(cuts[i])
+        lib.moe_balance_loss(logits, ids, s["counts"], s["probs"], s["losses"], s["wb"], seq_offsets=s["off"])
+        return [s[x].clone() for x in ("dy", "dh", "dgain", "dpost", "dgate", "counts", "probs", "losses")]
+
+    alone, one = [], state()
+    for i in range(n):
+        alone.append(step(one, i))
+        torch.cuda.synchronize()
+    streams, states = [torch.cuda.Stream(), torch.cuda.Stream()], [state(), state()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for i in range(n):
+        for j in range(2):
+            with torch.cuda.stream(streams[j]):
+                got[j].append(step(states[j], i if j == 0 else n - 1 - i))
+    torch.cuda.synchronize()
+    for i in range(n):
+        for a, b, c in zip(alone[i], got[0][i], got[1][n - 1 - i]):
+            assert torch.equal(a, b) and torch.equal(a, c)
