@@ -887,7 +887,7 @@ __device__ __forceinline__ void add_residual(const Args& a, int64_t row, int c, 
 // Bias of the values that a thread sums: acc[j] is column c0 + j of y, with SwiGLU the gate value of column c0 + j % 64
 // or its up value.  Each warp fetches its own copy to where its rows go through later: copies that nothing waits for
 // until the sums are done, and that need no registers meanwhile (a load into registers at this place made a block of K
-// 8% longer).
+// 8% longer).  end_rows waits for them: one call of each per item.
 template <bool SWIGLU>
 __device__ __forceinline__ void fetch_bias(const Args& a, int e, int c0, uint8_t* buf) {
     if (!a.bias) return;
@@ -1074,7 +1074,9 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             const int c0 = kTileCols * it.tile + kTileCols / 2 * half;
             const int o_lo = min(c0 / kBlock, a.nb - 1) * a.kb, o_hi = o_lo + a.nb / 2 * a.kb;
             uint8_t* buf = smem + M::kOut + (warp - 4) * 16 * kOutRow;
-            if (END != END_NONE) {   // on their way while the blocks are
+            // On their way while the blocks are.  A warp without rows of this item has no use for a bias, and does not
+            // come to the wait in end_rows: copies left in flight would meet those of its next item in the same place.
+            if (END != END_NONE && 32 * quarter < it.rows) {
                 fetch_bias<SWIGLU>(a, it.e, c0, buf);
                 if (RESIDUAL && p < it.rows) prefetch_residual(a, (int64_t)it.row0 + p, c0, SWIGLU ? 64 : 128);
             }
