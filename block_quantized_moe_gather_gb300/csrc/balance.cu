@@ -498,12 +498,10 @@ balance_finish_kernel(const __grid_constant__ BalanceArgs a) {
     __shared__ int s_last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = (a.E + 31) / 32;
     const int s = blockIdx.x / blocks, block = blockIdx.x - s * blocks, e = block * 32 + lane;
-    // balance_kernel does not write the offsets, and lets this kernel start only once what came before it has ended: they
-    // are read before the wait
+    bq::grid_dependency_wait();   // nothing before this line touches global memory, which earlier kernels may have written
+    bq::allow_dependents();
     int lo, hi;
     sequence(a.offsets, s, a.T, a.status, lo, hi);
-    bq::grid_dependency_wait();
-    bq::allow_dependents();
     GroupSums r = add_slots(a, s, block, lo, hi, warp, kWarps);
     s_red[warp][lane] = r.p;
     s_redc[warp][lane] = r.c;

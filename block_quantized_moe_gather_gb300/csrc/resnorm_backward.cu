@@ -302,14 +302,13 @@ sum_parts_kernel(const SumArgs a) {
     const Gate& gate = a.columns.gate;
     const bool branch = (int)blockIdx.y == a.sum_branch;
     float f = 1.f, post = 1.f, sum = 0.f;
-    // Behind residual_norm_backward_kernel, which writes neither gains nor gate and lets this kernel start only once
-    // what came before it has ended: the constants are read before the wait.
+    bq::grid_dependency_wait();   // nothing before this line touches global memory, which earlier kernels may have written
+    bq::allow_dependents();
+    // the constants, on their way beside the parts
     if (branch && warp == 0 && c < a.H && a.parts) {   // without rows (and that kernel) the gate and the gains may be missing
         if (gate.kind == GATE_CHANNEL) f = load1(gate.p, c, gate.dtype);
         if (a.columns.post) post = load1(a.columns.post, c, a.columns.gain_dtype);
     }
-    bq::grid_dependency_wait();
-    bq::allow_dependents();
     if (c < a.H) {
 #pragma unroll 8
         for (int64_t i = warp; i < a.parts; i += kWarps) sum += part[i * a.H + c];
