@@ -674,6 +674,16 @@ def _vector(where: str, what: str, t, n: int):
     return t.data_ptr(), dt
 
 
+def _workspace(where: str, t):
+    """(pointer, bytes) of a workspace, or (None, 0).  A tensor that holds fewer bytes than it has elements (an expanded
+    one) would be written past its end."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        _refuse(3, where, f"the workspace has shape {list(t.shape)} and strides {tuple(t.stride())}, expected a contiguous one")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _gate(where: str, gate, t: int, h: int):
     """(kind, pointer, bq_dtype, row stride) of a gate [T, 1], [H] or [T, H]."""
     if gate is None:
@@ -754,7 +764,7 @@ def residual_norm_backward(y, h_out, dh_out, dx, dy, dh, gain=None, post_gain=No
             pgate, _, _, _, ldgate = _rows_of(where, "dgate", dgate, t, n, gate_dt)
         else:
             pgate = _dense(where, "dgate", dgate, gate.shape, "f32")
-    pw, nw = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    pw, nw = _workspace(where, workspace)
     _check(_lib.bq_residual_norm_backward(desc, py, ldy, ph, ldh, po, ldo, px, ldx, pd, ldd, pg, ldg,
                                           *sums, pgate, ldgate, pw, nw, st), where)
     return dy, dh
@@ -794,8 +804,8 @@ def moe_balance_loss(logits, ids, counts, probs, losses, workspace, bias=None, s
     pc = _dense(where, "counts", counts, (s, e), "i32")
     pp = _dense(where, "probs", probs, (s, e), "f32")
     po = _dense(where, "losses", losses, (2,), "f32")
-    _check(_lib.bq_moe_balance_loss(pl, pb, t, e, pi, k, scoring, ps, s, pc, pp, po, workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(), st), where)
+    _check(_lib.bq_moe_balance_loss(pl, pb, t, e, pi, k, scoring, ps, s, pc, pp, po, *_workspace(where, workspace), st),
+           where)
     return counts, probs, losses
 
 
@@ -820,7 +830,7 @@ def moe_route_backward(logits, ids, dweights, dlogits, bias=None, scoring: int =
                                             ("counts", counts, (s, e), "i32"), ("dlosses", dlosses, (2,), "f32"),
                                             ("dbias", dbias, (e,), "f32"))]
     pb, pw, pc, pd, pdb = vectors
-    ws, nw = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    ws, nw = _workspace(where, workspace)
     _check(_lib.bq_moe_route_backward(pl, pb, t, e, pi, k, scoring, scale, pw, pc, pd, ps, s, po, dt, pdb, ws, nw, st),
            where)
     return dlogits
