@@ -20,6 +20,7 @@
 // under the softmax rule takes 10.3 us, 5.1 at the copy bandwidth.  Few rows are latency (129 x 128: statistics 6.2 us,
 // gradient of weights alone 4.1).
 #include <algorithm>
+#include <atomic>
 
 #include "packed_f32.cuh"
 #include "row_types.cuh"
@@ -31,6 +32,7 @@ using namespace bq;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSequences = 65536;
+constexpr int kMaxExperts = 1024;
 constexpr int kMaxRows = INT32_MAX - 64;   // a warp's row behind its last, 16 further on, is still an int
 constexpr float kLog2E = 1.4426950408889634f;
 
@@ -882,7 +884,7 @@ void with_share(int E, bool vec, F f) {
 
 bq_status check_router(const char* name, int T, int E, int k, int scoring, const int32_t* offsets, int S) {
     if (T < 0 || T > kMaxRows) return bq::fail(BQ_ERR_SHAPE, "%s: T = %d outside [0, %d]", name, T, kMaxRows);
-    if (E < 1 || E > 1024) return bq::fail(BQ_ERR_SHAPE, "%s: E = %d outside [1, 1024]", name, E);
+    if (E < 1 || E > kMaxExperts) return bq::fail(BQ_ERR_SHAPE, "%s: E = %d outside [1, %d]", name, E, kMaxExperts);
     if (k < 1 || k > 8 || k > E) return bq::fail(BQ_ERR_SHAPE, "%s: k = %d outside [1, min(8, E)]", name, k);
     if ((int64_t)T * k > (int64_t)INT32_MAX)
         return bq::fail(BQ_ERR_SHAPE, "%s: T * k = %lld pairs exceeds %d", name, (long long)T * k, INT32_MAX);
@@ -927,11 +929,25 @@ cudaError_t launch_cluster(Kernel kernel, int ctas, size_t smem, cudaStream_t st
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename Kernel>
-cudaError_t allow_smem(Kernel kernel, size_t smem) {
-    return smem <= 48 * 1024 ? cudaSuccess
-                             : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// Lets a kernel take more shared memory than 48 KB: the most that any call needs, set once per device (the attribute is a
+// property of the function on the current device; set to each call's own size, it could be lowered by another host thread
+// before a launch that needs more).
+template <auto kernel>
+cudaError_t allow_smem(size_t smem) {
+    if (smem <= 48 * 1024) return cudaSuccess;
+    static std::atomic<bool> attr_set[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const bool known = dev >= 0 && dev < 64;
+    if (known && attr_set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    const size_t most = balance_smem(kMaxExperts);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e == cudaSuccess && known) attr_set[dev].store(true, std::memory_order_release);
+    return e;
 }
+
+template <auto kernel>
+using Constant = std::integral_constant<decltype(kernel), kernel>;   // a kernel as an argument
 
 // Warps that share a group of 32 experts of a sequence: as many as there are for it, but two slots each at least.
 int share_of(int warps, int64_t slots, int S, int E) {
@@ -944,7 +960,7 @@ int share_of(int warps, int64_t slots, int S, int E) {
 }  // namespace
 
 extern "C" size_t bq_moe_balance_workspace_bytes(int32_t T, int32_t E, int32_t S) {
-    if (T < 0 || T > kMaxRows || E < 1 || E > 1024 || S < 1 || S > kMaxSequences) return 0;
+    if (T < 0 || T > kMaxRows || E < 1 || E > kMaxExperts || S < 1 || S > kMaxSequences) return 0;
     const size_t slots = (size_t)balance_chunking(T).chunks + S;
     return 2 * up256(slots * E * 4) + up256(slots * 4) + up256((size_t)S * ((E + 31) / 32) * 8) + 256;
 }
@@ -984,13 +1000,14 @@ extern "C" bq_status bq_moe_balance_loss(const float* logits, const float* bias,
     with_share(E, vec, [&](auto nper, auto v) {
         constexpr int N = decltype(nper)::value;
         constexpr bool VEC = decltype(v)::value;
-        auto go = [&](auto kernel) {
-            if ((e = allow_smem(kernel, balance_smem(E))) != cudaSuccess) return;
+        auto go = [&](auto constant) {
+            constexpr auto kernel = decltype(constant)::value;
+            if ((e = allow_smem<kernel>(balance_smem(E))) != cudaSuccess) return;
             if (one) e = launch_cluster(kernel, ctas, balance_smem(E), st, a, share, 1);
             else e = bq::launch_after(kernel, dim3(ctas), dim3(kThreads), balance_smem(E), st, a, share, 0);
         };
-        if (scoring == BQ_SCORE_SQRTSOFTPLUS) go(balance_kernel<N, VEC, RULE_SCORE>);
-        else go(balance_kernel<N, VEC, RULE_SOFTMAX>);
+        if (scoring == BQ_SCORE_SQRTSOFTPLUS) go(Constant<balance_kernel<N, VEC, RULE_SCORE>>());
+        else go(Constant<balance_kernel<N, VEC, RULE_SOFTMAX>>());
     });
     if ((s = launched(name, e)) != BQ_OK || one) return s;
     return launched(name, bq::launch_after(balance_finish_kernel, dim3((unsigned)(S * ((E + 31) / 32))), dim3(kThreads), 0,
@@ -998,7 +1015,7 @@ extern "C" bq_status bq_moe_balance_loss(const float* logits, const float* bias,
 }
 
 extern "C" size_t bq_moe_route_backward_workspace_bytes(int32_t T, int32_t E) {
-    if (T < 0 || T > kMaxRows || E < 1 || E > 1024) return 0;
+    if (T < 0 || T > kMaxRows || E < 1 || E > kMaxExperts) return 0;
     return up256((size_t)std::max(1, gradient_chunking(T, true).chunks) * E * 4);
 }
 
@@ -1042,8 +1059,9 @@ extern "C" bq_status bq_moe_route_backward(const float* logits, const float* bia
         const size_t smem = dbias ? (size_t)kWarps * E * 4 : 0;
         const bool score = scoring == BQ_SCORE_SQRTSOFTPLUS;
         cudaError_t e = cudaSuccess;
-        auto go = [&](auto kernel, auto... more) {
-            if ((e = allow_smem(kernel, smem)) != cudaSuccess) return;
+        auto go = [&](auto constant, auto... more) {
+            constexpr auto kernel = decltype(constant)::value;
+            if ((e = allow_smem<kernel>(smem)) != cudaSuccess) return;
             if (one) e = launch_cluster(kernel, c.chunks, smem, st, a, more...);
             else e = bq::launch_after(kernel, dim3(c.chunks), dim3(kThreads), smem, st, a, more...);
         };
@@ -1052,11 +1070,12 @@ extern "C" bq_status bq_moe_route_backward(const float* logits, const float* bia
             with_share(E, vec, [&](auto nper, auto v) {
                 constexpr int N = decltype(nper)::value;
                 constexpr bool VEC = decltype(v)::value;
-                score ? go(route_backward_kernel<N, VEC, RULE_SCORE>) : go(route_backward_kernel<N, VEC, RULE_SOFTMAX>);
+                score ? go(Constant<route_backward_kernel<N, VEC, RULE_SCORE>>()) : go(Constant<route_backward_kernel<N, VEC, RULE_SOFTMAX>>());
             });
         } else {
             const int wide = E * es % 16 == 0 && bq::aligned(dlogits, 16);
-            score ? go(route_weights_backward_kernel<RULE_SCORE>, wide) : go(route_weights_backward_kernel<RULE_SOFTMAX>, wide);
+            score ? go(Constant<route_weights_backward_kernel<RULE_SCORE>>(), wide)
+                  : go(Constant<route_weights_backward_kernel<RULE_SOFTMAX>>(), wide);
         }
         if ((s = launched(name, e)) != BQ_OK) return s;
     }
