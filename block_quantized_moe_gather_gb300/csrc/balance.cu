@@ -202,11 +202,26 @@ __device__ __forceinline__ float row_dot(const float (&x)[NPER], const float (&y
     return warp_sum(sum2(dot));
 }
 
-// Scores (and slopes) of a row, and 1 / their sum (0 where every score is 0).
+// Where a row's largest logit m lies below this, e = exp(z) is less than 2^-28, and a score is exp(z / 2) to fp32's
+// precision.  exp(m / 2) cancels in score / sum and in slope / sum, and is left out of both: far below 0 (z < -174) the
+// scores themselves are below fp32's normal range.
+constexpr float kFarBelow = -20.f;
+
+__device__ __forceinline__ float far_score(float z, float m) { return exp2_approx((z - m) * (0.5f * kLog2E)); }
+
+// Scores (and slopes) of a row, and 1 / their sum (0 where every score is 0); both without the factor exp(m / 2) where the
+// largest logit m (0 for a row of -inf only) is below kFarBelow.
 template <bool SLOPE, int NPER>
-__device__ __forceinline__ float score_row(const float (&z)[NPER], float (&s)[NPER], float (&d)[NPER]) {
+__device__ __forceinline__ float score_row(const float (&z)[NPER], float m, float (&s)[NPER], float (&d)[NPER]) {
     float sum = 0.f;
-    if (NPER == 1) {
+    if (m < kFarBelow) {
+#pragma unroll
+        for (int i = 0; i < NPER; ++i) {
+            s[i] = far_score(z[i], m);
+            if (SLOPE) d[i] = 0.5f * s[i];
+            sum += s[i];
+        }
+    } else if (NPER == 1) {
         float unused0, unused1;
         scores_of<SLOPE>(z[0], 0.f, s[0], unused0, d[0], unused1);
         sum = s[0];
@@ -320,7 +335,7 @@ __device__ __forceinline__ void chunk_sums(const BalanceArgs& a, float* s_red, i
             else if (r + kWarps < hi) Row::load(a.logits + (int64_t)(r + kWarps) * a.E, a.bias, a.E, lane, next);
             const Softmax soft = softmax_row(z, p);
             float inv = soft.inv;
-            if (RULE == RULE_SCORE) inv = score_row<false>(z, p, unused);
+            if (RULE == RULE_SCORE) inv = score_row<false>(z, soft.m, p, unused);
 #pragma unroll
             for (int i = 0; i < NPER; ++i) {
                 acc[i] = __fmaf_rn(p[i], inv, acc[i]);
@@ -742,12 +757,13 @@ route_backward_kernel(const __grid_constant__ RouteGradArgs a) {
                 if (mine) base = exp2_approx((pair.z - soft.m) * kLog2E) * __fmaf_rn(own, soft.inv, rest);
             } else {
                 float sc[NPER], slope[NPER];
-                const float inv = score_row<true>(z, sc, slope), dot = row_dot(sc, weight) * inv;
+                const float inv = score_row<true>(z, soft.m, sc, slope), dot = row_dot(sc, weight) * inv;
 #pragma unroll
                 for (int i = 0; i < NPER; ++i) d[i] = __fmaf_rn(d[i], f, slope[i] * inv * (weight[i] - dot));
                 if (mine) {
                     float score, change, unused0, unused1;
-                    scores_of<true>(pair.z, 0.f, score, unused0, change, unused1);
+                    if (soft.m < kFarBelow) change = 0.5f * far_score(pair.z, soft.m);
+                    else scores_of<true>(pair.z, 0.f, score, unused0, change, unused1);
                     base = __fmaf_rn(exp2_approx((pair.z - soft.m) * kLog2E), f, change * inv * (own - dot));
                 }
             }

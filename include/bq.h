@@ -653,7 +653,8 @@ bq_status bq_residual_norm_backward(const bq_residual_norm_desc* desc, const voi
  *                  sum_e E * counts[s][e] / (k * n_s) * probs[s][e]
  *   losses[1]    = mean over all rows of sequences of logsumexp(z[t])^2
  * A row of -inf only has probabilities 0 and adds 0 to losses[1]; NaN and +inf
- * propagate.  An id outside [0, E) sets BQ_DEV_BAD_EXPERT_ID and counts nowhere.
+ * propagate.  Probabilities of other rows add up to 1 however far below 0 their
+ * logits are; those below 2^-110 may become 0.  An id outside [0, E) sets BQ_DEV_BAD_EXPERT_ID and counts nowhere.
  * Offsets that descend or leave [0, T] set BQ_DEV_BAD_ROW; what such a call
  * returns is undefined.  Sums are fp32 in a fixed order.
  *

@@ -111,12 +111,21 @@ def router_scores(z):
     return s, slope
 
 
-def router_probabilities(z, scoring):
-    if scoring != "sqrtsoftplus":
-        return router_softmax(z)[0]
-    s, _ = router_scores(z)
+def router_shares(z):
+    """``s / sum s`` and ``ds/dz / sum s`` of each row.  A row far below 0, where s is exp(z/2): without the factor
+    exp(max z / 2), which cancels (and is 0 in fp64 below -1490)."""
+    top = z.max(axis=1, keepdims=True)
+    far = (top < -80) & (top > -np.inf)
+    shifted = np.exp(0.5 * np.where(far, z - np.where(far, top, 0.0), 0.0))
+    s, slope = router_scores(np.where(far, 0.0, z))
+    s, slope = np.where(far, shifted, s), np.where(far, 0.5 * shifted, slope)
     whole = s.sum(axis=1, keepdims=True)
-    return s / np.where(whole == 0, 1.0, whole)
+    whole = np.where(whole == 0, 1.0, whole)
+    return s / whole, slope / whole
+
+
+def router_probabilities(z, scoring):
+    return router_softmax(z)[0] if scoring != "sqrtsoftplus" else router_shares(z)[0]
 
 
 def balance_loss(logits, ids, scoring="softmax", bias=None, offsets=None):
@@ -160,7 +169,7 @@ def route_backward(logits, ids, dweights, scoring="softmax", bias=None, scale=1.
     k = ids.shape[1]
     d = np.zeros((t, e))
     soft, lse = router_softmax(z)
-    score, slope = router_scores(z) if scoring == "sqrtsoftplus" else (None, None)
+    slope, share = (router_scores(z)[1], router_shares(z)[1]) if scoring == "sqrtsoftplus" else (None, None)
     if dweights is not None:
         for r in range(t):
             on = [j for j in range(k) if 0 <= ids[r, j] < e]
@@ -185,8 +194,7 @@ def route_backward(logits, ids, dweights, scoring="softmax", bias=None, scale=1.
             weight = float(dlosses[0]) * e * _f64(counts)[s] / (k * (b - a)) / (b - a) / used
             inner = weight[None, :] - (p[a:b] * weight).sum(axis=1, keepdims=True)
             if scoring == "sqrtsoftplus":
-                whole = score[a:b].sum(axis=1, keepdims=True)
-                d[a:b] += slope[a:b] / np.where(whole == 0, 1.0, whole) * inner
+                d[a:b] += share[a:b] * inner
             else:
                 d[a:b] += p[a:b] * inner
             d[a:b] += 2 * float(dlosses[1]) / rows * lse[a:b] * soft[a:b]
