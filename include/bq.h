@@ -540,6 +540,11 @@ bq_status bq_moe_mm_fp8_b128(const uint8_t* x, const float* xscales, int32_t row
  * itself (then with ldr = ldy) but not overlap it otherwise.  All of it in fp32
  * before the one rounding to `ydtype`.  epi: host struct, read during the call.
  * NaN of the product, bias or residual propagates through every activation.
+ * Exponentials and reciprocals are the special-function unit's: of its exact
+ * value, silu (also in SwiGLU; without an end that takes expf, so that the two may
+ * differ in their last places) is off by (16 + 2.2 |v|) 2^-24, gelu by
+ * (24 + 1.1 v^2) 2^-24, gelu_tanh by (16 + 8 |w|) 2^-24, w = 1.6 (v + 0.045 v^3);
+ * results below 2^-119 may become 0.
  * Errors: as above, plus BQ_ERR_SHAPE (unknown activation, ldr below the columns).
  */
 typedef enum {
