@@ -40,7 +40,7 @@ bool gate_up_map(CUtensorMap* map, const uint8_t* w, int E, int n, int k, int bo
 }
 
 template <bool SWIGLU, bool EPI>
-cudaError_t launch_lanes(const CUtensorMap& map_w, const CUtensorMap& map_x, const Args& a, int64_t items, int split,
+cudaError_t launch_lanes(const CUtensorMap& map_w, const CUtensorMap& map_x, const EndArgs& a, int64_t items, int split,
                          cudaStream_t st) {
     // per device: the attribute is a property of the function on the current device
     static std::atomic<bool> attr_set[64];
@@ -65,7 +65,7 @@ cudaError_t launch_lanes(const CUtensorMap& map_w, const CUtensorMap& map_x, con
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, mm_lanes_kernel<SWIGLU, EPI>, map_w, map_x, a, split);
+    return cudaLaunchKernelEx(&cfg, mm_lanes_kernel<SWIGLU, EPI>, map_w, map_x, static_cast<const ArgsOf<EPI>&>(a), split);
 }
 
 bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32_t rows, const int32_t* offsets,
@@ -119,10 +119,10 @@ bq_status run_mm(const char* name, const uint8_t* x, const float* xscales, int32
     bq_status s = bq::check_arch();
     if (s != BQ_OK) return s;
     const bq::WaitProbe probe = bq::wait_probe();
-    const Args a{xscales, rows, offsets, E, wscales, n, k, kb, (n + kBlock - 1) / kBlock, cols,
-                 y, ydtype, ldy, bq::device_status_ptr(), probe.limit_ns, probe.skip_weight_copies, (int)chunks,
-                 epi ? epi->bias : nullptr, epi && !swiglu ? epi->act : BQ_ACT_NONE, epi ? epi->scale : 1.f,
-                 epi ? epi->residual : nullptr, epi ? epi->ldr : 0};
+    const Args product{xscales, rows, offsets, E, wscales, n, k, kb, (n + kBlock - 1) / kBlock, cols,
+                       y, ydtype, ldy, bq::device_status_ptr(), probe.limit_ns, probe.skip_weight_copies, (int)chunks};
+    const EndArgs a{product, epi ? epi->bias : nullptr, epi && !swiglu ? epi->act : BQ_ACT_NONE, epi ? epi->scale : 1.f,
+                    epi ? epi->residual : nullptr, epi ? epi->ldr : 0};
     // an end that changes nothing is none
     const bool end = epi && (epi->bias || a.act != BQ_ACT_NONE || epi->scale != 1.f || epi->residual);
     CUtensorMap map_w, map_x;

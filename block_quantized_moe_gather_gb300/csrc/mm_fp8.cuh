@@ -45,13 +45,20 @@ struct Args {
     unsigned long long wait_limit_ns;
     int skip_copies;          // test only: the producer issues no copies (waits run out); 3: only in a part of a cluster
     int max_chunks;           // row chunks that offsets in order can make
-    // kernels with an end of their own only: y = scale * act(product + bias) + residual
+};
+
+// Of kernels with an end: y = scale * act(product + bias) + residual.  Those without take Args alone: with these fields
+// behind it, unused, the wide kernel with SwiGLU spilled 24 bytes of its sums a thread instead of 4.
+struct EndArgs : Args {
     const float* bias;        // [E][n], or NULL
     int act;                  // bq_activation
     float scale;
     const void* residual;     // rows like y's, or NULL
     int64_t ldr;
 };
+
+template <bool END>
+using ArgsOf = std::conditional_t<END, EndArgs, Args>;
 
 // ---------------------------------------------------------------- PTX used here only
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -267,7 +274,7 @@ __device__ __forceinline__ float load_value(const void* p, int64_t i, int dtype)
 // type is outside the loop, so that the loads are in flight together (inside it they came one after the other, 1.5 us
 // for 8 rows).
 template <int N>
-__device__ __forceinline__ void load_residual(const Args& a, int64_t row0, int step, int64_t end, int c, float (&r)[N]) {
+__device__ __forceinline__ void load_residual(const EndArgs& a, int64_t row0, int step, int64_t end, int c, float (&r)[N]) {
     uint32_t raw[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) raw[i] = 0;
@@ -293,7 +300,7 @@ __device__ __forceinline__ void load_residual(const Args& a, int64_t row0, int s
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // Lines of a row of the residual, columns [c, c + cols) (bounded), on their way into the L2.
-__device__ __forceinline__ void prefetch_residual(const Args& a, int64_t row, int c, int cols) {
+__device__ __forceinline__ void prefetch_residual(const EndArgs& a, int64_t row, int c, int cols) {
     const int es = a.ydtype == BQ_DT_F32 ? 4 : 2, end = min(c + cols, a.cols);
     const uint8_t* p = static_cast<const uint8_t*>(a.residual) + (row * a.ldr + c) * es;
     for (int i = 0; i < (end - c) * es; i += 128) prefetch_l2(p + i);
@@ -459,7 +466,7 @@ static_assert(LaneSmem::kBytes <= 232448 && LaneSmem::kTiles % 16 == 0, "smem");
 
 // Bias of the weight row that a lane holds: column c of y, with SwiGLU its gate value (lanes 0-15) or its up value.
 template <bool SWIGLU>
-__device__ __forceinline__ float lane_bias(const Args& a, int e, int c) {
+__device__ __forceinline__ float lane_bias(const EndArgs& a, int e, int c) {
     if (!a.bias || c >= a.cols) return 0.f;
     const int up = SWIGLU && (threadIdx.x & 16) ? a.cols : 0;
     return load_early(a.bias + (int64_t)e * a.n + up + c);
@@ -468,7 +475,7 @@ __device__ __forceinline__ float lane_bias(const Args& a, int e, int c) {
 // EPI: with an end (bias, activation, scale, residual).
 template <bool SWIGLU, bool EPI>
 __global__ void __launch_bounds__(kLaneThreads, 1)
-mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a,
+mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const ArgsOf<EPI> a,
                 int split) {
     using M = LaneSmem;
     constexpr int S = M::S, A = M::A, NT = kLaneRows;
@@ -521,6 +528,10 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
     const unsigned long long limit = a.wait_limit_ns;
 
     float bias = 0.f;   // of the column that an epilogue thread has (an end's)
+    auto ended = [&](float v, float residual) {
+        if constexpr (EPI) v = __fmaf_rn(a.scale, v, residual);
+        return v;
+    };
     const bool one = elect_one();
     bool ok = !(a.skip_copies == 3 && split > 1 ? rank & 1 : a.skip_copies);
     if (warp == 0) {
@@ -604,7 +615,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
         for (Items i(first, step, items, w_tiles); ok && i.more(); i.next()) {
             const Item it = i.get(chunks, a.E);
             const int c = SWIGLU ? 64 * it.tile + 16 * quarter + (lane & 15) : 128 * it.tile + p;
-            if (EPI) {   // on their way while the weights are
+            if constexpr (EPI) {   // on their way while the weights are
                 bias = lane_bias<SWIGLU>(a, it.e, c);
                 const int c0 = SWIGLU ? c - (lane & 15) : c - lane;
                 if (a.residual && lane < it.rows && c0 < a.cols)
@@ -643,7 +654,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                 break;         // one item per cluster
             }
             float res[NT];
-            if (EPI) {
+            if constexpr (EPI) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) acc[t] += bias;
                 // of the values that this thread stores: with SwiGLU those of every other row
@@ -665,7 +676,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                         const float recv = __shfl_xor_sync(0xffffffffu, lane < 16 ? acc[t + 1] : acc[t], 16);
                         const float g = lane < 16 ? acc[t] : recv, u = lane < 16 ? recv : acc[t + 1];
                         const int r = t + (lane >> 4);
-                        const float v = EPI ? __fmaf_rn(a.scale, silu_end(g) * u, res[t]) : silu_f(g) * u;
+                        const float v = ended((EPI ? silu_end(g) : silu_f(g)) * u, res[t]);
                         if (r < it.rows) bq::store_value(a.y, (int64_t)(it.row0 + r) * a.ldy + c, a.ydtype, v);
                     }
                 }
@@ -673,8 +684,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
                     if (t < it.rows)
-                        bq::store_value(a.y, (int64_t)(it.row0 + t) * a.ldy + c, a.ydtype,
-                                        EPI ? __fmaf_rn(a.scale, acc[t], res[t]) : acc[t]);
+                        bq::store_value(a.y, (int64_t)(it.row0 + t) * a.ldy + c, a.ydtype, ended(acc[t], res[t]));
             }
         }
     }
@@ -693,7 +703,7 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
             for (int t0 = rank; t0 < it.rows; t0 += kAtOnce * split) {
                 float part[kAtOnce][kMaxCluster] = {};
                 float res[kAtOnce];
-                if (EPI) load_residual(a, (int64_t)it.row0 + t0, split, (int64_t)it.row0 + it.rows, c, res);
+                if constexpr (EPI) load_residual(a, (int64_t)it.row0 + t0, split, (int64_t)it.row0 + it.rows, c, res);
 #pragma unroll
                 for (int j = 0; j < kAtOnce; ++j) {
                     const uint32_t at = ring + 4 * ((t0 + j * split) * 128 + p);
@@ -717,12 +727,12 @@ mm_lanes_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant
                         v[j] = (EPI ? silu_end(v[j]) : silu_f(v[j])) * u;
                     }
                 }
-                if (EPI && !SWIGLU) activate<END_ANY>(v, a.act);
+                if constexpr (EPI && !SWIGLU) activate<END_ANY>(v, a.act);
 #pragma unroll
                 for (int j = 0; j < kAtOnce; ++j) {
                     const int t = t0 + j * split;
                     if (t >= it.rows) break;
-                    if (EPI) v[j] = __fmaf_rn(a.scale, v[j], res[j]);
+                    v[j] = ended(v[j], res[j]);
                     if (c < a.cols && (!SWIGLU || lane < 16))
                         bq::store_value(a.y, (int64_t)(it.row0 + t) * a.ldy + c, a.ydtype, v[j]);
                 }
@@ -871,7 +881,7 @@ __device__ __forceinline__ void load32(const void* p, uint4& lo, uint4& hi) {
 // vectors: the matrix allows 32-byte loads (whole sectors), which then are in flight together.  (fp32 rows by way of
 // shared memory, eight lanes 128 bytes, took longer: 49 us against 44 for 2048 x 4096 x 4096.)
 template <int N>
-__device__ __forceinline__ void add_residual(const Args& a, int64_t row, int c, bool vectors, float* v) {
+__device__ __forceinline__ void add_residual(const EndArgs& a, int64_t row, int c, bool vectors, float* v) {
     const int64_t at = row * a.ldr + c;
     if (vectors && c + N <= a.cols) {
         const uint8_t* p = static_cast<const uint8_t*>(a.residual) + at * (128 / N);
@@ -900,7 +910,7 @@ __device__ __forceinline__ void add_residual(const Args& a, int64_t row, int c, 
 // until the sums are done, and that need no registers meanwhile (a load into registers at this place made a block of K
 // 8% longer).  end_rows waits for them: one call of each per item.
 template <bool SWIGLU>
-__device__ __forceinline__ void fetch_bias(const Args& a, int e, int c0, uint8_t* buf) {
+__device__ __forceinline__ void fetch_bias(const EndArgs& a, int e, int c0, uint8_t* buf) {
     if (!a.bias) return;
     const float* bias = a.bias + (int64_t)e * a.n;
 #pragma unroll
@@ -912,7 +922,7 @@ __device__ __forceinline__ void fetch_bias(const Args& a, int e, int c0, uint8_t
 
 // A row's end, in place: column c0 + n of y in acc[n].
 template <bool SWIGLU, int END, bool RESIDUAL>
-__device__ __forceinline__ void end_rows(const Args& a, float (&acc)[128], const uint8_t* buf, int64_t row, bool live, int c0,
+__device__ __forceinline__ void end_rows(const EndArgs& a, float (&acc)[128], const uint8_t* buf, int64_t row, bool live, int c0,
                                          bool vectors) {
     constexpr int kCols = SWIGLU ? 64 : 128;
     if (a.bias) {
@@ -952,7 +962,8 @@ __device__ __forceinline__ void end_rows(const Args& a, float (&acc)[128], const
 // END, RESIDUAL: the end (bias, activation, scale, residual) that it is compiled for.
 template <bool SWIGLU, int END, bool RESIDUAL>
 __global__ void __launch_bounds__(kWideThreads, 1)
-mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Args a) {
+mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+               const ArgsOf<(END > 0)> a) {
     using M = WideSmem;
     constexpr int S = M::S, A = M::A, kTileCols = SWIGLU ? 128 : 256;
     extern __shared__ uint8_t smem_dyn[];
@@ -1071,7 +1082,8 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         const int es = a.ydtype == BQ_DT_F32 ? 4 : 2;
         const uintptr_t y_align = reinterpret_cast<uintptr_t>(a.y) | (uintptr_t)(a.ldy * es);
         const bool aligned = y_align % 16 == 0, sectors = y_align % 32 == 0;
-        const bool vectors = (reinterpret_cast<uintptr_t>(a.residual) | (uintptr_t)(a.ldr * es)) % 32 == 0;
+        bool vectors = false;
+        if constexpr (RESIDUAL) vectors = (reinterpret_cast<uintptr_t>(a.residual) | (uintptr_t)(a.ldr * es)) % 32 == 0;
         // The slot in turn: its barriers (the second's 8 bytes behind the first's) and its columns, flipped by a bit.
         uint32_t bar_full = acc_full(half, 0), t = tmem + ((uint32_t)(32 * quarter) << 16) + half * A * 128, aph = 0;
         uint32_t bar_free = acc_empty(half, 0);
@@ -1087,9 +1099,11 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             uint8_t* buf = smem + M::kOut + (warp - 4) * 16 * kOutRow;
             // On their way while the blocks are.  A warp without rows of this item has no use for a bias, and does not
             // come to the wait in end_rows: copies left in flight would meet those of its next item in the same place.
-            if (END != END_NONE && 32 * quarter < it.rows) {
-                fetch_bias<SWIGLU>(a, it.e, c0, buf);
-                if (RESIDUAL && p < it.rows) prefetch_residual(a, (int64_t)it.row0 + p, c0, SWIGLU ? 64 : 128);
+            if constexpr (END != END_NONE) {
+                if (32 * quarter < it.rows) {
+                    fetch_bias<SWIGLU>(a, it.e, c0, buf);
+                    if (RESIDUAL && p < it.rows) prefetch_residual(a, (int64_t)it.row0 + p, c0, SWIGLU ? 64 : 128);
+                }
             }
             float acc[128];
 #pragma unroll
@@ -1140,7 +1154,7 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             const int rows = it.rows - 32 * quarter;   // of this warp
             if (rows > 0) {
                 const int64_t row0 = it.row0 + 32 * quarter;
-                if (END != END_NONE) end_rows<SWIGLU, END, RESIDUAL>(a, acc, buf, row0 + lane, lane < rows, c0, vectors);
+                if constexpr (END != END_NONE) end_rows<SWIGLU, END, RESIDUAL>(a, acc, buf, row0 + lane, lane < rows, c0, vectors);
                 auto out = [&](int n) { return SWIGLU && END == END_NONE ? silu_f(acc[n]) * acc[(64 + n) & 127] : acc[n]; };
                 auto out8 = [&](int n) {
                     const float f[8] = {out(n), out(n + 1), out(n + 2), out(n + 3), out(n + 4), out(n + 5), out(n + 6), out(n + 7)};
@@ -1204,7 +1218,7 @@ mm_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
 constexpr int kSms = 152;
 
 template <bool SWIGLU, int END, bool RESIDUAL>
-cudaError_t launch_wide(const CUtensorMap& map_w, const CUtensorMap& map_x, const Args& a, int64_t items,
+cudaError_t launch_wide(const CUtensorMap& map_w, const CUtensorMap& map_x, const EndArgs& a, int64_t items,
                         cudaStream_t st) {
     static std::atomic<bool> attr_set[64];
     int dev = 0;
@@ -1216,14 +1230,14 @@ cudaError_t launch_wide(const CUtensorMap& map_w, const CUtensorMap& map_x, cons
         attr_set[dev].store(true, std::memory_order_release);
     }
     return bq::launch_after(mm_wide_kernel<SWIGLU, END, RESIDUAL>, dim3((unsigned)std::min<int64_t>(items, kSms)), dim3(kWideThreads),
-                            WideSmem::kBytes, st, map_w, map_x, a);
+                            WideSmem::kBytes, st, map_w, map_x, static_cast<const ArgsOf<(END > 0)>&>(a));
 }
 
 // Of products with an end, each in a file of its own (a kernel of 128 sums a thread takes 10 s to compile): no activation
 // or one of no cost, and SwiGLU; and the others.
-cudaError_t launch_wide_simple_end(const CUtensorMap& map_w, const CUtensorMap& map_x, const Args& a, int64_t items,
+cudaError_t launch_wide_simple_end(const CUtensorMap& map_w, const CUtensorMap& map_x, const EndArgs& a, int64_t items,
                                    bool swiglu, cudaStream_t st);
-cudaError_t launch_wide_activation_end(const CUtensorMap& map_w, const CUtensorMap& map_x, const Args& a, int64_t items,
+cudaError_t launch_wide_activation_end(const CUtensorMap& map_w, const CUtensorMap& map_x, const EndArgs& a, int64_t items,
                                        cudaStream_t st);
 
 }  // namespace fp8mm

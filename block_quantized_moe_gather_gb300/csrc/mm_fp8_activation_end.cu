@@ -6,7 +6,7 @@
 namespace bq {
 namespace fp8mm {
 
-cudaError_t launch_wide_activation_end(const CUtensorMap& map_w, const CUtensorMap& map_x, const Args& a, int64_t items,
+cudaError_t launch_wide_activation_end(const CUtensorMap& map_w, const CUtensorMap& map_x, const EndArgs& a, int64_t items,
                                        cudaStream_t st) {
     if (a.residual) return launch_wide<false, END_ANY, true>(map_w, map_x, a, items, st);
     switch (a.act) {

@@ -5,7 +5,7 @@
 namespace bq {
 namespace fp8mm {
 
-cudaError_t launch_wide_simple_end(const CUtensorMap& map_w, const CUtensorMap& map_x, const Args& a, int64_t items,
+cudaError_t launch_wide_simple_end(const CUtensorMap& map_w, const CUtensorMap& map_x, const EndArgs& a, int64_t items,
                                    bool swiglu, cudaStream_t st) {
     if (swiglu)
         return a.residual ? launch_wide<true, END_SIMPLE, true>(map_w, map_x, a, items, st)
