@@ -347,19 +347,18 @@ Shape shape_of(int T, int H, int n_planes, int n_constants) {
     const int vecs = H / 8;
     auto bytes = [&](int stages) { return (size_t)(n_constants + stages * n_planes) * p.block * p.vpt * 16; };
     auto fit = [&](int ctas) { return (bytes(2) + 2048) * ctas <= kSmemOfSm; };   // two rows of each
-    // a block of 512 threads holds up to 1024 vectors of a row; wider rows, and rows of which one does not fit into
-    // shared memory, are shared by a cluster
-    for (p.cluster = 1;; p.cluster *= 2) {
-        p.slice = (vecs + p.cluster - 1) / p.cluster;
-        p.block = p.slice > 512 ? 512 : 256;
-        p.vpt = 2;
-        // Two vectors a thread share what a row costs a warp beside them (16384 x 2048 bf16 71 us, one a thread 88; 2400 x
-        // 512 10.6 and 10.5).  One where that brings a second CTA to the SM (2048 x 1536 fp32 25.2 us against 27.6), where
-        // rows are a warp each way (2400 x 256 7.8 against 8.8), and where a block an SM takes all rows (16 x 2048 5.2
-        // against 6.5, 300 x 1024 6.0 against 7.4; 600 x 1024 8.1 and 7.5).
-        if (p.cluster == 1 && p.slice <= 256 && (!fit(2) || p.slice <= 32 || (int64_t)T * p.slice <= kSms * 256)) p.vpt = 1;
-        if (p.slice <= 1024 && bytes(1) <= kSmemOfSm) break;
-    }
+    // a block of 512 threads holds up to 1024 vectors of a row (14 planes of 16 KB at most: four of constants, ten of a
+    // row); wider rows are shared by a cluster of two
+    static_assert(kMaxH / 8 <= 2 * 1024 && 14 * 1024 * 16 <= kSmemOfSm, "");
+    p.cluster = vecs > 1024 ? 2 : 1;
+    p.slice = (vecs + p.cluster - 1) / p.cluster;
+    p.block = p.slice > 512 ? 512 : 256;
+    p.vpt = 2;
+    // Two vectors a thread share what a row costs a warp beside them (16384 x 2048 bf16 71 us, one a thread 88; 2400 x
+    // 512 10.6 and 10.5).  One where that brings a second CTA to the SM (2048 x 1536 fp32 25.2 us against 27.6), where
+    // rows are a warp each way (2400 x 256 7.8 against 8.8), and where a block an SM takes all rows (16 x 2048 5.2
+    // against 6.5, 300 x 1024 6.0 against 7.4; 600 x 1024 8.1 and 7.5).
+    if (p.slice <= 256 && (!fit(2) || p.slice <= 32 || (int64_t)T * p.slice <= kSms * 256)) p.vpt = 1;
     p.threads = ((p.slice + p.vpt - 1) / p.vpt + 31) / 32 * 32;
     p.rows = p.cluster > 1 ? 1 : std::max(1, p.block / p.threads);
     const int per_sm = p.block == 256 && fit(2) ? 2 : 1;   // what the registers allow
@@ -367,8 +366,8 @@ Shape shape_of(int T, int H, int n_planes, int n_constants) {
     p.stage_bytes = n_planes * p.block * p.vpt * 16;
     p.at_stages = n_constants * p.block * p.vpt * 16;
     p.smem = bytes(p.stages);   // room for the block's two column sums too, 64 bytes per vector: six planes at least
-    // clusters of 1, 2, 4 and 8 CTAs that this GPU holds at once, with one CTA an SM
-    const int held = p.cluster == 1 ? kSms : p.cluster == 2 ? 76 : p.cluster == 4 ? 36 : 15;
+    // clusters of one and of two CTAs that this GPU holds at once, with one CTA an SM
+    const int held = kSms / p.cluster;
     p.blocks = (int)std::min<int64_t>(held * per_sm, ((int64_t)T + p.rows - 1) / p.rows);
     return p;
 }
