@@ -87,11 +87,18 @@ __device__ __forceinline__ void store8(uint8_t* row, int i, int dtype, const Vec
     }
 }
 
-__device__ __forceinline__ float load1(const uint8_t* p, int64_t i, int dtype) {
-    if (dtype == BQ_DT_F32) return reinterpret_cast<const float*>(p)[i];
-    if (dtype == BQ_DT_F16) return __half2float(reinterpret_cast<const __half*>(p)[i]);
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
+// One value, as its bits; and its value.
+__device__ __forceinline__ uint32_t load_raw(const uint8_t* p, int64_t i, int dtype) {
+    return dtype == BQ_DT_F32 ? reinterpret_cast<const uint32_t*>(p)[i] : reinterpret_cast<const uint16_t*>(p)[i];
 }
+
+__device__ __forceinline__ float raw_value(uint32_t raw, int dtype) {
+    return dtype == BQ_DT_F32   ? __uint_as_float(raw)
+           : dtype == BQ_DT_F16 ? __half2float(__ushort_as_half((unsigned short)raw))
+                                : __uint_as_float(raw << 16);
+}
+
+__device__ __forceinline__ float load1(const uint8_t* p, int64_t i, int dtype) { return raw_value(load_raw(p, i, dtype), dtype); }
 
 // By the special-function unit's exp2 and reciprocal, off by 2 units in the last place each; the exponent's argument
 // adds |v| units to the exponential.

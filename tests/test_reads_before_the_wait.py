@@ -8,7 +8,7 @@ import re
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "block_quantized_moe_gather_gb300", "csrc")
-READS = re.compile(r"__ldg\(|__ldcg\(|\bload1\(|\bload8<|\bload_early\(|\bload_value\(|\bsequence\(|\bsequence_totals\(|"
+READS = re.compile(r"__ldg\(|__ldcg\(|\bload1\(|\bload_raw\(|\bload8<|\bload_early\(|\bload_value\(|\bsequence\(|\bsequence_totals\(|"
                    r"\badd_slots\(|\btoken_factor\(|\bkeep_columns<|\bcount_chunks\(")
 
 
