@@ -14,11 +14,14 @@
 //
 // A warp takes a row, its logits in registers, the next row's on their way.  The logits are read once (and the
 // gradient written once), but issue bounds both passes before memory does (GB300, 16384 x 256, k = 8): the statistics
-// of scores over 9 sequences take 12.7 us, 2.5 at the copy bandwidth, of which the first kernel has 8 (three
+// of scores over 9 sequences take 13.4 us, 2.5 at the copy bandwidth, of which the first kernel has 8 (three
 // special-function instructions a logit, packed arithmetic, 55% of the issue slots at 30 warps an SM; 3.4 rows a warp
-// leave a fifth of the last round idle) and the second, a chain of latencies, 4; the gradient of weights and losses
-// under the softmax rule takes 10.3 us, 5.1 at the copy bandwidth.  Few rows are latency (129 x 128: statistics 6.2 us,
-// gradient of weights alone 4.1).
+// leave a fifth of the last round idle) and the second, a chain of latencies, 5; those of a softmax rule take 10.9.  The
+// gradient of weights and losses takes 10.3 us under a softmax rule and 17.8 under the score rule, 5.1 at the copy
+// bandwidth, that of the weights alone 7.7.  From 513 experts on a lane holds 32 of them, and the gradient under the score
+// rule does not fit its 128 registers (about 500 bytes a thread are spilled): 16384 x 1024 50 us, under a softmax rule 32,
+// 19.9 at the copy bandwidth; statistics 29 and 23, at the copy bandwidth 9.9.  Few rows are latency (129 x 128: statistics
+// 6.2 us, gradient of weights alone 4.1).
 #include <algorithm>
 #include <atomic>
 
@@ -875,7 +878,9 @@ Chunking chunking(int T, int most, int least) {
 
 // As many rows go to one cluster, which adds its chunks' sums up itself: what a second launch costs the host (1.2 us) is
 // saved, and on the GPU both take the same (200 x 256: statistics 6.1 us, gradient with that of the bias 5.8 and 5.6 in
-// two launches; 400 x 128 6.5 and 6.0, 6.4 and 4.8).
+// two launches; 400 x 128 6.5 and 6.0, 6.4 and 4.8).  With more than a few sequences the one cluster takes longer than a
+// block per group would (17 and 64 sequences: 200 x 256 11.2 and 20.1 us, in two launches 9.5 and 16.3; 200 x 1024 18.6
+// and 40.8, 15.5 and 30.3; 16 x 1024, one block, 47.6 and 114, 27.1 and 50.3).
 constexpr int kOneClusterRows = 256;
 
 Chunking balance_chunking(int T) { return T <= kOneClusterRows ? chunking(T, 8, kWarps) : chunking(T, 2 * kSms, kWarps); }

@@ -176,8 +176,8 @@ __device__ __forceinline__ float load_early(const float* p) {
 // The activations of the products' ends.  Two special-function instructions each (exp2, reciprocal) bound them, 2.1 us
 // for a tile of 128 x 256; what else they take is kept to less than that.  Both are off by 2 units in the last place at
 // most; results below the normal range become 0.  No MMA runs meanwhile, as the warps that end a tile are those that
-// scale the blocks of the next.  2048 x 4096 x 4096, bf16 out (two tiles a CTA): 30.5 us without an end, bias 31.3, relu
-// and bias 32.5, silu 35.9, gelu 37.1; bias and residual, whose rows cost 2.3 us a tile, 34.8.
+// scale the blocks of the next.  2048 x 4096 x 4096, bf16 out (two tiles a CTA): 30.9 us without an end, bias 32.1, relu
+// and bias 32.9, silu 36.1, gelu 37.0; bias and residual, whose rows cost 2.3 us a tile, 36.3.
 __device__ __forceinline__ float exp2_approx(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));

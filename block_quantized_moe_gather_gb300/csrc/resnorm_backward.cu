@@ -11,11 +11,15 @@
 // pass and one barrier, and a second pass writes all outputs.
 //
 // Four rows are read and two written (GB300, bf16, post norm, gate per channel:
-// 8192 x 4096 71 us, 5.7 TB/s; 2048 x 4096 27 us, 3.7 TB/s; fp32 stream and a gate
-// per value 2047 x 2048 24 us).  What bounds it there is issue and latency: the
-// sums and both rows' worth of packed arithmetic take 114 to 120 registers, so an
-// SM holds 16 warps, which issue in half of the cycles; the column sums' second
-// kernel takes 3 to 5 us.  Steps that led here, 2048 x 4096: rows fetched ahead
+// 8192 x 4096 72 us, 5.6 TB/s; 2048 x 4096 27 us, 3.7 TB/s).  From 2048 to 8192
+// rows a row costs 7.4 ns, at the copy bandwidth 7.2: memory bounds the walk, with
+// the 16 warps an SM that 114 to 120 registers leave issuing in half of the cycles.
+// 12 us are fixed: 6 are the column sums (without them 21.8 us: 304 parts of two
+// sums, 10 MB, are written and read again by a second kernel), the others the
+// launch, the first rows on their way and the last ones (2048 rows are 6.7 rounds
+// of 304 blocks).  With an fp32 stream and a gate per value (2047 x 2048 24 us) a
+// row costs 8.8 ns, at the copy bandwidth 6.6; why was not found.
+// Steps that led here, 2048 x 4096: rows fetched ahead
 // 85 -> 48 us, packed arithmetic and constants kept as fp32 37, two blocks an SM
 // 31, all sums of a row in one barrier 28.
 #include "resnorm.cuh"

@@ -584,7 +584,8 @@ bq_status bq_moe_mm_fp8_b128_epilogue(const uint8_t* x, const float* xscales, in
  *   h_out = residual_scale * h + scale * g * b
  *   x     = gain * n(h_out)                      (not computed where x is NULL)
  * Everything is computed in fp32 and rounded once to the output's type; x comes
- * from h_out before that rounding.
+ * from h_out before that rounding.  A gate's sigmoid is off by (16 + 2.2 |v|) 2^-24
+ * of its value, and 0 where that is below 2^-126.
  *
  * bq_residual_norm_backward: with dh_out and dx the gradients of h_out and x
  * (either may be NULL: none; then what only it needs, gain, may be NULL too),
@@ -659,7 +660,9 @@ bq_status bq_residual_norm_backward(const bq_residual_norm_desc* desc, const voi
  *   losses[1]    = mean over all rows of sequences of logsumexp(z[t])^2
  * A row of -inf only has probabilities 0 and adds 0 to losses[1]; NaN and +inf
  * propagate.  Probabilities of other rows add up to 1 however far below 0 their
- * logits are; those below 2^-110 may become 0.  An id outside [0, E) sets BQ_DEV_BAD_EXPERT_ID and counts nowhere.
+ * logits are; those below 2^-110 may become 0.  Exponentials and logarithms are the
+ * special-function unit's: a probability is off by (2 max |z| + 160) 2^-24 of itself
+ * at most.  An id outside [0, E) sets BQ_DEV_BAD_EXPERT_ID and counts nowhere.
  * Offsets that descend or leave [0, T] set BQ_DEV_BAD_ROW; what such a call
  * returns is undefined.  Sums are fp32 in a fixed order.
  *

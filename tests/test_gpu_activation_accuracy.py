@@ -80,3 +80,18 @@ def test_infinities_and_nan(lib, m):
         assert not got[1] > 0
         if act in ("gelu", "relu", "relu2"):
             assert got[1] == 0
+
+
+@pytest.mark.parametrize("dtype,rows", [("f32", 1), ("bf16", 3), ("f32", 700)])
+def test_relative_error_of_the_gates_sigmoid(lib, dtype, rows):
+    """A stream of zeros and a block's output of ones: h_out is the gate's sigmoid."""
+    import torch
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    v = torch.from_numpy(np.concatenate([np.linspace(-100, 100, 4000), np.linspace(-2, 2, 4096)]).astype(np.float32)).cuda()
+    gate = v.expand(rows, -1).to(dt).contiguous()
+    out = torch.empty(rows, v.numel(), device="cuda")
+    lib.residual_norm(torch.ones_like(out), torch.zeros_like(out), out, gate=gate, gate_sigmoid=True)
+    lib.device_status()
+    v = gate[0].double().cpu().numpy()
+    want, got = O.sigmoid(v), out.double().cpu().numpy()
+    assert (np.abs(got - want) <= (16 + 2.2 * np.abs(v)) * U * want + 2.0 ** -126).all()
